@@ -23,6 +23,8 @@ __all__ = [
     "device_error", "router_gemv_supported", "scratch_bytes", "sort_capacity", "router_gemv", "route_topk",
     "moe_sort", "mxfp8_quant", "moe_route_sort_quant", "router_gemv_noalloc", "shared_gate_up", "moe_route",
     "PreparedRoute", "moe_sort_quant", "mxfp4_quant", "norm_apply", "moe_route_sort_quant_norm",
+    "MxWeight", "ExpertScratch", "mx_gemm", "moe_gate_up", "moe_down", "PreparedMxGemm", "PreparedGateUp",
+    "PreparedDown",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -87,6 +89,12 @@ SIGNATURES = {
     "mr_device_error": (_I, [_I]),
     "mr_shared_gate_up": (_I, [_P, _I64, _P, _P, _I, _I, _I, _P, _P]),
     "mr_last_cuda_error": (_I, []),
+    "mr_mx_packed_scale_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "mr_mx_pack_scales": (_I, [_P, _I, _I, _I, _I, _I, _P, _P]),
+    "mr_expert_scratch_bytes": (_SZ, [_I, _I, _I, _I]),
+    "mr_mx_gemm": (_I, [_P, _P]),
+    "mr_moe_gate_up": (_I, [_P, _P]),
+    "mr_moe_down": (_I, [_P, _P]),
 }
 
 
@@ -652,7 +660,32 @@ def shared_gate_up(x, w13, w13_scale, out=None, stream=None):
     return out
 
 
-class PreparedRoute:
+class _Prepared:
+    """A call over fixed buffers: its parameter block is built and checked
+    once, and each call is one ABI call on the given (or torch's current)
+    stream.  The tensors are referenced for the object's life."""
+
+    def __call__(self, stream=None):
+        """Launch on the buffers' device; stream: a torch stream of that
+        device, a raw cudaStream_t (int) of that device, or None (torch's
+        current stream there)."""
+        if isinstance(stream, int):
+            sp = stream
+        else:
+            if stream is not None and stream.device != self.device:
+                raise ValueError(f"stream must be on {self.device}")
+            sp = _stream_on(self.device, stream)
+        if _torch().cuda.current_device() == self.device.index:
+            status = self._fn(self._ref, sp)
+        else:
+            with _launch_ctx(self.device):
+                status = self._fn(self._ref, sp)
+        if status != MR_OK:
+            _check(status, self._name)
+        return self.out
+
+
+class PreparedRoute(_Prepared):
     """The one-launch route over fixed buffers: the arguments are checked and
     the mr_route_params block is built once; each call is one launch of
     mr_moe_route on the given (or torch's current) stream.  The tensors are
@@ -666,27 +699,7 @@ class PreparedRoute:
                                                      norm_weight, norm, out, scratch, shared)
         self.device = x.device
         self._ref = ctypes.byref(self.p)
-        self._fn = _load().mr_moe_route
-
-    def __call__(self, stream=None):
-        """Launch on the route's device; stream: a torch stream of that
-        device, a raw cudaStream_t (int) of that device, or None (torch's
-        current stream there)."""
-        torch = _torch()
-        if isinstance(stream, int):
-            sp = stream
-        else:
-            if stream is not None and stream.device != self.device:
-                raise ValueError(f"stream must be on {self.device}")
-            sp = _stream_on(self.device, stream)
-        if torch.cuda.current_device() == self.device.index:
-            status = self._fn(self._ref, sp)
-        else:
-            with _launch_ctx(self.device):
-                status = self._fn(self._ref, sp)
-        if status != MR_OK:
-            _check(status, "mr_moe_route")
-        return self.out
+        self._fn, self._name = _load().mr_moe_route, "mr_moe_route"
 
 
 def _route_params(x, w, topk, block, scoring, bias, renormalize, quant, rstd, norm_weight, norm, out, scratch,
@@ -793,3 +806,282 @@ def moe_sort_quant(topk_ids, x, num_experts: int, block: int, quant: str = "mxfp
                                            _stream_on(dev, stream))
     _check(status, "mr_moe_sort_quant")
     return st, ex, nt, q, s
+
+
+# ---------------------------------------------------------------- expert products
+
+class MxWeight:
+    """An MX weight of mx_gemm ([R, K]) or of the experts ([E, R, K]): codes
+    uint8 (E4M3 [..., K], or E2M1 [..., K/2] as mxfp4_quant packs them) and
+    E8M0 scale bytes [..., K/32], both contiguous.  The codes are used where
+    they are; the scales are laid out once for the tensor core, here, on the
+    given (or torch's current) stream (refresh() after changing them).
+    gate_up: the weight of moe_gate_up, R = 2I with the gate rows first."""
+
+    def __init__(self, codes, scale, format: str = "mxfp8", gate_up: bool = False, stream=None):
+        torch = _torch()
+        if format not in ("mxfp8", "mxfp4"):
+            raise ValueError("format must be mxfp8 or mxfp4")
+        if codes.dim() not in (2, 3):
+            raise ValueError("codes must be [R, K] or [E, R, K]")
+        dev = _one_device(codes=codes, scale=scale)
+        self.format, self.gate_up, self.codes, self.scale, self.device = format, bool(gate_up), codes, scale, dev
+        self.E = codes.shape[0] if codes.dim() == 3 else 1
+        self.R = codes.shape[-2]
+        self.K = codes.shape[-1] * (2 if format == "mxfp4" else 1)
+        if self.K % 32:
+            raise ValueError("K must be a multiple of 32")
+        _check_out(codes, "codes", codes.shape, torch.uint8, dev)
+        _check_out(scale, "scale", (*codes.shape[:-1], self.K // 32), torch.uint8, dev)
+        n = int(_load().mr_mx_packed_scale_bytes(self.E, self.R, self.K, QUANT_FORMAT[format], int(self.gate_up)))
+        if n == 0:
+            raise MoeRouteUnsupported(MR_ERR_UNSUPPORTED, "mr_mx_packed_scale_bytes")
+        self.packed = torch.empty(n, dtype=torch.uint8, device=dev)
+        self.refresh(stream)
+
+    def refresh(self, stream=None):
+        """Lay the scales out again (after they were changed in place)."""
+        with _launch_ctx(self.device):
+            _check(_load().mr_mx_pack_scales(ctypes.c_void_p(self.scale.data_ptr()), self.E, self.R, self.K,
+                                             QUANT_FORMAT[self.format], int(self.gate_up),
+                                             ctypes.c_void_p(self.packed.data_ptr()),
+                                             _stream_on(self.device, stream)), "mr_mx_pack_scales")
+
+
+class ExpertScratch:
+    """A caller-owned scratch buffer of the expert products (zeroed once at
+    creation) for up to M_max tokens: ExpertScratch(M_max) for mx_gemm,
+    ExpertScratch(M_max, topk) for moe_gate_up, ExpertScratch(M_max, topk, R)
+    for moe_down with R output columns."""
+
+    def __init__(self, M_max: int, topk: int = 1, R: int = 0, device=None):
+        torch = _torch()
+        self.nbytes = int(_load().mr_expert_scratch_bytes(M_max, topk, R, int(R > 0)))
+        if self.nbytes == 0:
+            raise ValueError("scratch size query rejected the arguments")
+        self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=device if device is not None else "cuda")
+        self.reset()
+
+    def reset(self, stream=None):
+        """Zero the counters (the first SCRATCH_COUNTER_BYTES)."""
+        dev = self.tensor.device
+        with _launch_ctx(dev):
+            _check(_load().mr_scratch_reset(ctypes.c_void_p(self.tensor.data_ptr()), SCRATCH_COUNTER_BYTES,
+                                            _stream_on(dev, stream)), "mr_scratch_reset")
+
+    @property
+    def ptr(self):
+        return ctypes.c_void_p(self.tensor.data_ptr())
+
+
+class MxGemmParams(ctypes.Structure):
+    """mr_mx_gemm_params of moe_route.h, field for field."""
+    _fields_ = [("q", _P), ("ldq", _I64), ("scale", _P), ("lds", _I64), ("w", _P), ("w_scale", _P), ("M", _I),
+                ("R", _I), ("K", _I), ("format", _I), ("out", _P), ("ldo", _I64), ("out_fp32", _I), ("scratch", _P),
+                ("scratch_bytes", _SZ)]
+
+
+class GateUpParams(ctypes.Structure):
+    """mr_moe_gate_up_params of moe_route.h, field for field."""
+    _fields_ = [("q", _P), ("ldq", _I64), ("scale", _P), ("lds", _I64), ("sorted_rows", _I), ("w13", _P),
+                ("w13_scale", _P), ("E", _I), ("I", _I), ("K", _I), ("format", _I), ("sorted_token_ids", _P),
+                ("expert_ids", _P), ("n_blocks", _I), ("block", _I), ("M", _I), ("topk", _I), ("out_format", _I),
+                ("act", _P), ("act_scale", _P), ("scratch", _P), ("scratch_bytes", _SZ)]
+
+
+class DownParams(ctypes.Structure):
+    """mr_moe_down_params of moe_route.h, field for field."""
+    _fields_ = [("q", _P), ("ldq", _I64), ("scale", _P), ("lds", _I64), ("w2", _P), ("w2_scale", _P), ("E", _I),
+                ("R", _I), ("I", _I), ("format", _I), ("sorted_token_ids", _P), ("expert_ids", _P), ("n_blocks", _I),
+                ("block", _I), ("M", _I), ("topk", _I), ("topk_ids", _P), ("topk_weights", _P), ("add", _P),
+                ("out", _P), ("scratch", _P), ("scratch_bytes", _SZ)]
+
+
+def _mx_rows(p, q, scale, K, fmt, what="q"):
+    """Codes and scales of an MX activation, rows of K elements, into p; returns the rows."""
+    torch = _torch()
+    if q.dim() != 2 or q.shape[1] != (K // 2 if fmt == "mxfp4" else K) or (q.shape[1] > 1 and q.stride(1) != 1):
+        raise ValueError(f"{what} must be [rows, {K // 2 if fmt == 'mxfp4' else K}] with a contiguous last dimension")
+    if scale.dim() != 2 or tuple(scale.shape) != (q.shape[0], K // 32) or (K > 32 and scale.stride(1) != 1):
+        raise ValueError(f"{what}'s scale must be [{q.shape[0]}, {K // 32}] with a contiguous last dimension")
+    p.q = _dev_ptr(q, what, torch.uint8)
+    p.scale = _dev_ptr(scale, "scale", torch.uint8)
+    # one row: any stride will do
+    p.ldq = q.stride(0) if q.shape[0] > 1 else q.shape[1]
+    p.lds = scale.stride(0) if q.shape[0] > 1 else scale.shape[1]
+    return q.shape[0]
+
+
+def _check_sorted(st, ex, block, dev):
+    """The sort's outputs as the expert products read them; returns the blocks."""
+    torch = _torch()
+    if block < 1:
+        raise ValueError("block must be at least 1")
+    for t, name in ((st, "sorted_token_ids"), (ex, "expert_ids")):
+        if t.dim() != 1 or t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be a contiguous int32 vector on {dev}")
+    n = min(ex.numel(), st.numel() // block)
+    if n < 1:
+        raise ValueError("sorted_token_ids and expert_ids hold no block")
+    return n
+
+
+def _expert_scratch(scratch, M, topk, R, dev):
+    if scratch is None:
+        return ExpertScratch(M, topk, R, device=dev)
+    _check_scratch(scratch, dev)
+    return scratch
+
+
+class PreparedMxGemm(_Prepared):
+    """mx_gemm over fixed buffers; arguments as mx_gemm."""
+
+    def __init__(self, q, scale, w: MxWeight, out=None, out_dtype=None, scratch: ExpertScratch | None = None):
+        torch = _torch()
+        if w.codes.dim() != 2 or w.gate_up:
+            raise ValueError("mx_gemm takes a weight [R, K] laid out without gate_up")
+        dev = _one_device(q=q, scale=scale, w=w.codes, out=out)
+        p = self.p = MxGemmParams()
+        M = _mx_rows(p, q, scale, w.K, w.format)
+        if out is None:
+            out = torch.empty((M, w.R), dtype=out_dtype or torch.bfloat16, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
+        if out.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out must be bfloat16 or float32")
+        if tuple(out.shape) != (M, w.R) or (w.R > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < w.R):
+            raise ValueError(f"out must have shape {(M, w.R)} with a contiguous last dimension")
+        scratch = _expert_scratch(scratch, M, 1, 0, dev)
+        p.w, p.w_scale = w.codes.data_ptr(), w.packed.data_ptr()
+        p.M, p.R, p.K, p.format = M, w.R, w.K, QUANT_FORMAT[w.format]
+        p.out, p.ldo, p.out_fp32 = out.data_ptr(), out.stride(0) if M > 1 else w.R, int(out.dtype == torch.float32)
+        p.scratch, p.scratch_bytes = scratch.ptr, scratch.nbytes
+        self.out, self.device, self._keep = out, dev, (q, scale, w, scratch)
+        self._ref = ctypes.byref(p)
+        self._fn, self._name = _load().mr_mx_gemm, "mr_mx_gemm"
+
+
+def mx_gemm(q, scale, w: MxWeight, out=None, out_dtype=None, scratch: ExpertScratch | None = None, stream=None):
+    """Product of microscaled operands: [M, R] (bf16, or out_dtype fp32) =
+    x [M, K] @ w [R, K]^T with x given as the codes q and scales of
+    mxfp8_quant / mxfp4_quant, in the weight's format."""
+    return PreparedMxGemm(q, scale, w, out, out_dtype, scratch)(stream)
+
+
+class PreparedGateUp(_Prepared):
+    """moe_gate_up over fixed buffers; arguments as moe_gate_up."""
+
+    def __init__(self, q, scale, w13: MxWeight, sorted_token_ids, expert_ids, topk: int, block: int,
+                 num_tokens: int | None = None, sorted_rows: bool = False, quant=None, out=None,
+                 scratch: ExpertScratch | None = None):
+        torch = _torch()
+        if w13.codes.dim() != 3 or not w13.gate_up:
+            raise ValueError("moe_gate_up takes a weight [E, 2I, K] laid out with gate_up=True")
+        if quant not in QUANT_FORMAT:
+            raise ValueError(f"quant must be one of {list(QUANT_FORMAT)}")
+        o0, o1 = (out, None) if quant is None or out is None else out
+        dev = _one_device(q=q, scale=scale, w13=w13.codes, sorted_token_ids=sorted_token_ids, expert_ids=expert_ids,
+                          out=o0, out_scale=o1)
+        p = self.p = GateUpParams()
+        rows = _mx_rows(p, q, scale, w13.K, w13.format)
+        n = _check_sorted(sorted_token_ids, expert_ids, block, dev)
+        if sorted_rows:
+            if num_tokens is None:
+                raise ValueError("sorted rows need num_tokens")
+            if rows < n * block:
+                raise ValueError(f"sorted rows: q needs {n * block} rows, has {rows}")
+        elif num_tokens is not None and num_tokens != rows:
+            raise ValueError("num_tokens differs from the rows of q")
+        M = num_tokens if sorted_rows else rows
+        I = w13.R // 2
+        cap = sorted_token_ids.numel()
+        if quant is None:
+            if o0 is None:
+                o0 = torch.empty((cap, I), dtype=torch.bfloat16, device=dev)
+            _check_out(o0, "out", (cap, I), torch.bfloat16, dev)
+            out = o0
+        else:
+            iq = I // 2 if quant == "mxfp4" else I
+            if o0 is None:
+                o0 = torch.empty((cap, iq), dtype=torch.uint8, device=dev)
+                o1 = torch.empty((cap, I // 32), dtype=torch.uint8, device=dev)
+            _check_out(o0, "out codes", (cap, iq), torch.uint8, dev)
+            _check_out(o1, "out scale", (cap, I // 32), torch.uint8, dev)
+            out = (o0, o1)
+        scratch = _expert_scratch(scratch, M, topk, 0, dev)
+        p.sorted_rows = int(sorted_rows)
+        p.w13, p.w13_scale = w13.codes.data_ptr(), w13.packed.data_ptr()
+        p.E, p.I, p.K, p.format = w13.E, I, w13.K, QUANT_FORMAT[w13.format]
+        p.sorted_token_ids, p.expert_ids = sorted_token_ids.data_ptr(), expert_ids.data_ptr()
+        p.n_blocks, p.block, p.M, p.topk = n, block, M, topk
+        p.out_format, p.act = QUANT_FORMAT[quant], o0.data_ptr()
+        p.act_scale = None if quant is None else o1.data_ptr()
+        p.scratch, p.scratch_bytes = scratch.ptr, scratch.nbytes
+        self.out, self.device, self._keep = out, dev, (q, scale, w13, sorted_token_ids, expert_ids, scratch)
+        self._ref = ctypes.byref(p)
+        self._fn, self._name = _load().mr_moe_gate_up, "mr_moe_gate_up"
+
+
+def moe_gate_up(q, scale, w13: MxWeight, sorted_token_ids, expert_ids, topk: int, block: int,
+                num_tokens: int | None = None, sorted_rows: bool = False, quant=None, out=None,
+                scratch: ExpertScratch | None = None, stream=None):
+    """Stage 1 of the routed experts (mr_moe_gate_up): silu(x . gate^T) *
+    (x . up^T) of every assignment, at its sorted position.  q, scale: the
+    quantised tokens [M, ...], or with sorted_rows the rows at the sorted
+    positions (moe_sort_quant(..., sorted_rows=True); num_tokens is then the
+    number of tokens).  quant None: bf16 [capacity, I]; "mxfp8" / "mxfp4":
+    (codes, scales), as mxfp8_quant / mxfp4_quant of those rows.  Rows that
+    hold no assignment are left as they were."""
+    return PreparedGateUp(q, scale, w13, sorted_token_ids, expert_ids, topk, block, num_tokens, sorted_rows, quant,
+                          out, scratch)(stream)
+
+
+class PreparedDown(_Prepared):
+    """moe_down over fixed buffers; arguments as moe_down."""
+
+    def __init__(self, q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, expert_ids, block: int,
+                 add=None, out=None, scratch: ExpertScratch | None = None):
+        torch = _torch()
+        if w2.codes.dim() != 3 or w2.gate_up:
+            raise ValueError("moe_down takes a weight [E, R, I] laid out without gate_up")
+        dev = _one_device(q=q, scale=scale, w2=w2.codes, topk_ids=topk_ids, topk_weights=topk_weights,
+                          sorted_token_ids=sorted_token_ids, expert_ids=expert_ids, add=add, out=out)
+        p = self.p = DownParams()
+        rows = _mx_rows(p, q, scale, w2.K, w2.format)
+        n = _check_sorted(sorted_token_ids, expert_ids, block, dev)
+        if rows < n * block:
+            raise ValueError(f"q needs {n * block} rows, has {rows}")
+        if topk_ids.dim() != 2:
+            raise ValueError("topk_ids must be contiguous [M, k]")
+        M, topk = topk_ids.shape
+        _check_out(topk_ids, "topk_ids", (M, topk), torch.int32, dev)
+        _check_out(topk_weights, "topk_weights", (M, topk), torch.float32, dev)
+        if add is not None:
+            _check_out(add, "add", (M, w2.R), torch.bfloat16, dev)
+        if out is None:
+            out = torch.empty((M, w2.R), dtype=torch.bfloat16, device=dev)
+        _check_out(out, "out", (M, w2.R), torch.bfloat16, dev)
+        scratch = _expert_scratch(scratch, M, topk, w2.R, dev)
+        p.w2, p.w2_scale = w2.codes.data_ptr(), w2.packed.data_ptr()
+        p.E, p.R, p.I, p.format = w2.E, w2.R, w2.K, QUANT_FORMAT[w2.format]
+        p.sorted_token_ids, p.expert_ids = sorted_token_ids.data_ptr(), expert_ids.data_ptr()
+        p.n_blocks, p.block, p.M, p.topk = n, block, M, topk
+        p.topk_ids, p.topk_weights = topk_ids.data_ptr(), topk_weights.data_ptr()
+        p.add = None if add is None else add.data_ptr()
+        p.out = out.data_ptr()
+        p.scratch, p.scratch_bytes = scratch.ptr, scratch.nbytes
+        self.out, self.device = out, dev
+        self._keep = (q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, add, scratch)
+        self._ref = ctypes.byref(p)
+        self._fn, self._name = _load().mr_moe_down, "mr_moe_down"
+
+
+def moe_down(q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, expert_ids, block: int, add=None,
+             out=None, scratch: ExpertScratch | None = None, stream=None):
+    """Stage 2 of the routed experts and the combination (mr_moe_down): bf16
+    [M, R] = add + sum over a token's slots of topk_weights times its row of
+    act @ w2^T.  q, scale: act's codes and scales at the sorted positions, as
+    moe_gate_up(..., quant=...) returns them.  Slots whose id is outside
+    [0, E) add nothing."""
+    return PreparedDown(q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, block, add, out,
+                        scratch)(stream)

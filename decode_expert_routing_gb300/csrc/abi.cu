@@ -5,6 +5,7 @@
 #include <atomic>
 
 #include "../../include/moe_route.h"
+#include "expert_plan.h"
 #include "internal.h"
 #include "route_plan.h"
 #include "sort.cuh"
@@ -101,7 +102,8 @@ int mr_set_wait_limit_ns(uint64_t ns) {
 
 int mr_device_error(int clear) {
     const int v = mr::route_device_error(clear), t = mr::tc_gemv_device_error(clear);
-    return (v < 0 || t < 0) ? MR_ERR_CUDA : (v || t) ? MR_ERR_TIMEOUT : MR_OK;
+    const int x = mr::expert_device_error(clear);
+    return (v < 0 || t < 0 || x < 0) ? MR_ERR_CUDA : (v || t || x) ? MR_ERR_TIMEOUT : MR_OK;
 }
 
 #ifdef MR_TRACE
@@ -566,6 +568,198 @@ int mr_shared_gate_up(const void* x, int64_t ldx, const uint8_t* w13, const uint
     a.tok_shift = mr::ilog2_exact(sp.tok);
     a.xpitch = sp.xpitch;
     return cuda_status(mr::launch_route_cluster(rp, a, as_stream(stream)));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ expert products
+
+static int check_mx_format(int format) {
+    return format == MR_QUANT_MXFP8 || format == MR_QUANT_MXFP4 ? MR_OK : MR_ERR_INVALID_ARG;
+}
+
+// An MX operand of rows: codes with row stride ldq, scale bytes with row stride lds.
+static int check_mx_rows(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds, int K, int format) {
+    if (check_mx_format(format) != MR_OK || K < 1) return MR_ERR_INVALID_ARG;
+    if (K % 32 != 0) return MR_ERR_UNSUPPORTED;
+    if (q == nullptr || !aligned(q, 16) || scale == nullptr) return MR_ERR_INVALID_ARG;
+    const int64_t bytes = format == MR_QUANT_MXFP4 ? K / 2 : K;
+    if (ldq < bytes || ldq % 16 != 0 || lds < K / 32) return MR_ERR_INVALID_ARG;
+    return ldq < ((int64_t)1 << 40) ? MR_OK : MR_ERR_UNSUPPORTED;
+}
+
+// E weights [R, K]: limits of the tensor maps and of the kernel's 32-bit counts.
+static int check_mx_weight(int E, int R, int K, int gate_up) {
+    if (E < 1 || R < 1 || K < 1) return MR_ERR_INVALID_ARG;
+    if (E > MR_MAX_EXPERTS || K % 32 != 0 || K > (1 << 24) || R > (1 << 24)) return MR_ERR_UNSUPPORTED;
+    if (gate_up && R % 64 != 0) return MR_ERR_UNSUPPORTED;
+    return MR_OK;
+}
+
+static int check_mx_sorted(const int32_t* sorted, const int32_t* experts, int nblk, int block, int M, int topk, int E,
+                           int RT) {
+    if (M < 1 || topk < 1 || nblk < 1 || block < 1) return MR_ERR_INVALID_ARG;
+    if (sorted == nullptr || !aligned(sorted, 4) || experts == nullptr || !aligned(experts, 4))
+        return MR_ERR_INVALID_ARG;
+    if (topk > MR_MAX_TOPK || block > 1024) return MR_ERR_UNSUPPORTED;
+    const int64_t mk = (int64_t)M * topk, cap = (int64_t)nblk * block;
+    if (mk >= ((int64_t)1 << 30) || cap >= ((int64_t)1 << 31) || (cap / 256 + E) * RT >= ((int64_t)1 << 31))
+        return MR_ERR_UNSUPPORTED;
+    return MR_OK;
+}
+
+static int check_expert_scratch(const void* scratch, size_t have, size_t need) {
+    if (scratch == nullptr || !aligned(scratch, 256)) return MR_ERR_INVALID_ARG;
+    return have >= need ? MR_OK : MR_ERR_SCRATCH_TOO_SMALL;
+}
+
+static int run_expert(const mr::ExpertCall& c, void* stream) {
+    cudaError_t e = cudaSuccess;
+    const int s = mr::launch_expert(c, as_stream(stream), &e);
+    return s == MR_ERR_CUDA ? cuda_status(e) : s;
+}
+
+extern "C" {
+
+size_t mr_mx_packed_scale_bytes(int E, int R, int K, int format, int gate_up) {
+    if (check_mx_format(format) != MR_OK || check_mx_weight(E, R, K, gate_up) != MR_OK) return 0;
+    const mr::ExpertShape s = mr::expert_shape(R, K, format == MR_QUANT_MXFP4, gate_up != 0);
+    return (size_t)E * s.RT * s.KI * s.W * 512;
+}
+
+int mr_mx_pack_scales(const uint8_t* scale, int E, int R, int K, int format, int gate_up, void* packed, void* stream) {
+    int s = check_mx_format(format);
+    if (s != MR_OK || (s = check_mx_weight(E, R, K, gate_up)) != MR_OK) return s;
+    if (scale == nullptr || packed == nullptr || !aligned(packed, 16)) return MR_ERR_INVALID_ARG;
+    return cuda_status(mr::launch_mx_pack(scale, E, R, K, format == MR_QUANT_MXFP4, gate_up != 0, packed,
+                                          as_stream(stream)));
+}
+
+size_t mr_expert_scratch_bytes(int M_max, int topk, int R, int down) {
+    if (M_max < 1 || topk < 1 || topk > MR_MAX_TOPK || (down && R < 1)) return 0;
+    const int64_t mk = (int64_t)M_max * topk;
+    if (mk >= ((int64_t)1 << 30)) return 0;
+    return mr::expert_scratch_bytes(mk, down ? R : 0);
+}
+
+int mr_mx_gemm(const mr_mx_gemm_params* p, void* stream) {
+    if (p == nullptr || p->M < 1) return MR_ERR_INVALID_ARG;
+    int s = check_mx_rows(p->q, p->ldq, p->scale, p->lds, p->K, p->format);
+    if (s != MR_OK || (s = check_mx_weight(1, p->R, p->K, 0)) != MR_OK) return s;
+    if (p->w == nullptr || !aligned(p->w, 16) || p->w_scale == nullptr || !aligned(p->w_scale, 16) ||
+        p->out == nullptr || !aligned(p->out, p->out_fp32 ? 4 : 2) || p->ldo < p->R)
+        return MR_ERR_INVALID_ARG;
+    if (p->M >= (1 << 30)) return MR_ERR_UNSUPPORTED;
+    if ((s = check_expert_scratch(p->scratch, p->scratch_bytes, mr::expert_scratch_bytes(p->M, 0))) != MR_OK) return s;
+    mr::ExpertCall c{};
+    c.op = 0;
+    c.fp4 = p->format == MR_QUANT_MXFP4;
+    c.out_fmt = p->out_fp32 ? 3 : 0;
+    c.E = 1;
+    c.R = p->R;
+    c.K = p->K;
+    c.M = p->M;
+    c.topk = 1;
+    if (((int64_t)p->M / 256 + 1) * ((p->R + 127) / 128) >= ((int64_t)1 << 31)) return MR_ERR_UNSUPPORTED;
+    c.w = p->w;
+    c.w_scale = static_cast<const uint8_t*>(p->w_scale);
+    c.x = p->q;
+    c.x_scale = p->scale;
+    c.ldx = p->ldq;
+    c.lds = p->lds;
+    c.ldo = p->ldo;
+    c.x_rows = p->M;
+    c.out = p->out;
+    c.scratch = p->scratch;
+    return run_expert(c, stream);
+}
+
+int mr_moe_gate_up(const mr_moe_gate_up_params* p, void* stream) {
+    if (p == nullptr) return MR_ERR_INVALID_ARG;
+    int s = check_mx_rows(p->q, p->ldq, p->scale, p->lds, p->K, p->format);
+    if (s != MR_OK) return s;
+    if (p->I < 1) return MR_ERR_INVALID_ARG;
+    if (p->I % 32 != 0 || p->I > (1 << 23)) return MR_ERR_UNSUPPORTED;
+    if ((s = check_mx_weight(p->E, 2 * p->I, p->K, 1)) != MR_OK) return s;
+    if ((s = check_mx_sorted(p->sorted_token_ids, p->expert_ids, p->n_blocks, p->block, p->M, p->topk, p->E,
+                             (p->I + 63) / 64)) != MR_OK)
+        return s;
+    if (p->w13 == nullptr || !aligned(p->w13, 16) || p->w13_scale == nullptr || !aligned(p->w13_scale, 16))
+        return MR_ERR_INVALID_ARG;
+    const int of = p->out_format;
+    if (of != MR_QUANT_NONE && check_mx_format(of) != MR_OK) return MR_ERR_INVALID_ARG;
+    if (p->act == nullptr || !aligned(p->act, of == MR_QUANT_NONE ? 16 : 8) ||
+        (of != MR_QUANT_NONE && p->act_scale == nullptr))
+        return MR_ERR_INVALID_ARG;
+    const int64_t mk = (int64_t)p->M * p->topk;
+    if ((s = check_expert_scratch(p->scratch, p->scratch_bytes, mr::expert_scratch_bytes(mk, 0))) != MR_OK) return s;
+    mr::ExpertCall c{};
+    c.op = 1;
+    c.fp4 = p->format == MR_QUANT_MXFP4;
+    c.gather = p->sorted_rows ? 0 : 1;
+    c.out_fmt = of;
+    c.E = p->E;
+    c.R = 2 * p->I;
+    c.K = p->K;
+    c.M = p->M;
+    c.topk = p->topk;
+    c.nblk = p->n_blocks;
+    c.block = p->block;
+    c.w = p->w13;
+    c.w_scale = static_cast<const uint8_t*>(p->w13_scale);
+    c.x = p->q;
+    c.x_scale = p->scale;
+    c.ldx = p->ldq;
+    c.lds = p->lds;
+    c.x_rows = p->sorted_rows ? (int64_t)p->n_blocks * p->block : p->M;
+    c.sorted = p->sorted_token_ids;
+    c.experts = p->expert_ids;
+    c.out = p->act;
+    c.out_scale = p->act_scale;
+    c.scratch = p->scratch;
+    return run_expert(c, stream);
+}
+
+int mr_moe_down(const mr_moe_down_params* p, void* stream) {
+    if (p == nullptr) return MR_ERR_INVALID_ARG;
+    int s = check_mx_rows(p->q, p->ldq, p->scale, p->lds, p->I, p->format);
+    if (s != MR_OK || (s = check_mx_weight(p->E, p->R, p->I, 0)) != MR_OK) return s;
+    if ((s = check_mx_sorted(p->sorted_token_ids, p->expert_ids, p->n_blocks, p->block, p->M, p->topk, p->E,
+                             (p->R + 127) / 128)) != MR_OK)
+        return s;
+    if (p->w2 == nullptr || !aligned(p->w2, 16) || p->w2_scale == nullptr || !aligned(p->w2_scale, 16) ||
+        p->topk_ids == nullptr || !aligned(p->topk_ids, 4) || p->topk_weights == nullptr ||
+        !aligned(p->topk_weights, 4) || p->out == nullptr || !aligned(p->out, 2) || (p->add && !aligned(p->add, 2)))
+        return MR_ERR_INVALID_ARG;
+    const int64_t mk = (int64_t)p->M * p->topk;
+    const size_t need = mr::expert_scratch_bytes(mk, p->R);
+    if ((s = check_expert_scratch(p->scratch, p->scratch_bytes, need)) != MR_OK) return s;
+    mr::ExpertCall c{};
+    c.op = 2;
+    c.fp4 = p->format == MR_QUANT_MXFP4;
+    c.E = p->E;
+    c.R = p->R;
+    c.K = p->I;
+    c.M = p->M;
+    c.topk = p->topk;
+    c.nblk = p->n_blocks;
+    c.block = p->block;
+    c.w = p->w2;
+    c.w_scale = static_cast<const uint8_t*>(p->w2_scale);
+    c.x = p->q;
+    c.x_scale = p->scale;
+    c.ldx = p->ldq;
+    c.lds = p->lds;
+    c.x_rows = (int64_t)p->n_blocks * p->block;
+    c.sorted = p->sorted_token_ids;
+    c.experts = p->expert_ids;
+    c.topk_ids = p->topk_ids;
+    c.topk_weights = p->topk_weights;
+    c.add = p->add;
+    c.out = p->out;
+    c.y = reinterpret_cast<float*>(static_cast<char*>(p->scratch) + mr::kWorkOffset + mr::expert_part_bytes(mk));
+    c.scratch = p->scratch;
+    return run_expert(c, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,206 @@
+// The expert products' launches: mr_mx_pack_scales, mr_mx_gemm,
+// mr_moe_gate_up and mr_moe_down (see expert_gemm.cuh for the kernel).
+#include "../../include/moe_route.h"
+#include "expert_gemm.cuh"
+#include "expert_plan.h"
+#include "tensor_map.h"
+
+namespace mr {
+
+// ------------------------------------------------------------------ scales, once per weight
+
+// One 32-bit word (four scales of one weight row) per thread, into the order
+// in which the tensor core takes them: for each expert, 128-row tile and
+// stage, words [32 lanes][4 groups of 32 rows] (twice for E2M1: a stage is two
+// words wide).  Tile row i of a gate/up weight is, 16 rows of either in turn,
+// gate row or up row of the tile's 64 features.  Scales past the weight's
+// edge are zero bytes; they meet zero codes.
+__global__ void __launch_bounds__(256) mx_pack_kernel(const uint8_t* scale, uint32_t* packed, int64_t words, int R,
+                                                      int RT, int KI, int kb, int W, int gate_up) {
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += (int64_t)gridDim.x * blockDim.x) {
+        const int row = (int)(i & 3) * 32 + (int)((i >> 2) & 31);
+        int64_t u = i >> 7;
+        const int w = (int)(u % W);
+        u /= W;
+        const int ki = (int)(u % KI);
+        u /= KI;
+        const int rt = (int)(u % RT);
+        const int64_t e = u / RT;
+        int r = rt * 128 + row;
+        bool in = r < R;
+        if (gate_up) {
+            const int feature = rt * 64 + (row >> 5) * 16 + (row & 15);
+            r = ((row >> 4) & 1) * (R >> 1) + feature;
+            in = feature < (R >> 1);
+        }
+        uint32_t v = 0;
+        const uint8_t* s = scale + (e * R + r) * kb;
+        for (int b = 0; b < 4; ++b) {
+            const int k = (ki * W + w) * 4 + b;
+            if (in && k < kb) v |= (uint32_t)s[k] << (8 * b);
+        }
+        packed[i] = v;
+    }
+}
+
+cudaError_t launch_mx_pack(const uint8_t* scale, int64_t E, int R, int K, int fp4, int gate_up, void* packed,
+                           cudaStream_t st) {
+    const ExpertShape s = expert_shape(R, K, fp4, gate_up);
+    const int64_t words = E * s.RT * s.KI * s.W * 128;
+    int64_t ctas = (words + 255) / 256;
+    if (ctas > 152 * 8) ctas = 152 * 8;
+    return launch_kernel(mx_pack_kernel, dim3((unsigned)ctas), dim3(256), 0, st, scale, static_cast<uint32_t*>(packed),
+                         words, R, s.RT, s.KI, K / 32, s.W, gate_up);
+}
+
+// ------------------------------------------------------------------ the combination over a token's experts
+
+// out[m, r] = bf16(add[m, r] + sum_j weights[m, j] y[m * topk + j, r]), j
+// ascending in fp32; assignments whose expert is outside [0, E) are skipped.
+// A thread takes four columns of a row.
+__global__ void __launch_bounds__(256) expert_combine_kernel(const float* y, const int32_t* ids, const float* weights,
+                                                             const __nv_bfloat16* add, __nv_bfloat16* out, int64_t M,
+                                                             int topk, int R, int E) {
+    pdl_trigger();
+    pdl_wait();
+    const int per = (R + 3) >> 2;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < M * per; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t m = i / per;
+        const int r = (int)(i - m * per) * 4;
+        float s[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[u] = add != nullptr && r + u < R ? __bfloat162float(add[m * R + r + u]) : 0.0f;
+        for (int j = 0; j < topk; ++j) {
+            const int e = __ldg(ids + m * topk + j);
+            if (e < 0 || e >= E) continue;
+            const float w = __ldg(weights + m * topk + j);
+            const float* p = y + (m * topk + j) * R + r;
+            if ((R & 3) == 0) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+                s[0] = __fmaf_rn(w, v.x, s[0]);
+                s[1] = __fmaf_rn(w, v.y, s[1]);
+                s[2] = __fmaf_rn(w, v.z, s[2]);
+                s[3] = __fmaf_rn(w, v.w, s[3]);
+            } else {
+                for (int u = 0; u < 4 && r + u < R; ++u) s[u] = __fmaf_rn(w, __ldcg(p + u), s[u]);
+            }
+        }
+        for (int u = 0; u < 4; ++u)
+            if (r + u < R) out[m * R + r + u] = __float2bfloat16_rn(s[u]);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+namespace {
+
+bool encode(CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+    const EncodeTiled fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP4, int OP>
+cudaError_t launch_one(const ExpertArgs& a, int grid, cudaStream_t st) {
+    static int prepared[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
+        e = cudaFuncSetAttribute(expert_kernel<FP4, OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmemDyn);
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
+    }
+    return launch_kernel(expert_kernel<FP4, OP>, dim3((unsigned)grid), dim3(kExThreads), kExSmemDyn, st, a);
+}
+
+}  // namespace
+
+int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
+    const bool fp4 = c.fp4 != 0;
+    const int R = c.R, K = c.K;
+    const ExpertShape s = expert_shape(R, K, fp4, c.op == kExGateUp);
+    int dev = 0, sms = 0;
+    if ((*err = cudaGetDevice(&dev)) != cudaSuccess ||
+        (*err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return MR_ERR_CUDA;
+    ExpertArgs a{};
+    const cuuint64_t kbytes = (cuuint64_t)(fp4 ? K / 2 : K);
+    {
+        const cuuint64_t per = kbytes * (cuuint64_t)R;  // bytes of one expert
+        if (c.op == kExGateUp) {
+            // [expert][16-row group][gate or up][row of the group][k]: a box of
+            // four groups is a tile of 64 features with both of their rows
+            const cuuint64_t dims[5] = {kbytes, 16, 2, (cuuint64_t)(R / 32), (cuuint64_t)c.E};
+            const cuuint64_t strides[4] = {kbytes, per / 2, 16 * kbytes, per};
+            const cuuint32_t box[5] = {128, 16, 2, 4, 1};
+            if (!encode(&a.tm_w, c.w, 5, dims, strides, box)) return MR_ERR_UNSUPPORTED;
+        } else {
+            const cuuint64_t dims[3] = {kbytes, (cuuint64_t)R, (cuuint64_t)c.E};
+            const cuuint64_t strides[2] = {kbytes, per};
+            const cuuint32_t box[3] = {128, 128, 1};
+            if (!encode(&a.tm_w, c.w, 3, dims, strides, box)) return MR_ERR_UNSUPPORTED;
+        }
+        const cuuint64_t dims[2] = {kbytes, (cuuint64_t)c.x_rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)c.ldx};
+        const cuuint32_t box[2] = {128, c.gather ? 1u : 16u};
+        if (!encode(&a.tm_x, c.x, 2, dims, strides, box)) return MR_ERR_UNSUPPORTED;
+    }
+    a.w_scale = c.w_scale;
+    a.x_scale = c.x_scale;
+    a.lds = c.lds;
+    a.sorted = c.sorted;
+    a.experts = c.experts;
+    a.out = c.out;
+    a.out_scale = c.out_scale;
+    a.y = c.y;
+    a.ldo = c.ldo;
+    a.wait_ns = wait_limit_ns();
+    a.E = c.E;
+    a.R = R;
+    a.RT = s.RT;
+    a.KI = s.KI;
+    a.kb = K / 32;
+    a.M = c.M;
+    a.topk = c.topk;
+    a.mk = c.M * c.topk;
+    a.nblk = c.nblk;
+    a.block = c.block;
+    a.gather = c.gather;
+    a.sf_words = (K % 128 == 0 && c.lds % 4 == 0 && (reinterpret_cast<uintptr_t>(c.x_scale) & 3) == 0) ? 1 : 0;
+    a.out_fmt = c.out_fmt;
+    a.flags = launch_flags();
+    const int grid = sms;
+    cudaError_t e;
+    if (c.op == kExGemm) e = fp4 ? launch_one<true, kExGemm>(a, grid, st) : launch_one<false, kExGemm>(a, grid, st);
+    else if (c.op == kExGateUp)
+        e = fp4 ? launch_one<true, kExGateUp>(a, grid, st) : launch_one<false, kExGateUp>(a, grid, st);
+    else e = fp4 ? launch_one<true, kExDown>(a, grid, st) : launch_one<false, kExDown>(a, grid, st);
+    if (e == cudaSuccess && c.op == kExDown) {
+        const int64_t work = (int64_t)c.M * ((R + 3) / 4);
+        int64_t ctas = (work + 255) / 256;
+        if (ctas > (int64_t)sms * 8) ctas = (int64_t)sms * 8;
+        e = launch_kernel(expert_combine_kernel, dim3((unsigned)ctas), dim3(256), 0, st, static_cast<const float*>(c.y),
+                          c.topk_ids, c.topk_weights, static_cast<const __nv_bfloat16*>(c.add),
+                          static_cast<__nv_bfloat16*>(c.out), (int64_t)c.M, c.topk, R, c.E);
+    }
+    *err = e;
+    return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
+}
+
+int expert_device_error(int clear) {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_ex_timeout, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && v) {
+        const int z = 0;
+        if (cudaMemcpyToSymbol(g_ex_timeout, &z, sizeof(int)) != cudaSuccess) return -1;
+    }
+    return v;
+}
+
+}  // namespace mr

@@ -35,6 +35,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "route_plan.h"
+#include "tensor_map.h"
 
 namespace mr {
 
@@ -236,15 +237,7 @@ __global__ void __launch_bounds__(kRouteThreads, 1) tc_gemv_kernel(const __grid_
     MR_TRACE_STAMP(a.trace, 3);
 }
 
-namespace {
-
-// cuTensorMapEncodeTiled, from the driver through the runtime's entry-point
-// query (the library links only the CUDA runtime).
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() {
+EncodeTiled encode_tiled() {
     static EncodeTiled fn = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -258,10 +251,12 @@ EncodeTiled encode_fn() {
     return fn;
 }
 
+namespace {
+
 // A 2-D bf16 tensor map over rows x cols (row pitch pitch_elems) with a box
 // of 64 columns x box_rows rows in the 128-byte swizzle.
 bool encode_rows(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t pitch_elems, int box_rows) {
-    const EncodeTiled fn = encode_fn();
+    const EncodeTiled fn = encode_tiled();
     if (fn == nullptr) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)(pitch_elems * 2)};

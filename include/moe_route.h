@@ -510,6 +510,130 @@ int mr_shared_gate_up(const void *x, int64_t ldx, const uint8_t *w13, const uint
 int mr_router_gemv_noalloc(const void *x, int64_t ldx, const void *w, float *logits,
                            int M, int N, int K, void *stream);
 
+/*
+ * The expert products behind the route: weights and activations in one MX
+ * format (MR_QUANT_MXFP8 or MR_QUANT_MXFP4), multiplied on the block-scaled
+ * tensor core with fp32 accumulation.  An element is code * 2^(scale - 127),
+ * its scale shared by 32 elements along K; a NaN code or the scale byte 255
+ * makes the results that use it NaN.  K % 32 == 0.
+ *
+ * Weight scales are laid out once for the tensor core:
+ * mr_mx_packed_scale_bytes gives the size (0 for out-of-range arguments),
+ * mr_mx_pack_scales fills packed (16-byte aligned) from the row-major bytes
+ * scale [E, R, K/32].  gate_up != 0 for the weight of mr_moe_gate_up (R = 2I,
+ * gate rows first; I % 32 == 0), 0 for the others.  The codes stay as they
+ * are: E4M3 [E, R, K] or E2M1 [E, R, K/2], contiguous, 16-byte aligned.
+ */
+size_t mr_mx_packed_scale_bytes(int E, int R, int K, int format, int gate_up);
+int mr_mx_pack_scales(const uint8_t *scale, int E, int R, int K, int format, int gate_up, void *packed,
+                      void *stream);
+
+/*
+ * Scratch bytes for calls of up to M_max rows and top-k slots: of
+ * mr_moe_down with R output columns (down != 0), or of mr_mx_gemm (topk 1)
+ * and mr_moe_gate_up (down == 0, R ignored).  The first
+ * MR_SCRATCH_COUNTER_BYTES hold counters; the rules of every scratch buffer
+ * hold (zeroed once, then left reusable; not shared by calls that may run
+ * concurrently, captured graphs among them).  Returns 0 for out-of-range
+ * arguments.  Pure host function.
+ */
+size_t mr_expert_scratch_bytes(int M_max, int topk, int R, int down);
+
+/*
+ * Product of microscaled operands:
+ *   out[m, r] = sum_k x[m, k] w[r, k]
+ * q, scale: rows of codes and scale bytes with row strides ldq and lds in
+ * BYTES (q 16-byte aligned, ldq a multiple of 16); w: codes [R, K],
+ * w_scale: packed with gate_up == 0.  out: bf16, or fp32 with out_fp32 != 0,
+ * row stride ldo in elements.  Any M, R >= 1.  One launch.
+ */
+typedef struct mr_mx_gemm_params {
+    const uint8_t *q;
+    int64_t ldq;
+    const uint8_t *scale;
+    int64_t lds;
+    const uint8_t *w;
+    const void *w_scale;
+    int M, R, K, format;
+    void *out;
+    int64_t ldo;
+    int out_fp32;
+    void *scratch;
+    size_t scratch_bytes;
+} mr_mx_gemm_params;
+int mr_mx_gemm(const mr_mx_gemm_params *params, void *stream);
+
+/*
+ * Stage 1 of the routed experts: for every sorted position p that holds an
+ * assignment f of expert e,
+ *   h[p, r]   = sum_k x[k] w13[e, r, k]      x = row f / topk of q (or row p)
+ *   act[p, i] = bf16(silu(h[p, i]) * h[p, I + i])
+ * q, scale: with sorted_rows == 0 one row per token ([M, ...], gathered in
+ * the kernel); else one row per sorted position, as mr_moe_sort_quant writes
+ * them with MR_QUANT_SORTED_ROWS.  Strides as mr_mx_gemm.  w13: [E, 2I, K].
+ * sorted_token_ids, expert_ids: of mr_moe_sort or the route, for M tokens,
+ * topk slots and this block; n_blocks entries of expert_ids and n_blocks *
+ * block of sorted_token_ids are read (all of what the sort writes; blocks of
+ * no expert, id -1, are skipped).
+ * out_format MR_QUANT_NONE: act bf16 [n_blocks * block, I] (16-byte aligned);
+ * MR_QUANT_MXFP8 / _MXFP4: act quantised exactly as mr_mxfp8_quant /
+ * mr_mxfp4_quant of the bf16 rows, codes in act (8-byte aligned) and scale
+ * bytes [n_blocks * block, I/32] in act_scale.  Only the rows of assignments
+ * are written: padding positions and everything behind the last block keep
+ * what they held.  E <= 1024, topk <= 32, block <= 1024.  One launch.
+ */
+typedef struct mr_moe_gate_up_params {
+    const uint8_t *q;
+    int64_t ldq;
+    const uint8_t *scale;
+    int64_t lds;
+    int sorted_rows;
+    const uint8_t *w13;
+    const void *w13_scale;
+    int E, I, K, format;
+    const int32_t *sorted_token_ids;
+    const int32_t *expert_ids;
+    int n_blocks, block, M, topk;
+    int out_format;
+    void *act;
+    uint8_t *act_scale;
+    void *scratch;
+    size_t scratch_bytes;
+} mr_moe_gate_up_params;
+int mr_moe_gate_up(const mr_moe_gate_up_params *params, void *stream);
+
+/*
+ * Stage 2 of the routed experts and the combination over a token's slots:
+ *   y[f, r]   = sum_i act[p(f), i] w2[e, r, i]
+ *   out[m, r] = bf16(add[m, r] + sum_j topk_weights[m, j] y[m * topk + j, r])
+ * the sum over j ascending in fp32, so the result does not depend on the
+ * order in which experts finish.  q, scale: the rows of act at their sorted
+ * positions (strides as mr_mx_gemm; padding rows are read but change
+ * nothing); w2: [E, R, I].  Slots whose id in topk_ids is outside [0, E) add
+ * nothing; a token without any gives add, or zero.  topk_ids, topk_weights:
+ * [M, topk]; add: bf16 [M, R] or NULL; out: bf16 [M, R], may be add itself.
+ * scratch: mr_expert_scratch_bytes(M, topk, R, 1).
+ */
+typedef struct mr_moe_down_params {
+    const uint8_t *q;
+    int64_t ldq;
+    const uint8_t *scale;
+    int64_t lds;
+    const uint8_t *w2;
+    const void *w2_scale;
+    int E, R, I, format;
+    const int32_t *sorted_token_ids;
+    const int32_t *expert_ids;
+    int n_blocks, block, M, topk;
+    const int32_t *topk_ids;
+    const float *topk_weights;
+    const void *add;
+    void *out;
+    void *scratch;
+    size_t scratch_bytes;
+} mr_moe_down_params;
+int mr_moe_down(const mr_moe_down_params *params, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,105 @@
+"""Host-side checks of the expert products on a machine without a GPU: sizes,
+refusals, the binding's parameter blocks.  No call here reaches a kernel."""
+
+import ctypes
+
+import pytest
+
+import decode_expert_routing_gb300 as mr
+from decode_expert_routing_gb300 import build as mrbuild
+
+P = 0x10000  # never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    mrbuild.build()
+    return mr.load_library()
+
+
+def test_packed_scale_bytes(lib):
+    f = lib.mr_mx_packed_scale_bytes
+    assert f(1, 128, 128, 1, 0) == 512
+    assert f(1, 129, 128, 1, 0) == 1024
+    assert f(1, 128, 160, 1, 0) == 1024
+    assert f(1, 128, 256, 2, 0) == 1024        # E2M1: 256 elements a stage, two words a row
+    assert f(8, 1536, 6144, 1, 1) == 8 * 12 * 48 * 512
+    assert f(1, 64, 128, 1, 1) == 512          # 32 features: one tile
+    for bad in ((0, 128, 128, 1, 0), (1, 0, 128, 1, 0), (1, 128, 100, 1, 0), (1, 128, 128, 0, 0), (1, 128, 128, 3, 0),
+                (1025, 128, 128, 1, 0), (1, 96, 128, 1, 1)):
+        assert f(*bad) == 0, bad
+
+
+def test_expert_scratch_bytes(lib):
+    f = lib.mr_expert_scratch_bytes
+    small, big = f(1, 8, 0, 0), f(4096, 8, 0, 0)
+    assert 32768 < small < big == f(1 << 20, 8, 0, 0)
+    assert f(1, 8, 6144, 1) >= small + 8 * 6144 * 4
+    for bad in ((0, 8, 0, 0), (1, 0, 0, 0), (1, 33, 0, 0), (1, 8, 0, 1), (1 << 28, 32, 0, 0)):
+        assert f(*bad) == 0, bad
+
+
+def fill(p, **kw):
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return ctypes.byref(p)
+
+
+GEMM = dict(q=P, ldq=256, scale=P, lds=8, w=P, w_scale=P, M=4, R=100, K=256, format=1, out=P, ldo=100, out_fp32=0,
+            scratch=P, scratch_bytes=1 << 30)
+UP = dict(q=P, ldq=256, scale=P, lds=8, sorted_rows=0, w13=P, w13_scale=P, E=8, I=64, K=256, format=1,
+          sorted_token_ids=P, expert_ids=P, n_blocks=8, block=16, M=4, topk=2, out_format=0, act=P, act_scale=P,
+          scratch=P, scratch_bytes=1 << 30)
+DOWN = dict(q=P, ldq=64, scale=P, lds=2, w2=P, w2_scale=P, E=8, R=100, I=64, format=1, sorted_token_ids=P,
+            expert_ids=P, n_blocks=8, block=16, M=4, topk=2, topk_ids=P, topk_weights=P, add=None, out=P, scratch=P,
+            scratch_bytes=1 << 30)
+
+INVALID = [
+    ("gemm", dict(q=None)), ("gemm", dict(q=P + 8)), ("gemm", dict(ldq=240)), ("gemm", dict(ldq=264)),
+    ("gemm", dict(lds=7)), ("gemm", dict(scale=None)), ("gemm", dict(w=P + 4)), ("gemm", dict(w_scale=None)),
+    ("gemm", dict(M=0)), ("gemm", dict(R=0)), ("gemm", dict(K=0)), ("gemm", dict(format=0)), ("gemm", dict(format=7)),
+    ("gemm", dict(out=None)), ("gemm", dict(out=P + 1)), ("gemm", dict(out=P + 2, out_fp32=1)), ("gemm", dict(ldo=99)),
+    ("gemm", dict(scratch=None)), ("gemm", dict(scratch=P + 16)),
+    ("up", dict(I=0)), ("up", dict(E=0)), ("up", dict(M=0)), ("up", dict(topk=0)), ("up", dict(block=0)),
+    ("up", dict(n_blocks=0)), ("up", dict(sorted_token_ids=None)), ("up", dict(expert_ids=P + 2)),
+    ("up", dict(w13=None)), ("up", dict(act=None)), ("up", dict(act=P + 8)), ("up", dict(out_format=3)),
+    ("up", dict(out_format=1, act_scale=None)), ("up", dict(scratch=None)),
+    ("down", dict(w2=P + 8)), ("down", dict(topk_ids=None)), ("down", dict(topk_weights=P + 2)),
+    ("down", dict(out=None)), ("down", dict(add=P + 1)), ("down", dict(R=0)), ("down", dict(scratch=None)),
+]
+UNSUPPORTED = [
+    ("gemm", dict(K=272, ldq=272, lds=9)), ("gemm", dict(R=(1 << 24) + 1, ldo=1 << 25)),
+    ("gemm", dict(M=1 << 30)),
+    ("up", dict(I=48)), ("up", dict(E=1025)), ("up", dict(topk=33)), ("up", dict(block=1025)),
+    ("up", dict(M=1 << 27, topk=8)), ("up", dict(n_blocks=1 << 28)),
+    ("down", dict(E=2000)), ("down", dict(I=80, ldq=80, lds=3)),
+]
+
+
+def call(lib, op, change):
+    base, cls, fn = {"gemm": (GEMM, mr.MxGemmParams, lib.mr_mx_gemm), "up": (UP, mr.GateUpParams, lib.mr_moe_gate_up),
+                     "down": (DOWN, mr.DownParams, lib.mr_moe_down)}[op]
+    return fn(fill(cls(), **{**base, **change}), None)
+
+
+@pytest.mark.parametrize("op,change", INVALID)
+def test_invalid_arguments(lib, op, change):
+    assert call(lib, op, change) == mr.MR_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("op,change", UNSUPPORTED)
+def test_unsupported_shapes(lib, op, change):
+    assert call(lib, op, change) == mr.MR_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("op", ["gemm", "up", "down"])
+def test_short_scratch(lib, op):
+    assert call(lib, op, dict(scratch_bytes=1000)) == mr.MR_ERR_SCRATCH_TOO_SMALL
+
+
+def test_null_parameter_blocks(lib):
+    for fn in (lib.mr_mx_gemm, lib.mr_moe_gate_up, lib.mr_moe_down):
+        assert fn(None, None) == mr.MR_ERR_INVALID_ARG
+    assert lib.mr_mx_pack_scales(None, 1, 128, 128, 1, 0, P, None) == mr.MR_ERR_INVALID_ARG
+    assert lib.mr_mx_pack_scales(P, 1, 128, 128, 1, 0, P + 8, None) == mr.MR_ERR_INVALID_ARG
+    assert lib.mr_mx_pack_scales(P, 1, 128, 100, 1, 0, P, None) == mr.MR_ERR_UNSUPPORTED
