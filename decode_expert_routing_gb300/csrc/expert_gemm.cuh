@@ -12,12 +12,17 @@
 // Work: an expert's rows form column tiles of at most 256 rows; a tile is one
 // column tile times 128 weight rows, and its K range is cut into stages of
 // 128 bytes of codes a row (128 E4M3 or 256 E2M1 elements).  One CTA per SM
-// walks the tiles.  Warp 0 copies the codes (tensor maps, 128-byte swizzle;
-// rows in token order by four-row gathers) and the weights' scales (laid out
-// once, see mx_pack_kernel), warp 2 puts the activations' scales into the
-// same layout, one thread of warp 1 copies scales to tensor memory and
-// issues the products, and warps 4-7 read the accumulator back while the next
-// tile is computed into the other one.
+// walks the tiles.  Warp 0 copies the codes (tensor maps, 128-byte swizzle) and
+// the weights' scales (laid out once, see mx_pack_kernel), warp 3 the codes of
+// rows in token order (four-row gathers), warp 2 puts the activations' scales
+// into the weights' scale layout, warp 1 copies scales to tensor memory and
+// issues the products, and warps 4-11 read the accumulator back while the
+// next tile is computed into the other one.
+//
+// The loops of warps 0 and 1 are uniform over the warp (waits end in a vote,
+// one elected lane issues): as code of a single lane, the copies and products
+// of a stage took 700 and 850 cycles to issue, in uniform registers a
+// fraction of that.
 #pragma once
 
 #include <cuda.h>
@@ -28,11 +33,12 @@
 
 namespace mr {
 
-constexpr int kExThreads = 256;
+constexpr int kExThreads = 384;          // 4 warps of copies and products, 8 that read back
 constexpr int kExMaxStages = 12;
 constexpr int kExMaxN = 256;             // activation rows of a tile
 constexpr int kExWBytes = 128 * 128;     // one stage of weight codes
-constexpr int kExSmemDyn = 219 * 1024;   // dynamic shared memory (one CTA per SM)
+constexpr int kExSmemDyn = 214 * 1024;   // dynamic shared memory (one CTA per SM)
+constexpr int kExListMax = 1536;        // column tiles in the shared list
 constexpr int kExSfCol = 488;            // tensor-memory columns of the scale factors
 constexpr int kExBuf1 = 232;             // first column of the second accumulator
 // The two accumulators share columns 232-255 (256 + 256 + 24 columns of
@@ -45,6 +51,7 @@ enum { kExGemm = 0, kExGateUp = 1, kExDown = 2 };
 struct ExpertArgs {
     CUtensorMap tm_w;        // weight codes, box of 128 rows x 128 bytes
     CUtensorMap tm_x;        // activation codes, box of 16 rows (gather: 1 row) x 128 bytes
+    CUtensorMap tm_x64;      // the same in boxes of 64 rows
     const uint8_t* w_scale;  // packed: [E][row tile][stage][512 * words]
     const uint8_t* x_scale;  // [rows][lds] bytes
     int64_t lds;
@@ -58,7 +65,8 @@ struct ExpertArgs {
     int E, R, RT, KI, kb;    // weight rows, row tiles, stages, scale bytes per row
     int M, topk, mk, nblk, block;
     int gather;              // x rows in token order
-    int sf_words;            // the scale rows can be read as 32-bit words
+    int sf_vec;              // bytes that the scale rows can be read in: 16, 8, 4 or 1
+    int list_cap;            // column tiles that the shared list holds (0: none, they are searched for)
     int out_fmt;             // 0 bf16, 1 MXFP8, 2 MXFP4, 3 fp32
     int flags;
 };
@@ -77,37 +85,48 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, unsigned parity) {
         : "memory");
     return ok != 0;
 }
-// Waits for the phase of this parity, at most limit_ns; a wait that runs out
-// sets the device's flag and *abort, which ends every other wait of the CTA.
-__device__ __forceinline__ bool ex_wait(uint32_t bar, unsigned parity, unsigned long long limit_ns,
-                                        volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
+// The whole warp waits for the phase of this parity, at most limit_ns; a wait
+// that runs out sets the device's flag and *abort, which ends every other
+// wait of the CTA.
+__device__ __noinline__ bool ex_wait_slow(uint32_t bar, unsigned parity, unsigned long long limit_ns,
+                                          volatile int* abort) {
     const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort) return false;
-        if (global_ns() - t0 >= limit_ns) {
+    for (int i = 1;; ++i) {
+        if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+        if ((i & 15) != 0) continue;
+        const bool late = global_ns() - t0 >= limit_ns;
+        if (__any_sync(kFull, late)) {
             *abort = 1;
             atomicExch(&g_ex_timeout, 1);
-            return false;
         }
+        if (__any_sync(kFull, *abort != 0)) return false;
     }
-    return true;
+}
+__device__ __forceinline__ bool ex_wait(uint32_t bar, unsigned parity, unsigned long long limit_ns,
+                                        volatile int* abort) {
+    return __all_sync(kFull, mbar_try_wait(bar, parity)) || ex_wait_slow(bar, parity, limit_ns, abort);
+}
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool ex_elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
-// Shared-memory matrix descriptor: K-major rows of 128 bytes in the 128-byte
+// Shared-memory matrix descriptors without their address field (address >> 4
+// in the low 14 bits).  Codes: K-major rows of 128 bytes in the 128-byte
 // swizzle (8-row groups 1024 bytes apart); a k-step starts 32 bytes further.
-__device__ __forceinline__ unsigned long long ex_desc_sw128(uint32_t addr) {
-    return (unsigned long long)((addr >> 4) & 0x3FFFu) | (1ull << 16) | ((unsigned long long)(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
-}
+constexpr unsigned long long kExDescCodes =
+    (1ull << 16) | ((unsigned long long)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 // Scale factors: 32 rows of 16 bytes without swizzle, 8-row groups 128 bytes apart.
-__device__ __forceinline__ unsigned long long ex_desc_sf(uint32_t addr) {
-    return (unsigned long long)((addr >> 4) & 0x3FFFu) | ((unsigned long long)(128 >> 4) << 32) | (1ull << 46);
+constexpr unsigned long long kExDescSf = ((unsigned long long)(128 >> 4) << 32) | (1ull << 46);
+__device__ __forceinline__ unsigned long long ex_desc(unsigned long long kind, uint32_t addr) {
+    return kind | (unsigned long long)((addr >> 4) & 0x3FFFu);
 }
 // 32 rows of 16 bytes to four tensor-memory columns, repeated in each of the
 // four 32-lane quarters: lane l, column c holds the four scales of row 32 c + l.
 __device__ __forceinline__ void ex_copy_sf(uint32_t tmem, uint32_t addr) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(ex_desc_sf(addr)) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(ex_desc(kExDescSf, addr)) : "memory");
 }
 // Instruction descriptor without the scale selectors: E4M3 (format 0 of
 // kind::mxf8f6f4) or E2M1 (format 1 of kind::mxf4), both operands K-major,
@@ -173,15 +192,15 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* map, int x
         "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
         : "memory");
 }
-// Barrier of the four epilogue warps; true when ok holds in all of them.
-__device__ __forceinline__ bool ex_epi_sync(bool ok) {
+// Barrier id of threads threads (whole warps); true when ok holds in all of them.
+__device__ __forceinline__ bool ex_sync(int id, int threads, bool ok) {
     uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "barrier.cta.red.and.pred p, 1, 128, q;\n\t"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+        "barrier.cta.red.and.pred p, %1, %2, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)ok)
+        : "r"(id), "r"(threads), "r"((uint32_t)ok)
         : "memory");
     return r != 0;
 }
@@ -191,31 +210,60 @@ struct ExTables {
     int* first;  // [E] first sorted position
     int* rows;   // [E] rows
     int* pre;    // [E + 1] column tiles before expert e
+    int2* list;  // [list_cap] column tiles: first position, expert << 16 | rows
 };
 struct ExTile {
     int e, rt, r0, rows, n;  // expert, row tile, first position, real rows, accumulator columns
 };
 __device__ __forceinline__ int ex_ncol(int rows) { return (rows + kExMaxN - 1) / kExMaxN; }
+// Rows of each column tile of an expert (equal shares, a multiple of 16):
+// at most 256, and every tile has at least one row.
+__device__ __forceinline__ int ex_share(int rows, int nct) { return ((rows + nct - 1) / nct + 15) & ~15; }
 
-__device__ __forceinline__ ExTile ex_tile(const ExTables& t, int E, int RT, int tile) {
+// Column tile ct of the list, or (a list that does not fit: more than some
+// hundred thousand assignments) by a search over the experts.
+__device__ __forceinline__ ExTile ex_tile(const ExTables& t, int E, int ct, int rt, bool listed) {
     ExTile o;
-    const int ct = tile / RT;
-    o.rt = tile - ct * RT;
-    int lo = 0, hi = E;  // pre[lo] <= ct < pre[hi]
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (t.pre[m] <= ct) lo = m;
-        else hi = m;
+    o.rt = rt;
+    if (listed) {
+        const int2 v = t.list[ct];
+        o.r0 = __shfl_sync(kFull, v.x, 0);
+        const int w = __shfl_sync(kFull, v.y, 0);
+        o.e = w >> 16;
+        o.rows = w & 0xFFFF;
+    } else {
+        int lo = 0, hi = E;  // pre[lo] <= ct < pre[hi]
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            if (__shfl_sync(kFull, t.pre[m], 0) <= ct) lo = m;
+            else hi = m;
+        }
+        o.e = lo;
+        const int rows = t.rows[lo], nct = t.pre[lo + 1] - t.pre[lo], i = ct - t.pre[lo];
+        const int per = ex_share(rows, nct);
+        o.r0 = __shfl_sync(kFull, t.first[lo] + i * per, 0);
+        o.rows = __shfl_sync(kFull, min(per, rows - i * per), 0);
     }
-    o.e = lo;
-    const int rows = t.rows[lo], nct = t.pre[lo + 1] - t.pre[lo], i = ct - t.pre[lo];
-    // equal shares: per <= 256, and every tile has at least one row
-    const int per = ((rows + nct - 1) / nct + 15) & ~15;
-    o.r0 = t.first[lo] + i * per;
-    o.rows = min(per, rows - i * per);
     o.n = (o.rows + 15) & ~15;
     return o;
 }
+
+// The tiles of this CTA, every gridDim.x-th: row tiles fastest, so that the
+// CTAs at work share few activation rows and each weight is read once.
+struct ExWalk {
+    int ct, rt, dct, drt, RT;
+    __device__ __forceinline__ ExWalk(int rt_count) : RT(rt_count) {
+        ct = (int)blockIdx.x / RT;
+        rt = (int)blockIdx.x - ct * RT;
+        dct = (int)gridDim.x / RT;
+        drt = (int)gridDim.x - dct * RT;
+    }
+    __device__ __forceinline__ void next() {
+        ct += dct;
+        rt += drt;
+        if (rt >= RT) rt -= RT, ++ct;
+    }
+};
 
 template <bool FP4, int OP>
 __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_constant__ ExpertArgs a) {
@@ -223,26 +271,28 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
     extern __shared__ __align__(16) unsigned char dsm[];
     __shared__ __align__(8) unsigned long long s_full[kExMaxStages], s_empty[kExMaxStages], s_tfull[2], s_tfree, s_drain;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_total, s_nmax, s_warp[8];
-    __shared__ int s_f[2][kExMaxN];
-    __shared__ __align__(16) unsigned char s_act[OP == kExGateUp ? 2 * 16 * kExStagePitch : 16];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int s_abort, s_total, s_nmax, s_warp[kExThreads / 32];
+    __shared__ __align__(16) int s_f[2][OP == kExGemm ? 4 : kExMaxN];
+    __shared__ __align__(16) unsigned char s_act[OP == kExGateUp ? 4 * 16 * kExStagePitch : 16];
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
+    const bool gather = OP == kExGateUp && a.gather;
 
     // ---- set-up that reads nothing of the kernel before
     if (tid == 0) {
         for (int s = 0; s < kExMaxStages; ++s) {
-            mbar_init(smem_u32(&s_full[s]), 2);
+            mbar_init(smem_u32(&s_full[s]), gather ? 3 : 2);
             mbar_init(smem_u32(&s_empty[s]), 1);
         }
         mbar_init(smem_u32(&s_tfull[0]), 1);
         mbar_init(smem_u32(&s_tfull[1]), 1);
-        mbar_init(smem_u32(&s_tfree), 4);
+        mbar_init(smem_u32(&s_tfree), 8);
         mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        tma_prefetch_map(&a.tm_w);
-        tma_prefetch_map(&a.tm_x);
         s_abort = 0;
         s_nmax = 16;
+        tma_prefetch_map(&a.tm_w);
+        tma_prefetch_map(&a.tm_x);
+        if (!gather) tma_prefetch_map(&a.tm_x64);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
@@ -250,7 +300,8 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     ExTables t;
-    t.first = reinterpret_cast<int*>(dsm);
+    t.list = reinterpret_cast<int2*>(dsm);
+    t.first = reinterpret_cast<int*>(t.list + a.list_cap);
     t.rows = t.first + a.E;
     t.pre = t.rows + a.E;
     for (int e = tid; e < a.E; e += kExThreads) {
@@ -261,25 +312,30 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
     pdl_wait();
     __syncthreads();
 
-    // ---- the experts' runs of blocks: first and last block of each
+    // ---- the experts' runs of blocks: first block and the block behind the last
     if (OP != kExGemm) {
         for (int b = tid; b < a.nblk; b += kExThreads) {
             const int e = a.experts[b];
+            const int before = b > 0 ? a.experts[b - 1] : -1, after = b < a.nblk - 1 ? a.experts[b + 1] : -1;
             if (e < 0 || e >= a.E) continue;
-            if (b == 0 || a.experts[b - 1] != e) t.first[e] = b * a.block;
-            if (b == a.nblk - 1 || a.experts[b + 1] != e) t.rows[e] = b + 1;
+            if (before != e) t.first[e] = b * a.block;
+            if (after != e) t.rows[e] = b + 1;
         }
         __syncthreads();
-        for (int e = warp; e < a.E; e += kExThreads / 32) {
-            const int f = t.first[e];
-            if (f < 0) continue;
-            // rows of the run without the padding of its last block (the
-            // assignments of a block stand before its padding)
-            const int last = (t.rows[e] - 1) * a.block;
-            int real = 0;
-            for (int i = lane; i < a.block; i += 32) real += a.sorted[last + i] < a.mk ? 1 : 0;
-            real = __reduce_add_sync(kFull, real);
-            if (lane == 0) t.rows[e] = max(last - f + real, 0);
+        for (int e = tid; e < a.E; e += kExThreads)
+            if (t.first[e] >= 0) t.rows[e] = max(t.rows[e] * a.block - t.first[e], 0);
+        // the assignments of a block stand before its padding: every 16th
+        // entry of a run's last block tells where the run's rows may end
+        const int probes = (a.block - 1) / 16;
+        if (probes > 0) {
+            __syncthreads();
+            for (int i = tid; i < a.E * probes; i += kExThreads) {
+                const int e = i / probes, j = (i - e * probes + 1) * 16, f = t.first[e];
+                if (f < 0) continue;
+                // the run's end: a cut leaves at least 16 rows of its last block
+                const int last = (f + t.rows[e] + a.block - 1) / a.block * a.block - a.block;
+                if (last >= f && a.sorted[last + j] >= a.mk) atomicMin(&t.rows[e], last + j - f);
+            }
         }
         __syncthreads();
     }
@@ -295,80 +351,76 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
                 if (lane >= o) v += u;
             }
             if (lane == 31) s_warp[warp] = v;
-            if (c > 0) atomicMax(&s_nmax, ((rows + c - 1) / c + 15) & ~15);
+            if (c > 0) atomicMax(&s_nmax, ex_share(rows, c));
             __syncthreads();
             int before = run;
-            for (int w = 0; w < warp; ++w) before += s_warp[w];
-            if (e < a.E) t.pre[e] = before + v - c;
-            for (int w = 0; w < kExThreads / 32; ++w) run += s_warp[w];
+            for (int w = 0; w < kExThreads / 32; ++w) {
+                if (w < warp) before += s_warp[w];
+                run += s_warp[w];
+            }
+            before += v - c;
+            if (e < a.E) {
+                t.pre[e] = before;
+                for (int i = 0; i < c && before + i < a.list_cap; ++i) {
+                    const int per = ex_share(rows, c);
+                    t.list[before + i] = make_int2(t.first[e] + i * per, (e << 16) | min(per, rows - i * per));
+                }
+            }
             __syncthreads();
         }
         if (tid == 0) {
             t.pre[a.E] = run;
-            s_total = run * a.RT;
+            s_total = run;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
 
-    const int total = s_total, xrows = s_nmax;
+    const int total = __shfl_sync(kFull, s_total, 0), xrows = __shfl_sync(kFull, s_nmax, 0);
+    const bool listed = total <= a.list_cap;
     const int H = (xrows + 127) >> 7;  // 128-row groups of the activations' scales
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(kFull, s_tmem, 0);
     // stages of weight and activation codes, then their scale factors
-    const uint32_t tab = (uint32_t)(3 * a.E + 1) * 4u;
-    const uint32_t base = (smem_u32(dsm) + tab + 1023u) & ~1023u;
+    const uint32_t dyn = smem_u32(dsm);
+    const uint32_t base = (dyn + (uint32_t)a.list_cap * 8u + (uint32_t)(3 * a.E + 1) * 4u + 1023u) & ~1023u;
     const uint32_t code_bytes = (uint32_t)(kExWBytes + xrows * 128), sf_bytes = (uint32_t)(W * 512 * (1 + H));
-    const uint32_t room = smem_u32(dsm) + (uint32_t)kExSmemDyn - base;
-    const int nst = min(kExMaxStages, (int)(room / (code_bytes + sf_bytes)));
+    const int nst = min(kExMaxStages, (int)((dyn + (uint32_t)kExSmemDyn - base) / (code_bytes + sf_bytes)));
     const uint32_t sf_base = base + (uint32_t)nst * code_bytes;
-    const int step = (int)gridDim.x;
-    int st = 0;        // stage of the ring
-    unsigned ph = 0;   // its phase
+    const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
+    int st = 0;       // stage of the ring
+    unsigned ph = 0;  // its phase
+    ExWalk walk(a.RT);
 
     if (warp == 0) {
         // ---- codes, and the weights' scales
         int issued = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; ok && tile < total; tile += step) {
-            const ExTile o = ex_tile(t, a.E, a.RT, tile);
-            int tok[8];
-            if (OP == kExGateUp && a.gather) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = (lane + (i >> 2) * 32) * 4 + (i & 3);
-                    int f = r < o.rows ? a.sorted[o.r0 + r] : 0;
-                    if (f < 0 || f >= a.mk) f = 0;  // a padding position: any row, its column is not used
-                    tok[i] = f / a.topk;
-                }
-            }
+        for (; ok && walk.ct < total; walk.next()) {
+            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
             const uint8_t* ws = a.w_scale + ((int64_t)o.e * a.RT + o.rt) * a.KI * (W * 512);
+            const unsigned tx = (unsigned)(kExWBytes + W * 512 + (gather ? 0 : o.n * 128));
             for (int ki = 0; ki < a.KI; ++ki) {
-                if (!__all_sync(kFull, ex_wait(smem_u32(&s_empty[st]), ph ^ 1u, a.wait_ns, &s_abort))) {
+                if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
                 }
-                const uint32_t full = smem_u32(&s_full[st]);
-                const uint32_t ws_s = base + (uint32_t)st * code_bytes, xs_s = ws_s + kExWBytes;
-                if (lane == 0) {
-                    const unsigned stall = ((a.flags & 2) && issued == 0) ? 16u : 0u;
-                    mbar_expect_tx(full, (unsigned)(kExWBytes + o.n * 128 + W * 512) + stall);
-                    if (OP == kExGateUp) tma_load_5d(ws_s, &a.tm_w, ki * 128, 0, 0, o.rt * 4, o.e, full);
-                    else tma_load_3d(ws_s, &a.tm_w, ki * 128, o.rt * 128, o.e, full);
-                    bulk_load(sf_base + (uint32_t)st * sf_bytes, ws + (int64_t)ki * (W * 512), W * 512, full);
+                const uint32_t full = full0 + 8u * st, wsm = base + (uint32_t)st * code_bytes;
+                if (ex_elect()) {
+                    mbar_expect_tx(full, tx + (((a.flags & 2) && issued == 0) ? 16u : 0u));
+                    if (OP == kExGateUp) tma_load_5d(wsm, &a.tm_w, ki * 128, 0, 0, o.rt * 4, o.e, full);
+                    else tma_load_3d(wsm, &a.tm_w, ki * 128, o.rt * 128, o.e, full);
+                    bulk_load(sf_base + (uint32_t)st * sf_bytes, ws, W * 512, full);
+                    if (!gather) {
+                        int r = 0;
+                        for (; r + 64 <= o.n; r += 64)
+                            tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x64, ki * 128, o.r0 + r, full);
+                        for (; r < o.n; r += 16)
+                            tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x, ki * 128, o.r0 + r, full);
+                    }
                 }
                 __syncwarp();
-                if (OP == kExGateUp && a.gather) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int g = lane + i * 32;
-                        if (g * 4 < o.n)
-                            tma_gather4(xs_s + (uint32_t)g * 512u, &a.tm_x, ki * 128, tok[4 * i], tok[4 * i + 1],
-                                        tok[4 * i + 2], tok[4 * i + 3], full);
-                    }
-                } else if (lane * 16 < o.n) {
-                    tma_load_2d(xs_s + (uint32_t)lane * 2048u, &a.tm_x, ki * 128, o.r0 + lane * 16, full);
-                }
+                ws += W * 512;
                 ++issued;
                 if (++st == nst) st = 0, ph ^= 1u;
             }
@@ -378,179 +430,239 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
             for (int i = 0; i < min(issued, nst); ++i) {
                 if (--st < 0) st = nst - 1, ph ^= 1u;
                 const unsigned long long t0 = global_ns();
-                while (!mbar_try_wait(smem_u32(&s_full[st]), ph) && global_ns() - t0 < a.wait_ns / 16 + 1000) {
+                while (!mbar_try_wait(full0 + 8u * st, ph) && global_ns() - t0 < a.wait_ns / 16 + 1000) {
                 }
             }
         }
     } else if (warp == 1) {
-        // ---- products: one thread
-        if (lane == 0) {
-            bool ok = true;
-            int it = 0;
-            for (int tile = blockIdx.x; ok && tile < total; tile += step, ++it) {
-                const ExTile o = ex_tile(t, a.E, a.RT, tile);
-                const uint32_t d = tmem + ((it & 1) ? kExBuf1 : 0);
-                const uint32_t sfa = tmem + kExSfCol, sfb = sfa + 4 * W;
-                const uint32_t idesc = ex_idesc<FP4>(o.n);
-                if (it > 0) {
-                    ok = ex_wait(smem_u32(&s_tfree), (unsigned)(it - 1) & 1u, a.wait_ns, &s_abort);
-                    tc_fence_after();
+        // ---- products
+        bool ok = true;
+        const uint32_t sfa = tmem + kExSfCol, sfb = sfa + 4 * W;
+        for (int it = 0; ok && walk.ct < total; walk.next(), ++it) {
+            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
+            const uint32_t d = tmem + ((it & 1) ? kExBuf1 : 0);
+            const uint32_t idesc = ex_idesc<FP4>(o.n);
+            if (it > 0) {
+                ok = ex_wait(smem_u32(&s_tfree), (unsigned)(it - 1) & 1u, a.wait_ns, &s_abort);
+                tc_fence_after();
+            }
+            for (int ki = 0; ok && ki < a.KI; ++ki) {
+                if (!ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
+                    ok = false;
+                    break;
                 }
-                for (int ki = 0; ok && ki < a.KI; ++ki) {
-                    if (!ex_wait(smem_u32(&s_full[st]), ph, a.wait_ns, &s_abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t wa = base + (uint32_t)st * code_bytes, xa = wa + kExWBytes;
-                    const uint32_t sa = sf_base + (uint32_t)st * sf_bytes, sb = sa + W * 512;
+                tc_fence_after();
+                const uint32_t wa = base + (uint32_t)st * code_bytes;
+                const uint32_t sa = sf_base + (uint32_t)st * sf_bytes;
+                if (ex_elect()) {
+                    const unsigned long long da = ex_desc(kExDescCodes, wa), db = ex_desc(kExDescCodes, wa + kExWBytes);
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         ex_copy_sf(sfa + 4 * w, sa + 512 * w);
-                        for (int h = 0; h * 128 < o.n; ++h) ex_copy_sf(sfb + 4 * (w * H + h), sb + 512 * (w * H + h));
+                        ex_copy_sf(sfb + 4 * w * H, sa + 512 * (W + w * H));
+                        if (o.n > 128) ex_copy_sf(sfb + 4 * w * H + 4, sa + 512 * (W + w * H) + 512);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int w = FP4 ? j >> 1 : 0;
                         const uint32_t sel = FP4 ? (uint32_t)(j & 1) * 2 : (uint32_t)j;
-                        ex_mma<FP4>(d, ex_desc_sw128(wa + 32 * j), ex_desc_sw128(xa + 32 * j), idesc, sel, sfa + 4 * w,
-                                    sfb + 4 * w * H, ki > 0 || j > 0);
+                        ex_mma<FP4>(d, da + 2 * j, db + 2 * j, idesc, sel, sfa + 4 * w, sfb + 4 * w * H,
+                                    ki > 0 || j > 0);
                     }
-                    ex_commit(smem_u32(&s_empty[st]));
-                    if (++st == nst) st = 0, ph ^= 1u;
+                    ex_commit(empty0 + 8u * st);
+                    if (ki == a.KI - 1) ex_commit(smem_u32(&s_tfull[it & 1]));
                 }
-                if (ok) ex_commit(smem_u32(&s_tfull[it & 1]));
+                __syncwarp();
+                if (++st == nst) st = 0, ph ^= 1u;
             }
         }
-        __syncwarp();
     } else if (warp == 2) {
         // ---- the activations' scales, as [32 rows][4 groups of 32 rows] words
         bool ok = true;
-        constexpr int B = FP4 ? 2 : 4;  // stages read at a time: 16 bytes of each row
-        for (int tile = blockIdx.x; ok && tile < total; tile += step) {
-            const ExTile o = ex_tile(t, a.E, a.RT, tile);
+        constexpr int B = 4 / W;  // stages read at a time: 16 bytes of each row
+        for (; ok && walk.ct < total; walk.next()) {
+            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
             const uint8_t* row[8];
+            const int G = (o.n + 31) >> 5;
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
                 const int r = min(g * 32 + lane, o.rows - 1);
                 int64_t src = o.r0 + r;
-                if (OP == kExGateUp && a.gather) {
+                if (gather && g < G) {
                     int f = a.sorted[o.r0 + r];
                     if (f < 0 || f >= a.mk) f = 0;
                     src = f / a.topk;
                 }
                 row[g] = a.x_scale + src * a.lds;
             }
-            const int G = (o.n + 31) >> 5;
             for (int k0 = 0; ok && k0 < a.KI; k0 += B) {
-                uint32_t v[B * W][8];
+                uint4 v[8];
+                const int b = k0 * W * 4;  // first scale byte
 #pragma unroll
-                for (int i = 0; i < B * W; ++i) {
-                    const int b = (k0 * W + i) * 4;  // first scale byte
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        v[i][g] = 0u;
-                        if (g >= G) continue;
-                        if (a.sf_words) {
-                            if (b < a.kb) v[i][g] = __ldg(reinterpret_cast<const uint32_t*>(row[g] + b));
-                        } else {
-                            for (int u = 0; u < 4; ++u)
-                                if (b + u < a.kb) v[i][g] |= (uint32_t)__ldg(row[g] + b + u) << (8 * u);
+                for (int g = 0; g < 8; ++g) {
+                    v[g] = make_uint4(0u, 0u, 0u, 0u);
+                    if (g >= G) continue;
+                    if (a.sf_vec == 16) {
+                        v[g] = __ldg(reinterpret_cast<const uint4*>(row[g] + b));
+                    } else if (a.sf_vec == 8) {
+                        const uint2 lo = __ldg(reinterpret_cast<const uint2*>(row[g] + b));
+                        v[g].x = lo.x;
+                        v[g].y = lo.y;
+                        if (b + 8 < a.kb) {
+                            const uint2 hi = __ldg(reinterpret_cast<const uint2*>(row[g] + b + 8));
+                            v[g].z = hi.x;
+                            v[g].w = hi.y;
                         }
+                    } else {
+                        uint32_t x[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int at = b + 4 * i;
+                            if (a.sf_vec == 4) {
+                                if (at < a.kb) x[i] = __ldg(reinterpret_cast<const uint32_t*>(row[g] + at));
+                            } else {
+                                for (int u = 0; u < 4; ++u)
+                                    if (at + u < a.kb) x[i] |= (uint32_t)__ldg(row[g] + at + u) << (8 * u);
+                            }
+                        }
+                        v[g] = make_uint4(x[0], x[1], x[2], x[3]);
                     }
                 }
 #pragma unroll
                 for (int s = 0; s < B; ++s) {
                     if (k0 + s >= a.KI) break;
-                    if (!__all_sync(kFull, ex_wait(smem_u32(&s_empty[st]), ph ^ 1u, a.wait_ns, &s_abort))) {
+                    if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t sb = sf_base + (uint32_t)st * sf_bytes + W * 512;
+                    const uint32_t sb = sf_base + (uint32_t)st * sf_bytes + W * 512 + 16u * lane;
 #pragma unroll
                     for (int w = 0; w < W; ++w)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (h < H)
+                        for (int h = 0; h < 2; ++h) {
+                            const int i = s * W + w;
+                            auto word = [i](uint4 q) { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; };
+                            if (h * 128 < o.n)
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                                 sb + 512u * (uint32_t)(w * H + h) + 16u * lane),
-                                             "r"(v[s * W + w][4 * h]), "r"(v[s * W + w][4 * h + 1]),
-                                             "r"(v[s * W + w][4 * h + 2]), "r"(v[s * W + w][4 * h + 3])
+                                                 sb + 512u * (uint32_t)(w * H + h)),
+                                             "r"(word(v[4 * h])), "r"(word(v[4 * h + 1])), "r"(word(v[4 * h + 2])),
+                                             "r"(word(v[4 * h + 3]))
                                              : "memory");
+                        }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_full[st]));
+                    if (lane == 0) mbar_arrive(full0 + 8u * st);
                     if (++st == nst) st = 0, ph ^= 1u;
                 }
             }
         }
-    } else if (warp >= 4) {
-        // ---- accumulator -> outputs
-        const int wq = warp & 3, et = tid - 128;
+    } else if (warp == 3) {
+        // ---- codes of rows in token order: lane i gathers rows 4 i .. 4 i + 3 (and 128 further on)
+        bool ok = gather;
+        for (; ok && walk.ct < total; walk.next()) {
+            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
+            int tok[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = (lane + (i >> 2) * 32) * 4 + (i & 3);
+                int f = r < o.rows ? a.sorted[o.r0 + r] : 0;
+                if (f < 0 || f >= a.mk) f = 0;  // a padding position: any row, its column is not used
+                tok[i] = f / a.topk;
+            }
+            for (int ki = 0; ki < a.KI; ++ki) {
+                if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = full0 + 8u * st, xsm = base + (uint32_t)st * code_bytes + kExWBytes;
+                if (ex_elect()) mbar_expect_tx(full, (unsigned)(o.n * 128));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int g = lane + i * 32;
+                    if (g * 4 < o.n)
+                        tma_gather4(xsm + (uint32_t)g * 512u, &a.tm_x, ki * 128, tok[4 * i], tok[4 * i + 1],
+                                    tok[4 * i + 2], tok[4 * i + 3], full);
+                }
+                __syncwarp();
+                if (++st == nst) st = 0, ph ^= 1u;
+            }
+        }
+    } else {
+        // ---- accumulator -> outputs: warps 4-7 and 8-11 take alternate chunks of 16 columns
+        const int wq = warp & 3, grp = (warp >> 2) - 1, et = tid - 128, gt = et & 127;
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-        int it = 0;
-        for (int tile = blockIdx.x; tile < total; tile += step, ++it) {
-            const ExTile o = ex_tile(t, a.E, a.RT, tile);
+        unsigned turn = 0;  // staging buffer of the group
+        for (int it = 0; walk.ct < total; walk.next(), ++it) {
+            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
             int* f = s_f[it & 1];
-            if (OP != kExGemm)
-                for (int c = et; c < o.n; c += 128) f[c] = c < o.rows ? a.sorted[o.r0 + c] : a.mk;
+            if (OP != kExGemm && et < o.n) f[et] = et < o.rows ? a.sorted[o.r0 + et] : a.mk;
             const bool ok = ex_wait(smem_u32(&s_tfull[it & 1]), (unsigned)(it >> 1) & 1u, a.wait_ns, &s_abort);
-            if (!ex_epi_sync(ok)) break;
+            if (!ex_sync(1, 256, ok)) break;
             tc_fence_after();
             const uint32_t d = tmem + lanes + ((it & 1) ? kExBuf1 : 0);
             const int nch = o.n >> 4;
             // the shared columns first: the chunks after which the next tile may start
-            const bool down_first = !(it & 1) && o.n > kExBuf1;
-            const int need = down_first ? nch - kExBuf1 / 16 : (it & 1) ? min(2, nch) : 0;
-            if (need == 0 && lane == 0) mbar_arrive(smem_u32(&s_tfree));
-            for (int i = 0; i < nch; ++i) {
-                const int ch = down_first ? nch - 1 - i : i, c0 = ch * 16;
+            const bool from_top = !(it & 1) && o.n > kExBuf1;
+            const int need = from_top ? nch - kExBuf1 / 16 : (it & 1) ? min(2, nch) : 0;
+            if (need <= grp && lane == 0) mbar_arrive(smem_u32(&s_tfree));
+            const int r = o.rt * 128 + wq * 32 + lane;
+            for (int i = grp; i < nch; i += 2) {
+                const int c0 = (from_top ? nch - 1 - i : i) * 16;
                 uint32_t v[16];
                 ex_ld16(v, d + (uint32_t)c0);
-                if (i + 1 == need) {
+                if (i < need && i + 2 >= need) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&s_tfree));
                 }
                 if (OP == kExGemm) {
-                    const int r = o.rt * 128 + wq * 32 + lane;
-                    if (r < a.R) {
+                    const int64_t at = (int64_t)(o.r0 + c0) * a.ldo + r;
+                    const int cols = r < a.R ? o.rows - c0 : 0;
+                    if (a.out_fmt == 3) {
+                        float* p = static_cast<float*>(a.out) + at;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c0 + j < o.rows) {
-                                const int64_t at = (int64_t)(o.r0 + c0 + j) * a.ldo + r;
-                                if (a.out_fmt == 3) static_cast<float*>(a.out)[at] = __uint_as_float(v[j]);
-                                else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(__uint_as_float(v[j]));
-                            }
+                        for (int j = 0; j < 16; ++j, p += a.ldo)
+                            if (j < cols) *p = __uint_as_float(v[j]);
+                    } else {
+                        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + at;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j, p += a.ldo)
+                            if (j < cols) *p = __float2bfloat16_rn(__uint_as_float(v[j]));
                     }
                 } else if (OP == kExDown) {
-                    const int r = o.rt * 128 + wq * 32 + lane;
+                    float* y = a.y + r;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int as = f[c0 + j];
-                        if (r < a.R && as >= 0 && as < a.mk) a.y[(int64_t)as * a.R + r] = __uint_as_float(v[j]);
+                    for (int j4 = 0; j4 < 4; ++j4) {
+                        const int4 as = *reinterpret_cast<const int4*>(f + c0 + 4 * j4);
+                        const int s4[4] = {as.x, as.y, as.z, as.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if ((unsigned)s4[j] < (unsigned)a.mk && r < a.R)
+                                y[(int64_t)s4[j] * a.R] = __uint_as_float(v[4 * j4 + j]);
                     }
                 } else {
                     // lanes 0-15 hold gate rows and lanes 16-31 the up rows of
                     // the same features: lanes 0-15 take the even columns,
                     // lanes 16-31 the odd ones
-                    unsigned char* stage = s_act + (i & 1) * 16 * kExStagePitch;
+                    unsigned char* stage = s_act + (grp * 2 + (turn++ & 1)) * 16 * kExStagePitch;
                     const bool hi = lane >= 16;
+                    unsigned char* put0 = stage + (hi ? kExStagePitch : 0) + (wq * 16 + (lane & 15)) * 2;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float mine = __uint_as_float(hi ? v[2 * j + 1] : v[2 * j]);
                         const float other = __shfl_xor_sync(kFull, __uint_as_float(hi ? v[2 * j] : v[2 * j + 1]), 16);
                         const float gv = hi ? other : mine, uv = hi ? mine : other;
-                        const float s = gv / (1.0f + expf(-gv)) * uv;
-                        *reinterpret_cast<__nv_bfloat16*>(stage + (2 * j + (hi ? 1 : 0)) * kExStagePitch +
-                                                          (wq * 16 + (lane & 15)) * 2) = __float2bfloat16_rn(s);
+                        // (e^-g = inf gives 0; the quotient is good to 2 ulps)
+                        const float s = __fdividef(gv, 1.0f + expf(-gv)) * uv;
+                        *reinterpret_cast<__nv_bfloat16*>(put0 + 2 * j * kExStagePitch) = __float2bfloat16_rn(s);
                     }
-                    ex_epi_sync(true);
+                    ex_sync(2 + grp, 128, true);
                     // 8 threads per column, 8 features each
-                    const int c = et >> 3, seg = et & 7, i0 = o.rt * 64 + seg * 8;
+                    const int c = gt >> 3, seg = gt & 7, i0 = o.rt * 64 + seg * 8;
                     const uint4 q = *reinterpret_cast<const uint4*>(stage + c * kExStagePitch + seg * 16);
-                    const int as = f[c0 + c], I = a.R >> 1;
-                    const bool put = as >= 0 && as < a.mk && i0 < I;
+                    const int I = a.R >> 1;
+                    const bool put = (unsigned)f[c0 + c] < (unsigned)a.mk && i0 < I;
                     const int64_t p = o.r0 + c0 + c;
                     if (a.out_fmt == 0) {
                         if (put) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + p * I + i0) = q;
@@ -572,9 +684,10 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
     }
     __syncthreads();
     if (warp == 1) {
-        if (s_abort && lane == 0) {
+        if (s_abort) {
             // products already issued are waited for before their tensor memory goes
-            ex_commit(smem_u32(&s_drain));
+            if (ex_elect()) ex_commit(smem_u32(&s_drain));
+            __syncwarp();
             const unsigned long long t0 = global_ns();
             while (!mbar_try_wait(smem_u32(&s_drain), 0) && global_ns() - t0 < a.wait_ns) {
             }

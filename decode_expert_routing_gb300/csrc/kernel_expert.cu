@@ -148,8 +148,10 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
         }
         const cuuint64_t dims[2] = {kbytes, (cuuint64_t)c.x_rows};
         const cuuint64_t strides[1] = {(cuuint64_t)c.ldx};
-        const cuuint32_t box[2] = {128, c.gather ? 1u : 16u};
-        if (!encode(&a.tm_x, c.x, 2, dims, strides, box)) return MR_ERR_UNSUPPORTED;
+        const cuuint32_t box[2] = {128, c.gather ? 1u : 16u}, box64[2] = {128, 64};
+        if (!encode(&a.tm_x, c.x, 2, dims, strides, box) ||
+            (!c.gather && !encode(&a.tm_x64, c.x, 2, dims, strides, box64)))
+            return MR_ERR_UNSUPPORTED;
     }
     a.w_scale = c.w_scale;
     a.x_scale = c.x_scale;
@@ -172,7 +174,13 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     a.nblk = c.nblk;
     a.block = c.block;
     a.gather = c.gather;
-    a.sf_words = (K % 128 == 0 && c.lds % 4 == 0 && (reinterpret_cast<uintptr_t>(c.x_scale) & 3) == 0) ? 1 : 0;
+    a.sf_vec = 1;
+    for (int v = 4; v <= 16; v *= 2)  // rows whose bytes end on the boundary too: no read past a row
+        if (a.kb % v == 0 && c.lds % v == 0 && reinterpret_cast<uintptr_t>(c.x_scale) % v == 0) a.sf_vec = v;
+    {  // column tiles: one per expert with rows, and one for every further 256 rows
+        const int64_t mk = (int64_t)c.M * c.topk, most = (mk < c.E ? mk : c.E) + mk / kExMaxN + 1;
+        a.list_cap = most <= kExListMax ? (int)most : 0;
+    }
     a.out_fmt = c.out_fmt;
     a.flags = launch_flags();
     const int grid = sms;
