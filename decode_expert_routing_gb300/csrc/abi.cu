@@ -757,7 +757,6 @@ int mr_moe_down(const mr_moe_down_params* p, void* stream) {
     c.topk_weights = p->topk_weights;
     c.add = p->add;
     c.out = p->out;
-    c.y = reinterpret_cast<float*>(static_cast<char*>(p->scratch) + mr::kWorkOffset + mr::expert_part_bytes(mk));
     c.scratch = p->scratch;
     return run_expert(c, stream);
 }

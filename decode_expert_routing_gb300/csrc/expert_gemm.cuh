@@ -13,11 +13,17 @@
 // column tile times 128 weight rows, and its K range is cut into stages of
 // 128 bytes of codes a row (128 E4M3 or 256 E2M1 elements).  One CTA per SM
 // walks the tiles.  Warp 0 copies the codes (tensor maps, 128-byte swizzle) and
-// the weights' scales (laid out once, see mx_pack_kernel), warp 3 the codes of
-// rows in token order (four-row gathers), warp 2 puts the activations' scales
-// into the weights' scale layout, warp 1 copies scales to tensor memory and
-// issues the products, and warps 4-11 read the accumulator back while the
-// next tile is computed into the other one.
+// the weights' scales (laid out once, see mx_pack_kernel), two warps the codes
+// of rows in token order, two the activations' scales (into the weights' scale
+// layout), warp 1 copies scales to tensor memory and issues the products, and
+// warps 4-11 read the accumulator back while the next tile is computed into
+// the other one.
+//
+// PAIR: two CTAs of a cluster form tiles of 256 weight rows, each with its own
+// 128 and half of the activation rows (cta_group::2): a stage is 16 KB + 64 n
+// bytes instead of 16 KB + 128 n.  Loads from L2 (about 16 TB/s over all SMs)
+// bound tiles of many rows, so it takes them: gate/up of 32768 rows 302 -> 275
+// us, the E2M1 product 4096 x 6144 x 6144 62 -> 56 us.
 //
 // The loops of warps 0 and 1 are uniform over the warp (waits end in a vote,
 // one elected lane issues): as code of a single lane, the copies and products
@@ -33,7 +39,8 @@
 
 namespace mr {
 
-constexpr int kExThreads = 384;          // 4 warps of copies and products, 8 that read back
+// Warps: 0 copies, 1 products, 2-3 scales, 4-11 read back, and for gate/up 12-13 gather.
+__host__ __device__ constexpr int ex_threads(int op) { return op == 1 ? 448 : 384; }
 constexpr int kExMaxStages = 12;
 constexpr int kExMaxN = 256;             // activation rows of a tile
 constexpr int kExWBytes = 128 * 128;     // one stage of weight codes
@@ -50,19 +57,20 @@ enum { kExGemm = 0, kExGateUp = 1, kExDown = 2 };
 
 struct ExpertArgs {
     CUtensorMap tm_w;        // weight codes, box of 128 rows x 128 bytes
-    CUtensorMap tm_x;        // activation codes, box of 16 rows (gather: 1 row) x 128 bytes
+    CUtensorMap tm_x;        // activation codes, box of 16 rows x 128 bytes (not with gather)
     CUtensorMap tm_x64;      // the same in boxes of 64 rows
     const uint8_t* w_scale;  // packed: [E][row tile][stage][512 * words]
     const uint8_t* x_scale;  // [rows][lds] bytes
     int64_t lds;
     const int32_t* sorted;   // [cap] assignment of a sorted position
     const int32_t* experts;  // [nblk] expert of a block
-    void* out;               // bf16 (or fp32) rows, or E4M3 / E2M1 codes
+    void* out;               // bf16 (or fp32) rows, or E4M3 / E2M1 codes; kExDown: bf16 [assignments][R]
     uint8_t* out_scale;
-    float* y;                // kExDown: [assignments][R] fp32
     int64_t ldo;             // elements between output rows (kExGemm)
+    const uint8_t* x;        // activation codes (rows in token order)
+    int64_t ldx;
     unsigned long long wait_ns;
-    int E, R, RT, KI, kb;    // weight rows, row tiles, stages, scale bytes per row
+    int E, R, RT, KI, kb, kbytes;  // weight rows, row tiles, stages, scale and code bytes per row
     int M, topk, mk, nblk, block;
     int gather;              // x rows in token order
     int sf_vec;              // bytes that the scale rows can be read in: 16, 8, 4 or 1
@@ -78,7 +86,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, unsigned parity) {
     unsigned ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// The same without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -125,39 +145,56 @@ __device__ __forceinline__ unsigned long long ex_desc(unsigned long long kind, u
 }
 // 32 rows of 16 bytes to four tensor-memory columns, repeated in each of the
 // four 32-lane quarters: lane l, column c holds the four scales of row 32 c + l.
+// (PAIR: in both CTAs, each from its own shared memory.)
+template <bool PAIR>
 __device__ __forceinline__ void ex_copy_sf(uint32_t tmem, uint32_t addr) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(ex_desc(kExDescSf, addr)) : "memory");
+    if (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(ex_desc(kExDescSf, addr))
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(ex_desc(kExDescSf, addr))
+                     : "memory");
 }
 // Instruction descriptor without the scale selectors: E4M3 (format 0 of
 // kind::mxf8f6f4) or E2M1 (format 1 of kind::mxf4), both operands K-major,
-// E8M0 scales, 128 rows, n columns.
-template <bool FP4>
+// E8M0 scales, 128 rows (PAIR: 256, 128 in each CTA), n columns.
+template <bool FP4, bool PAIR>
 __device__ __forceinline__ uint32_t ex_idesc(int n) {
-    return ((FP4 ? 1u : 0u) << 7) | ((FP4 ? 1u : 0u) << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (1u << 27);
+    return ((FP4 ? 1u : 0u) << 7) | ((FP4 ? 1u : 0u) << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+           ((PAIR ? 2u : 1u) << 27);
 }
 // One k-step (32 E4M3 or 64 E2M1 elements); sel = index of its first scale in
 // the 32-bit scale words of both operands.
-template <bool FP4>
+#define EX_MMA(group, kind)                                                                                       \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                \
+                 "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), \
+                 "l"(a), "l"(b), "r"(id), "r"(sfa), "r"(sfb), "r"((uint32_t)acc)                                  \
+                 : "memory")
+template <bool FP4, bool PAIR>
 __device__ __forceinline__ void ex_mma(uint32_t d, unsigned long long a, unsigned long long b, uint32_t idesc,
                                        uint32_t sel, uint32_t sfa, uint32_t sfb, bool acc) {
     const uint32_t id = idesc | (sel << 4) | (sel << 29);
-    if (FP4)
+    if (FP4 && PAIR) EX_MMA("2", "mxf4.block_scale.scale_vec::2X");
+    else if (FP4) EX_MMA("1", "mxf4.block_scale.scale_vec::2X");
+    else if (PAIR) EX_MMA("2", "mxf8f6f4.block_scale.scale_vec::1X");
+    else EX_MMA("1", "mxf8f6f4.block_scale.scale_vec::1X");
+}
+#undef EX_MMA
+// An arrival (PAIR: in both CTAs, at the same place) when the products issued so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void ex_commit(uint32_t bar) {
+    if (PAIR)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-                d),
-            "l"(a), "l"(b), "r"(id), "r"(sfa), "r"(sfb), "r"((uint32_t)acc)
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                bar),
+            "h"((unsigned short)3)
             : "memory");
     else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], "
-            "p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(id), "r"(sfa), "r"(sfb), "r"((uint32_t)acc)
-            : "memory");
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                     : "memory");
 }
-__device__ __forceinline__ void ex_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void ex_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // 16 accumulator columns of this warp's 32 lanes.
 __device__ __forceinline__ void ex_ld16(uint32_t (&v)[16], uint32_t addr) {
@@ -183,14 +220,9 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* map, int x
         "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
         : "memory");
 }
-// Four rows of a tensor map (box of one row), 128 bytes each.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* map, int x, int r0, int r1, int r2, int r3,
-                                            uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-        "%3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-        : "memory");
+// 16 bytes of global memory (bytes of them, 0 or 16; the rest zeros) into shared memory.
+__device__ __forceinline__ void ex_cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // Barrier id of threads threads (whole warps); true when ok holds in all of them.
 __device__ __forceinline__ bool ex_sync(int id, int threads, bool ok) {
@@ -216,12 +248,17 @@ struct ExTile {
     int e, rt, r0, rows, n;  // expert, row tile, first position, real rows, accumulator columns
 };
 __device__ __forceinline__ int ex_ncol(int rows) { return (rows + kExMaxN - 1) / kExMaxN; }
-// Rows of each column tile of an expert (equal shares, a multiple of 16):
-// at most 256, and every tile has at least one row.
-__device__ __forceinline__ int ex_share(int rows, int nct) { return ((rows + nct - 1) / nct + 15) & ~15; }
+// Rows of each column tile of an expert (equal shares, a multiple of 16): at
+// most 256, and every tile has at least one row.
+// (a pair's columns are split between its CTAs: a multiple of 32)
+template <bool PAIR>
+__device__ __forceinline__ int ex_round(int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; }
+template <bool PAIR>
+__device__ __forceinline__ int ex_share(int rows, int nct) { return ex_round<PAIR>((rows + nct - 1) / nct); }
 
 // Column tile ct of the list, or (a list that does not fit: more than some
 // hundred thousand assignments) by a search over the experts.
+template <bool PAIR>
 __device__ __forceinline__ ExTile ex_tile(const ExTables& t, int E, int ct, int rt, bool listed) {
     ExTile o;
     o.rt = rt;
@@ -240,23 +277,23 @@ __device__ __forceinline__ ExTile ex_tile(const ExTables& t, int E, int ct, int 
         }
         o.e = lo;
         const int rows = t.rows[lo], nct = t.pre[lo + 1] - t.pre[lo], i = ct - t.pre[lo];
-        const int per = ex_share(rows, nct);
+        const int per = ex_share<PAIR>(rows, nct);
         o.r0 = __shfl_sync(kFull, t.first[lo] + i * per, 0);
         o.rows = __shfl_sync(kFull, min(per, rows - i * per), 0);
     }
-    o.n = (o.rows + 15) & ~15;
+    o.n = ex_round<PAIR>(o.rows);
     return o;
 }
 
-// The tiles of this CTA, every gridDim.x-th: row tiles fastest, so that the
-// CTAs at work share few activation rows and each weight is read once.
+// The tiles of this CTA (or pair), every nth of n, row tiles fastest: the CTAs
+// at work share few activation rows and each weight is read once.
 struct ExWalk {
     int ct, rt, dct, drt, RT;
-    __device__ __forceinline__ ExWalk(int rt_count) : RT(rt_count) {
-        ct = (int)blockIdx.x / RT;
-        rt = (int)blockIdx.x - ct * RT;
-        dct = (int)gridDim.x / RT;
-        drt = (int)gridDim.x - dct * RT;
+    __device__ __forceinline__ ExWalk(int me, int n, int row_tiles) : RT(row_tiles) {
+        ct = me / RT;
+        rt = me - ct * RT;
+        dct = n / RT;
+        drt = n - dct * RT;
     }
     __device__ __forceinline__ void next() {
         ct += dct;
@@ -265,39 +302,55 @@ struct ExWalk {
     }
 };
 
-template <bool FP4, int OP>
-__global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_constant__ ExpertArgs a) {
+template <bool FP4, int OP, bool PAIR>
+__global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_constant__ ExpertArgs a) {
+    constexpr int kExThreads = ex_threads(OP);
     constexpr int W = FP4 ? 2 : 1;  // scale words (of 4 bytes) per row and stage
     extern __shared__ __align__(16) unsigned char dsm[];
     __shared__ __align__(8) unsigned long long s_full[kExMaxStages], s_empty[kExMaxStages], s_tfull[2], s_tfree, s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_total, s_nmax, s_warp[kExThreads / 32];
     __shared__ __align__(16) int s_f[2][OP == kExGemm ? 4 : kExMaxN];
+    __shared__ __align__(8) unsigned long long s_land[2][OP == kExGateUp ? kExMaxStages : 1];  // gathered codes are there
+    __shared__ int s_tok[2][OP == kExGateUp ? kExMaxN / 2 : 1];  // tokens of the rows that a warp gathers
     __shared__ __align__(16) unsigned char s_act[OP == kExGateUp ? 4 * 16 * kExStagePitch : 16];
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
     const bool gather = OP == kExGateUp && a.gather;
+    const int rank = PAIR ? (int)cluster_rank() : 0;
 
     // ---- set-up that reads nothing of the kernel before
     if (tid == 0) {
         for (int s = 0; s < kExMaxStages; ++s) {
-            mbar_init(smem_u32(&s_full[s]), gather ? 3 : 2);
+            mbar_init(smem_u32(&s_full[s]), (gather ? 5 : 3) + (PAIR && rank == 0 ? 1 : 0));  // (one from the peer)
             mbar_init(smem_u32(&s_empty[s]), 1);
+            if (OP == kExGateUp) {
+                mbar_init(smem_u32(&s_land[0][s]), 32);
+                mbar_init(smem_u32(&s_land[1][s]), 32);
+            }
         }
         mbar_init(smem_u32(&s_tfull[0]), 1);
         mbar_init(smem_u32(&s_tfull[1]), 1);
-        mbar_init(smem_u32(&s_tfree), 8);
+        mbar_init(smem_u32(&s_tfree), PAIR ? 16 : 8);
         mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_abort = 0;
         s_nmax = 16;
         tma_prefetch_map(&a.tm_w);
-        tma_prefetch_map(&a.tm_x);
-        if (!gather) tma_prefetch_map(&a.tm_x64);
+        if (!gather) {
+            tma_prefetch_map(&a.tm_x);
+            tma_prefetch_map(&a.tm_x64);
+        }
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     ExTables t;
     t.list = reinterpret_cast<int2*>(dsm);
@@ -351,7 +404,7 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
                 if (lane >= o) v += u;
             }
             if (lane == 31) s_warp[warp] = v;
-            if (c > 0) atomicMax(&s_nmax, ex_share(rows, c));
+            if (c > 0) atomicMax(&s_nmax, ex_share<PAIR>(rows, c));
             __syncthreads();
             int before = run;
             for (int w = 0; w < kExThreads / 32; ++w) {
@@ -362,7 +415,7 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
             if (e < a.E) {
                 t.pre[e] = before;
                 for (int i = 0; i < c && before + i < a.list_cap; ++i) {
-                    const int per = ex_share(rows, c);
+                    const int per = ex_share<PAIR>(rows, c);
                     t.list[before + i] = make_int2(t.first[e] + i * per, (e << 16) | min(per, rows - i * per));
                 }
             }
@@ -374,7 +427,8 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (PAIR) ex_cluster_sync();
+    else __syncthreads();
     tc_fence_after();
 
     const int total = __shfl_sync(kFull, s_total, 0), xrows = __shfl_sync(kFull, s_nmax, 0);
@@ -384,22 +438,26 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
     // stages of weight and activation codes, then their scale factors
     const uint32_t dyn = smem_u32(dsm);
     const uint32_t base = (dyn + (uint32_t)a.list_cap * 8u + (uint32_t)(3 * a.E + 1) * 4u + 1023u) & ~1023u;
-    const uint32_t code_bytes = (uint32_t)(kExWBytes + xrows * 128), sf_bytes = (uint32_t)(W * 512 * (1 + H));
+    const uint32_t code_bytes = (uint32_t)(kExWBytes + xrows * (PAIR ? 64 : 128)), sf_bytes = (uint32_t)(W * 512 * (1 + H));
     const int nst = min(kExMaxStages, (int)((dyn + (uint32_t)kExSmemDyn - base) / (code_bytes + sf_bytes)));
     const uint32_t sf_base = base + (uint32_t)nst * code_bytes;
     const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
     int st = 0;       // stage of the ring
     unsigned ph = 0;  // its phase
-    ExWalk walk(a.RT);
+    // a pair takes two row tiles at a time, one in each CTA
+    ExWalk walk((int)blockIdx.x >> (PAIR ? 1 : 0), (int)gridDim.x >> (PAIR ? 1 : 0), PAIR ? (a.RT + 1) >> 1 : a.RT);
+#define EX_TILE ex_tile<PAIR>(t, a.E, walk.ct, PAIR ? walk.rt * 2 + rank : walk.rt, listed)
 
     if (warp == 0) {
         // ---- codes, and the weights' scales
         int issued = 0;
         bool ok = true;
         for (; ok && walk.ct < total; walk.next()) {
-            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
-            const uint8_t* ws = a.w_scale + ((int64_t)o.e * a.RT + o.rt) * a.KI * (W * 512);
-            const unsigned tx = (unsigned)(kExWBytes + W * 512 + (gather ? 0 : o.n * 128));
+            const ExTile o = EX_TILE;
+            // (a pair's second row tile may lie past the weight: its codes read as zeros, and no scale is read there)
+            const uint8_t* ws = a.w_scale + ((int64_t)o.e * a.RT + min(o.rt, a.RT - 1)) * a.KI * (W * 512);
+            const int nx = PAIR ? o.n >> 1 : o.n, rx = o.r0 + rank * nx;  // this CTA's activation rows
+            const unsigned tx = (unsigned)(kExWBytes + W * 512 + (gather ? 0 : nx * 128));
             for (int ki = 0; ki < a.KI; ++ki) {
                 if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
                     ok = false;
@@ -413,10 +471,10 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
                     bulk_load(sf_base + (uint32_t)st * sf_bytes, ws, W * 512, full);
                     if (!gather) {
                         int r = 0;
-                        for (; r + 64 <= o.n; r += 64)
-                            tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x64, ki * 128, o.r0 + r, full);
-                        for (; r < o.n; r += 16)
-                            tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x, ki * 128, o.r0 + r, full);
+                        for (; r + 64 <= nx; r += 64)
+                            tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x64, ki * 128, rx + r, full);
+                        for (; r < nx; r += 16)
+                            tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x, ki * 128, rx + r, full);
                     }
                 }
                 __syncwarp();
@@ -434,14 +492,29 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
                 }
             }
         }
+    } else if (warp == 1 && PAIR && rank == 1) {
+        // ---- a pair's products are issued by its first CTA: told when this CTA's operands are in place
+        bool ok = true;
+        const uint32_t peer = map_rank(full0, 0);
+        for (; ok && walk.ct < total; walk.next()) {
+            for (int ki = 0; ki < a.KI; ++ki) {
+                if (!ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
+                    ok = false;
+                    break;
+                }
+                if (ex_elect()) mbar_arrive_remote(peer + 8u * st);  // (after the wait, whose outcome it passes on)
+                __syncwarp();
+                if (++st == nst) st = 0, ph ^= 1u;
+            }
+        }
     } else if (warp == 1) {
         // ---- products
         bool ok = true;
         const uint32_t sfa = tmem + kExSfCol, sfb = sfa + 4 * W;
         for (int it = 0; ok && walk.ct < total; walk.next(), ++it) {
-            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
+            const ExTile o = EX_TILE;
             const uint32_t d = tmem + ((it & 1) ? kExBuf1 : 0);
-            const uint32_t idesc = ex_idesc<FP4>(o.n);
+            const uint32_t idesc = ex_idesc<FP4, PAIR>(o.n);
             if (it > 0) {
                 ok = ex_wait(smem_u32(&s_tfree), (unsigned)(it - 1) & 1u, a.wait_ns, &s_abort);
                 tc_fence_after();
@@ -458,35 +531,37 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
                     const unsigned long long da = ex_desc(kExDescCodes, wa), db = ex_desc(kExDescCodes, wa + kExWBytes);
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
-                        ex_copy_sf(sfa + 4 * w, sa + 512 * w);
-                        ex_copy_sf(sfb + 4 * w * H, sa + 512 * (W + w * H));
-                        if (o.n > 128) ex_copy_sf(sfb + 4 * w * H + 4, sa + 512 * (W + w * H) + 512);
+                        ex_copy_sf<PAIR>(sfa + 4 * w, sa + 512 * w);
+                        ex_copy_sf<PAIR>(sfb + 4 * w * H, sa + 512 * (W + w * H));
+                        if (o.n > 128) ex_copy_sf<PAIR>(sfb + 4 * w * H + 4, sa + 512 * (W + w * H) + 512);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int w = FP4 ? j >> 1 : 0;
                         const uint32_t sel = FP4 ? (uint32_t)(j & 1) * 2 : (uint32_t)j;
-                        ex_mma<FP4>(d, da + 2 * j, db + 2 * j, idesc, sel, sfa + 4 * w, sfb + 4 * w * H,
+                        ex_mma<FP4, PAIR>(d, da + 2 * j, db + 2 * j, idesc, sel, sfa + 4 * w, sfb + 4 * w * H,
                                     ki > 0 || j > 0);
                     }
-                    ex_commit(empty0 + 8u * st);
-                    if (ki == a.KI - 1) ex_commit(smem_u32(&s_tfull[it & 1]));
+                    ex_commit<PAIR>(empty0 + 8u * st);
+                    if (ki == a.KI - 1) ex_commit<PAIR>(smem_u32(&s_tfull[it & 1]));
                 }
                 __syncwarp();
                 if (++st == nst) st = 0, ph ^= 1u;
             }
         }
-    } else if (warp == 2) {
-        // ---- the activations' scales, as [32 rows][4 groups of 32 rows] words
+    } else if (warp == 2 || warp == 3) {
+        // ---- the activations' scales, as [32 rows][4 groups of 32 rows] words: one warp for rows 0-127 of the
+        // tile, one for rows 128-255.  16 bytes of each row are read at a time (B stages), one time ahead.
         bool ok = true;
-        constexpr int B = 4 / W;  // stages read at a time: 16 bytes of each row
+        constexpr int B = 4 / W;
+        const int half = warp == 2 ? 0 : 1;
         for (; ok && walk.ct < total; walk.next()) {
-            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
-            const uint8_t* row[8];
-            const int G = (o.n + 31) >> 5;
+            const ExTile o = EX_TILE;
+            const uint8_t* row[4];
+            const int G = max(0, min(4, ((o.n + 31) >> 5) - 4 * half));  // groups of 32 rows that are this warp's
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const int r = min(g * 32 + lane, o.rows - 1);
+            for (int g = 0; g < 4; ++g) {
+                const int r = min((half * 4 + g) * 32 + lane, o.rows - 1);
                 int64_t src = o.r0 + r;
                 if (gather && g < G) {
                     int f = a.sorted[o.r0 + r];
@@ -495,24 +570,18 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
                 }
                 row[g] = a.x_scale + src * a.lds;
             }
-            for (int k0 = 0; ok && k0 < a.KI; k0 += B) {
-                uint4 v[8];
-                const int b = k0 * W * 4;  // first scale byte
+            auto load = [&](uint4 (&v)[4], int b) {  // b: first scale byte
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
+                for (int g = 0; g < 4; ++g) {
                     v[g] = make_uint4(0u, 0u, 0u, 0u);
                     if (g >= G) continue;
                     if (a.sf_vec == 16) {
-                        v[g] = __ldg(reinterpret_cast<const uint4*>(row[g] + b));
+                        if (b < a.kb) v[g] = __ldg(reinterpret_cast<const uint4*>(row[g] + b));
                     } else if (a.sf_vec == 8) {
-                        const uint2 lo = __ldg(reinterpret_cast<const uint2*>(row[g] + b));
-                        v[g].x = lo.x;
-                        v[g].y = lo.y;
-                        if (b + 8 < a.kb) {
-                            const uint2 hi = __ldg(reinterpret_cast<const uint2*>(row[g] + b + 8));
-                            v[g].z = hi.x;
-                            v[g].w = hi.y;
-                        }
+                        uint2 lo = make_uint2(0u, 0u), hi = make_uint2(0u, 0u);
+                        if (b < a.kb) lo = __ldg(reinterpret_cast<const uint2*>(row[g] + b));
+                        if (b + 8 < a.kb) hi = __ldg(reinterpret_cast<const uint2*>(row[g] + b + 8));
+                        v[g] = make_uint4(lo.x, lo.y, hi.x, hi.y);
                     } else {
                         uint32_t x[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -528,73 +597,127 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
                         v[g] = make_uint4(x[0], x[1], x[2], x[3]);
                     }
                 }
+            };
+            auto store = [&](const uint4 (&v)[4], int k0) {
 #pragma unroll
                 for (int s = 0; s < B; ++s) {
-                    if (k0 + s >= a.KI) break;
-                    if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sb = sf_base + (uint32_t)st * sf_bytes + W * 512 + 16u * lane;
+                    if (k0 + s >= a.KI) return true;
+                    if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) return false;
+                    const uint32_t sb = sf_base + (uint32_t)st * sf_bytes + (W + half) * 512 + 16u * lane;
+                    if (G > 0) {
 #pragma unroll
-                    for (int w = 0; w < W; ++w)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int w = 0; w < W; ++w) {
                             const int i = s * W + w;
                             auto word = [i](uint4 q) { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; };
-                            if (h * 128 < o.n)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                                 sb + 512u * (uint32_t)(w * H + h)),
-                                             "r"(word(v[4 * h])), "r"(word(v[4 * h + 1])), "r"(word(v[4 * h + 2])),
-                                             "r"(word(v[4 * h + 3]))
-                                             : "memory");
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sb + 512u * (uint32_t)(w * H)),
+                                         "r"(word(v[0])), "r"(word(v[1])), "r"(word(v[2])), "r"(word(v[3]))
+                                         : "memory");
                         }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full0 + 8u * st);
                     if (++st == nst) st = 0, ph ^= 1u;
                 }
+                return true;
+            };
+            uint4 v0[4], v1[4];
+            load(v0, 0);
+            for (int k0 = 0; ok && k0 < a.KI; k0 += 2 * B) {
+                load(v1, (k0 + B) * W * 4);
+                ok = store(v0, k0);
+                if (!ok || k0 + B >= a.KI) break;
+                load(v0, (k0 + 2 * B) * W * 4);
+                ok = store(v1, k0 + B);
             }
         }
-    } else if (warp == 3) {
-        // ---- codes of rows in token order: lane i gathers rows 4 i .. 4 i + 3 (and 128 further on)
+    } else if (OP == kExGateUp && warp >= 12) {
+        // ---- codes of rows in token order: two warps, four rows (of 128 bytes) of every eight each.  A stage's
+        // copies arrive on a barrier of the warp; once they are there the warp passes the stage on (the proxy fence
+        // has to be its own), in between waiting for the next stage to come free.
+        // (Four-row tensor-map gathers took some 90 cycles each: 495 instead of 350 us for 1001 tokens.)
+        const int which = warp - 12;
+        int* tok = s_tok[which];
+        const int quad = lane >> 3, chunk = lane & 7;  // this lane's row of four and 16-byte chunk
+        const uint32_t land0 = smem_u32(&s_land[which][0]);
         bool ok = gather;
-        for (; ok && walk.ct < total; walk.next()) {
-            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
-            int tok[8];
+        int late = 0, lst = 0;  // stages not passed on yet, and the first of them
+        unsigned lph = 0;
+        int f[4];  // assignments of the tile's rows 8 i + 4 which + 0..3, i < 32 (those of this CTA)
+        ExTile o{};
+        auto fetch = [&] {
+            if (!ok || walk.ct >= total) return;
+            o = EX_TILE;
+            const int nx = PAIR ? o.n >> 1 : o.n;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = (lane + (i >> 2) * 32) * 4 + (i & 3);
-                int f = r < o.rows ? a.sorted[o.r0 + r] : 0;
-                if (f < 0 || f >= a.mk) f = 0;  // a padding position: any row, its column is not used
-                tok[i] = f / a.topk;
+            for (int u = 0; u < 4; ++u) {
+                const int i = lane + 32 * u, r = rank * nx + (i >> 2) * 8 + which * 4 + (i & 3);
+                f[u] = i < nx / 2 && r < o.rows ? a.sorted[o.r0 + r] : 0;
             }
-            for (int ki = 0; ki < a.KI; ++ki) {
-                if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t full = full0 + 8u * st, xsm = base + (uint32_t)st * code_bytes + kExWBytes;
-                if (ex_elect()) mbar_expect_tx(full, (unsigned)(o.n * 128));
-                __syncwarp();
+        };
+        auto pass_on = [&] {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full0 + 8u * lst);
+            if (++lst == nst) lst = 0, lph ^= 1u;
+            --late;
+        };
+        fetch();
+        while (ok && walk.ct < total) {
+            const int nx = PAIR ? o.n >> 1 : o.n;
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int g = lane + i * 32;
-                    if (g * 4 < o.n)
-                        tma_gather4(xsm + (uint32_t)g * 512u, &a.tm_x, ki * 128, tok[4 * i], tok[4 * i + 1],
-                                    tok[4 * i + 2], tok[4 * i + 3], full);
+            for (int u = 0; u < 4; ++u)  // (positions past the real ones take any token: their columns are not used)
+                if (lane + 32 * u < nx / 2) tok[lane + 32 * u] = (unsigned)f[u] < (unsigned)a.mk ? f[u] / a.topk : 0;
+            __syncwarp();
+            walk.next();
+            fetch();  // the next tile's, while this one is copied
+            for (int ki = 0; ok && ki < a.KI; ++ki) {
+                unsigned long long t0 = 0;
+                for (int turn = 1; !__all_sync(kFull, mbar_test(empty0 + 8u * st, ph ^ 1u)); ++turn) {
+                    if (late > 0 && __all_sync(kFull, mbar_test(land0 + 8u * lst, lph))) {
+                        pass_on();
+                        continue;
+                    }
+                    if ((turn & 63) != 0) continue;
+                    if (t0 == 0) t0 = global_ns();
+                    if (__any_sync(kFull, global_ns() - t0 >= a.wait_ns)) {
+                        *(volatile int*)&s_abort = 1;
+                        atomicExch(&g_ex_timeout, 1);
+                    }
+                    if (__any_sync(kFull, *(volatile int*)&s_abort != 0)) {
+                        ok = false;
+                        break;
+                    }
                 }
-                __syncwarp();
+                if (!ok) break;
+                const uint32_t xsm = base + (uint32_t)st * code_bytes + kExWBytes;
+                const int at = ki * 128 + chunk * 16, bytes = at < a.kbytes ? 16 : 0;
+                const uint8_t* x = a.x + (bytes ? at : 0);
+                for (int i = quad; i < nx / 2; i += 4) {
+                    const int r = (i >> 2) * 8 + which * 4 + quad;
+                    ex_cp_async16(xsm + (uint32_t)(r * 128 + ((chunk ^ (r & 7)) << 4)), x + (int64_t)tok[i] * a.ldx, bytes);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(land0 + 8u * st) : "memory");
+                ++late;
+                if (__all_sync(kFull, mbar_test(land0 + 8u * lst, lph))) pass_on();
                 if (++st == nst) st = 0, ph ^= 1u;
             }
         }
+        while (late > 0 && ex_wait(land0 + 8u * lst, lph, a.wait_ns, &s_abort)) pass_on();
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ---- accumulator -> outputs: warps 4-7 and 8-11 take alternate chunks of 16 columns
         const int wq = warp & 3, grp = (warp >> 2) - 1, et = tid - 128, gt = et & 127;
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
         unsigned turn = 0;  // staging buffer of the group
+        const uint32_t tfree = PAIR ? map_rank(smem_u32(&s_tfree), 0) : smem_u32(&s_tfree);
+        auto release = [&] {
+            if (PAIR) mbar_arrive_remote(tfree);
+            else mbar_arrive(tfree);
+        };
         for (int it = 0; walk.ct < total; walk.next(), ++it) {
-            const ExTile o = ex_tile(t, a.E, walk.ct, walk.rt, listed);
+            const ExTile o = EX_TILE;
             int* f = s_f[it & 1];
             if (OP != kExGemm && et < o.n) f[et] = et < o.rows ? a.sorted[o.r0 + et] : a.mk;
             const bool ok = ex_wait(smem_u32(&s_tfull[it & 1]), (unsigned)(it >> 1) & 1u, a.wait_ns, &s_abort);
@@ -605,7 +728,7 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
             // the shared columns first: the chunks after which the next tile may start
             const bool from_top = !(it & 1) && o.n > kExBuf1;
             const int need = from_top ? nch - kExBuf1 / 16 : (it & 1) ? min(2, nch) : 0;
-            if (need <= grp && lane == 0) mbar_arrive(smem_u32(&s_tfree));
+            if (need <= grp && lane == 0) release();
             const int r = o.rt * 128 + wq * 32 + lane;
             for (int i = grp; i < nch; i += 2) {
                 const int c0 = (from_top ? nch - 1 - i : i) * 16;
@@ -614,7 +737,7 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
                 if (i < need && i + 2 >= need) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_tfree));
+                    if (lane == 0) release();
                 }
                 if (OP == kExGemm) {
                     const int64_t at = (int64_t)(o.r0 + c0) * a.ldo + r;
@@ -631,7 +754,7 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
                             if (j < cols) *p = __float2bfloat16_rn(__uint_as_float(v[j]));
                     }
                 } else if (OP == kExDown) {
-                    float* y = a.y + r;
+                    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.out) + r;
 #pragma unroll
                     for (int j4 = 0; j4 < 4; ++j4) {
                         const int4 as = *reinterpret_cast<const int4*>(f + c0 + 4 * j4);
@@ -639,7 +762,7 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if ((unsigned)s4[j] < (unsigned)a.mk && r < a.R)
-                                y[(int64_t)s4[j] * a.R] = __uint_as_float(v[4 * j4 + j]);
+                                y[(int64_t)s4[j] * a.R] = __float2bfloat16_rn(__uint_as_float(v[4 * j4 + j]));
                     }
                 } else {
                     // lanes 0-15 hold gate rows and lanes 16-31 the up rows of
@@ -682,11 +805,13 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
             tc_fence_before();
         }
     }
-    __syncthreads();
+    __syncwarp();
+    if (PAIR) ex_cluster_sync();  // (no CTA leaves while its peer may still use its memory)
+    else __syncthreads();
     if (warp == 1) {
         if (s_abort) {
             // products already issued are waited for before their tensor memory goes
-            if (ex_elect()) ex_commit(smem_u32(&s_drain));
+            if (rank == 0 && ex_elect()) ex_commit<PAIR>(smem_u32(&s_drain));
             __syncwarp();
             const unsigned long long t0 = global_ns();
             while (!mbar_try_wait(smem_u32(&s_drain), 0) && global_ns() - t0 < a.wait_ns) {
@@ -694,8 +819,10 @@ __global__ void __launch_bounds__(kExThreads, 1) expert_kernel(const __grid_cons
         }
         __syncwarp();
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+#undef EX_TILE
 }
 
 }  // namespace mr

@@ -56,38 +56,96 @@ cudaError_t launch_mx_pack(const uint8_t* scale, int64_t E, int R, int K, int fp
 // ------------------------------------------------------------------ the combination over a token's experts
 
 // out[m, r] = bf16(add[m, r] + sum_j weights[m, j] y[m * topk + j, r]), j
-// ascending in fp32; assignments whose expert is outside [0, E) are skipped.
-// A thread takes four columns of a row.
-__global__ void __launch_bounds__(256) expert_combine_kernel(const float* y, const int32_t* ids, const float* weights,
-                                                             const __nv_bfloat16* add, __nv_bfloat16* out, int64_t M,
-                                                             int topk, int R, int E) {
-    pdl_trigger();
+// ascending in fp32; slots whose id is outside [0, E) are skipped, whatever y
+// holds there.  A thread takes eight columns of a row (VEC; else one): eight
+// slots' rows are in flight at a time.  Bound by reading y: 4096 tokens x 8 x
+// 6144 is 403 MB.  Launched so that its CTAs are in place when the products
+// end (the wait is for all of them, and for the memory they wrote).
+template <bool VEC>
+__global__ void __launch_bounds__(256) expert_combine_kernel(const __nv_bfloat16* y, const int32_t* ids,
+                                                             const float* weights, const __nv_bfloat16* add,
+                                                             __nv_bfloat16* out, int64_t M, int topk, int R, int E) {
+    constexpr int N = VEC ? 8 : 1;
     pdl_wait();
-    const int per = (R + 3) >> 2;
+    const int per = R / N;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < M * per; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t m = i / per;
-        const int r = (int)(i - m * per) * 4;
-        float s[4];
+        const int r = (int)(i - m * per) * N;
+        float s[N];
+        auto wide = [](uint4 q, float* f) {
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int u = 0; u < 4; ++u) s[u] = add != nullptr && r + u < R ? __bfloat162float(add[m * R + r + u]) : 0.0f;
-        for (int j = 0; j < topk; ++j) {
-            const int e = __ldg(ids + m * topk + j);
-            if (e < 0 || e >= E) continue;
-            const float w = __ldg(weights + m * topk + j);
-            const float* p = y + (m * topk + j) * R + r;
-            if ((R & 3) == 0) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
-                s[0] = __fmaf_rn(w, v.x, s[0]);
-                s[1] = __fmaf_rn(w, v.y, s[1]);
-                s[2] = __fmaf_rn(w, v.z, s[2]);
-                s[3] = __fmaf_rn(w, v.w, s[3]);
-            } else {
-                for (int u = 0; u < 4 && r + u < R; ++u) s[u] = __fmaf_rn(w, __ldcg(p + u), s[u]);
+            for (int u = 0; u < 4; ++u) {
+                f[2 * u] = __uint_as_float(w[u] << 16);
+                f[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u);
+            }
+        };
+        if (add == nullptr) {
+#pragma unroll
+            for (int u = 0; u < N; ++u) s[u] = 0.0f;
+        } else if (VEC) {
+            wide(*reinterpret_cast<const uint4*>(add + m * R + r), s);
+        } else {
+            s[0] = __bfloat162float(add[m * R + r]);
+        }
+        for (int j0 = 0; j0 < topk; j0 += 8) {
+            uint4 v[8];
+            int id[8];
+            float w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                id[u] = -1;
+                if (j0 + u >= topk) continue;
+                const int64_t f = m * topk + j0 + u;
+                const __nv_bfloat16* p = y + f * R + r;
+                id[u] = __ldg(ids + f);
+                w[u] = __ldg(weights + f);
+                if (VEC) v[u] = __ldcg(reinterpret_cast<const uint4*>(p));
+                else v[u].x = (uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if ((unsigned)id[u] >= (unsigned)E) continue;
+                float f[8];
+                if (VEC) wide(v[u], f);
+                else f[0] = __uint_as_float(v[u].x);
+#pragma unroll
+                for (int q = 0; q < N; ++q) s[q] = __fmaf_rn(w[u], f[q], s[q]);
             }
         }
-        for (int u = 0; u < 4; ++u)
-            if (r + u < R) out[m * R + r + u] = __float2bfloat16_rn(s[u]);
+        if (VEC) {
+            uint4 q;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.x) : "f"(s[1]), "f"(s[0]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.y) : "f"(s[3 % N]), "f"(s[2 % N]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.z) : "f"(s[5 % N]), "f"(s[4 % N]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.w) : "f"(s[7 % N]), "f"(s[6 % N]));
+            *reinterpret_cast<uint4*>(out + m * R + r) = q;
+        } else {
+            out[m * R + r] = __float2bfloat16_rn(s[0]);
+        }
     }
+}
+
+cudaError_t launch_combine(const ExpertCall& c, const __nv_bfloat16* y, int sms, cudaStream_t st) {
+    const auto* add = static_cast<const __nv_bfloat16*>(c.add);
+    auto* out = static_cast<__nv_bfloat16*>(c.out);
+    const bool vec = c.R % 8 == 0 && (reinterpret_cast<uintptr_t>(add) | reinterpret_cast<uintptr_t>(out)) % 16 == 0;
+    const int64_t work = (int64_t)c.M * (c.R / (vec ? 8 : 1));
+    int64_t ctas = (work + 255) / 256;
+    if (ctas > (int64_t)sms * 8) ctas = (int64_t)sms * 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, vec ? expert_combine_kernel<true> : expert_combine_kernel<false>, y, c.topk_ids,
+                           c.topk_weights, add, out, (int64_t)c.M, c.topk, c.R, c.E);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ host
@@ -104,19 +162,39 @@ bool encode(CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP4, int OP>
+template <bool FP4, int OP, bool PAIR>
 cudaError_t launch_one(const ExpertArgs& a, int grid, cudaStream_t st) {
     static int prepared[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const auto kernel = expert_kernel<FP4, OP, PAIR>;
     if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(expert_kernel<FP4, OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmemDyn);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmemDyn);
         if (e != cudaSuccess) return e;
         __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
     }
-    return launch_kernel(expert_kernel<FP4, OP>, dim3((unsigned)grid), dim3(kExThreads), kExSmemDyn, st, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(PAIR ? grid & ~1 : grid));
+    cfg.blockDim = dim3(ex_threads(OP));
+    cfg.dynamicSmemBytes = kExSmemDyn;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = (launch_flags() & 1) ? 1 : 0;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <int OP>
+cudaError_t launch_op(const ExpertArgs& a, bool fp4, bool pair, int grid, cudaStream_t st) {
+    if (fp4) return pair ? launch_one<true, OP, true>(a, grid, st) : launch_one<true, OP, false>(a, grid, st);
+    return pair ? launch_one<false, OP, true>(a, grid, st) : launch_one<false, OP, false>(a, grid, st);
 }
 
 }  // namespace
@@ -148,9 +226,8 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
         }
         const cuuint64_t dims[2] = {kbytes, (cuuint64_t)c.x_rows};
         const cuuint64_t strides[1] = {(cuuint64_t)c.ldx};
-        const cuuint32_t box[2] = {128, c.gather ? 1u : 16u}, box64[2] = {128, 64};
-        if (!encode(&a.tm_x, c.x, 2, dims, strides, box) ||
-            (!c.gather && !encode(&a.tm_x64, c.x, 2, dims, strides, box64)))
+        const cuuint32_t box[2] = {128, 16}, box64[2] = {128, 64};
+        if (!c.gather && (!encode(&a.tm_x, c.x, 2, dims, strides, box) || !encode(&a.tm_x64, c.x, 2, dims, strides, box64)))
             return MR_ERR_UNSUPPORTED;
     }
     a.w_scale = c.w_scale;
@@ -160,7 +237,6 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     a.experts = c.experts;
     a.out = c.out;
     a.out_scale = c.out_scale;
-    a.y = c.y;
     a.ldo = c.ldo;
     a.wait_ns = wait_limit_ns();
     a.E = c.E;
@@ -183,20 +259,16 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     }
     a.out_fmt = c.out_fmt;
     a.flags = launch_flags();
-    const int grid = sms;
-    cudaError_t e;
-    if (c.op == kExGemm) e = fp4 ? launch_one<true, kExGemm>(a, grid, st) : launch_one<false, kExGemm>(a, grid, st);
-    else if (c.op == kExGateUp)
-        e = fp4 ? launch_one<true, kExGateUp>(a, grid, st) : launch_one<false, kExGateUp>(a, grid, st);
-    else e = fp4 ? launch_one<true, kExDown>(a, grid, st) : launch_one<false, kExDown>(a, grid, st);
-    if (e == cudaSuccess && c.op == kExDown) {
-        const int64_t work = (int64_t)c.M * ((R + 3) / 4);
-        int64_t ctas = (work + 255) / 256;
-        if (ctas > (int64_t)sms * 8) ctas = (int64_t)sms * 8;
-        e = launch_kernel(expert_combine_kernel, dim3((unsigned)ctas), dim3(256), 0, st, static_cast<const float*>(c.y),
-                          c.topk_ids, c.topk_weights, static_cast<const __nv_bfloat16*>(c.add),
-                          static_cast<__nv_bfloat16*>(c.out), (int64_t)c.M, c.topk, R, c.E);
-    }
+    a.x = c.x;
+    a.ldx = c.ldx;
+    a.kbytes = (int)kbytes;
+    if (c.op == kExDown) a.out = static_cast<char*>(c.scratch) + kWorkOffset + expert_part_bytes(a.mk);
+    const int grid = sms < kExMaxCtas ? sms : kExMaxCtas;
+    const bool pair = expert_pair(a.mk, c.E);
+    cudaError_t e = c.op == kExGemm     ? launch_op<kExGemm>(a, fp4, pair, grid, st)
+                          : c.op == kExGateUp ? launch_op<kExGateUp>(a, fp4, pair, grid, st)
+                                              : launch_op<kExDown>(a, fp4, pair, grid, st);
+    if (e == cudaSuccess && c.op == kExDown) e = launch_combine(c, static_cast<const __nv_bfloat16*>(a.out), sms, st);
     *err = e;
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }

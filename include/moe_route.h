@@ -604,7 +604,7 @@ int mr_moe_gate_up(const mr_moe_gate_up_params *params, void *stream);
 
 /*
  * Stage 2 of the routed experts and the combination over a token's slots:
- *   y[f, r]   = sum_i act[p(f), i] w2[e, r, i]
+ *   y[f, r]   = bf16(sum_i act[p(f), i] w2[e, r, i])
  *   out[m, r] = bf16(add[m, r] + sum_j topk_weights[m, j] y[m * topk + j, r])
  * the sum over j ascending in fp32, so the result does not depend on the
  * order in which experts finish.  q, scale: the rows of act at their sorted
@@ -612,7 +612,7 @@ int mr_moe_gate_up(const mr_moe_gate_up_params *params, void *stream);
  * nothing); w2: [E, R, I].  Slots whose id in topk_ids is outside [0, E) add
  * nothing; a token without any gives add, or zero.  topk_ids, topk_weights:
  * [M, topk]; add: bf16 [M, R] or NULL; out: bf16 [M, R], may be add itself.
- * scratch: mr_expert_scratch_bytes(M, topk, R, 1).
+ * scratch: mr_expert_scratch_bytes(M, topk, R, 1).  Two launches.
  */
 typedef struct mr_moe_down_params {
     const uint8_t *q;

@@ -101,6 +101,8 @@ def down(a, w2, st, ex, ids, wts, block, E, add=None):
         y[f[m]] = rows @ w2[k].T
         d[f[m]] = sum_bound(rows.shape[1]) * (rows.abs() @ w2[k].abs().T)
     w = (wts.double() * ((ids >= 0) & (ids < E)))[..., None]
+    # a product is rounded to bf16 before it is weighted: half a step of a value within d of y
+    d = d + half_step(torch.bfloat16) * (y.abs() + d)
     y, d = y.unflatten(0, (M, topk)), d.unflatten(0, (M, topk))
     out = (w * y).sum(1)
     mag = (w * y).abs().sum(1)

@@ -34,7 +34,9 @@ def test_expert_scratch_bytes(lib):
     f = lib.mr_expert_scratch_bytes
     small, big = f(1, 8, 0, 0), f(4096, 8, 0, 0)
     assert 32768 < small < big == f(1 << 20, 8, 0, 0)
-    assert f(1, 8, 6144, 1) >= small + 8 * 6144 * 4
+    assert f(1, 8, 6144, 1) >= small + 8 * 6144 * 2
+    for mk in (1, 7, 100, 2047, 2048, 30000, 33000, 70000, 200000):  # grows with the rows
+        assert f(mk, 1, 6144, 1) <= f(mk + 1, 1, 6144, 1)
     for bad in ((0, 8, 0, 0), (1, 0, 0, 0), (1, 33, 0, 0), (1, 8, 0, 1), (1 << 28, 32, 0, 0)):
         assert f(*bad) == 0, bad
 
