@@ -91,7 +91,7 @@ SIGNATURES = {
     "mr_last_cuda_error": (_I, []),
     "mr_mx_packed_scale_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "mr_mx_pack_scales": (_I, [_P, _I, _I, _I, _I, _I, _P, _P]),
-    "mr_expert_scratch_bytes": (_SZ, [_I, _I, _I, _I]),
+    "mr_expert_scratch_bytes": (_SZ, [_I, _I, _I]),
     "mr_mx_gemm": (_I, [_P, _P]),
     "mr_moe_gate_up": (_I, [_P, _P]),
     "mr_moe_down": (_I, [_P, _P]),
@@ -849,25 +849,16 @@ class MxWeight:
 
 
 class ExpertScratch:
-    """A caller-owned scratch buffer of the expert products (zeroed once at
-    creation) for up to M_max tokens: ExpertScratch(M_max) for mx_gemm,
-    ExpertScratch(M_max, topk) for moe_gate_up, ExpertScratch(M_max, topk, R)
-    for moe_down with R output columns."""
+    """A caller-owned scratch buffer of moe_down for up to M_max tokens of
+    topk slots and R output columns (a torch uint8 tensor; its contents do
+    not matter between calls)."""
 
-    def __init__(self, M_max: int, topk: int = 1, R: int = 0, device=None):
+    def __init__(self, M_max: int, topk: int, R: int, device=None):
         torch = _torch()
-        self.nbytes = int(_load().mr_expert_scratch_bytes(M_max, topk, R, int(R > 0)))
+        self.nbytes = int(_load().mr_expert_scratch_bytes(M_max, topk, R))
         if self.nbytes == 0:
             raise ValueError("scratch size query rejected the arguments")
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=device if device is not None else "cuda")
-        self.reset()
-
-    def reset(self, stream=None):
-        """Zero the counters (the first SCRATCH_COUNTER_BYTES)."""
-        dev = self.tensor.device
-        with _launch_ctx(dev):
-            _check(_load().mr_scratch_reset(ctypes.c_void_p(self.tensor.data_ptr()), SCRATCH_COUNTER_BYTES,
-                                            _stream_on(dev, stream)), "mr_scratch_reset")
 
     @property
     def ptr(self):
@@ -877,8 +868,7 @@ class ExpertScratch:
 class MxGemmParams(ctypes.Structure):
     """mr_mx_gemm_params of moe_route.h, field for field."""
     _fields_ = [("q", _P), ("ldq", _I64), ("scale", _P), ("lds", _I64), ("w", _P), ("w_scale", _P), ("M", _I),
-                ("R", _I), ("K", _I), ("format", _I), ("out", _P), ("ldo", _I64), ("out_fp32", _I), ("scratch", _P),
-                ("scratch_bytes", _SZ)]
+                ("R", _I), ("K", _I), ("format", _I), ("out", _P), ("ldo", _I64), ("out_fp32", _I)]
 
 
 class GateUpParams(ctypes.Structure):
@@ -886,7 +876,7 @@ class GateUpParams(ctypes.Structure):
     _fields_ = [("q", _P), ("ldq", _I64), ("scale", _P), ("lds", _I64), ("sorted_rows", _I), ("w13", _P),
                 ("w13_scale", _P), ("E", _I), ("I", _I), ("K", _I), ("format", _I), ("sorted_token_ids", _P),
                 ("expert_ids", _P), ("n_blocks", _I), ("block", _I), ("M", _I), ("topk", _I), ("out_format", _I),
-                ("act", _P), ("act_scale", _P), ("scratch", _P), ("scratch_bytes", _SZ)]
+                ("act", _P), ("act_scale", _P)]
 
 
 class DownParams(ctypes.Structure):
@@ -926,17 +916,10 @@ def _check_sorted(st, ex, block, dev):
     return n
 
 
-def _expert_scratch(scratch, M, topk, R, dev):
-    if scratch is None:
-        return ExpertScratch(M, topk, R, device=dev)
-    _check_scratch(scratch, dev)
-    return scratch
-
-
 class PreparedMxGemm(_Prepared):
     """mx_gemm over fixed buffers; arguments as mx_gemm."""
 
-    def __init__(self, q, scale, w: MxWeight, out=None, out_dtype=None, scratch: ExpertScratch | None = None):
+    def __init__(self, q, scale, w: MxWeight, out=None, out_dtype=None):
         torch = _torch()
         if w.codes.dim() != 2 or w.gate_up:
             raise ValueError("mx_gemm takes a weight [R, K] laid out without gate_up")
@@ -951,29 +934,26 @@ class PreparedMxGemm(_Prepared):
             raise ValueError("out must be bfloat16 or float32")
         if tuple(out.shape) != (M, w.R) or (w.R > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < w.R):
             raise ValueError(f"out must have shape {(M, w.R)} with a contiguous last dimension")
-        scratch = _expert_scratch(scratch, M, 1, 0, dev)
         p.w, p.w_scale = w.codes.data_ptr(), w.packed.data_ptr()
         p.M, p.R, p.K, p.format = M, w.R, w.K, QUANT_FORMAT[w.format]
         p.out, p.ldo, p.out_fp32 = out.data_ptr(), out.stride(0) if M > 1 else w.R, int(out.dtype == torch.float32)
-        p.scratch, p.scratch_bytes = scratch.ptr, scratch.nbytes
-        self.out, self.device, self._keep = out, dev, (q, scale, w, scratch)
+        self.out, self.device, self._keep = out, dev, (q, scale, w)
         self._ref = ctypes.byref(p)
         self._fn, self._name = _load().mr_mx_gemm, "mr_mx_gemm"
 
 
-def mx_gemm(q, scale, w: MxWeight, out=None, out_dtype=None, scratch: ExpertScratch | None = None, stream=None):
+def mx_gemm(q, scale, w: MxWeight, out=None, out_dtype=None, stream=None):
     """Product of microscaled operands: [M, R] (bf16, or out_dtype fp32) =
     x [M, K] @ w [R, K]^T with x given as the codes q and scales of
     mxfp8_quant / mxfp4_quant, in the weight's format."""
-    return PreparedMxGemm(q, scale, w, out, out_dtype, scratch)(stream)
+    return PreparedMxGemm(q, scale, w, out, out_dtype)(stream)
 
 
 class PreparedGateUp(_Prepared):
     """moe_gate_up over fixed buffers; arguments as moe_gate_up."""
 
     def __init__(self, q, scale, w13: MxWeight, sorted_token_ids, expert_ids, topk: int, block: int,
-                 num_tokens: int | None = None, sorted_rows: bool = False, quant=None, out=None,
-                 scratch: ExpertScratch | None = None):
+                 num_tokens: int | None = None, sorted_rows: bool = False, quant=None, out=None):
         torch = _torch()
         if w13.codes.dim() != 3 or not w13.gate_up:
             raise ValueError("moe_gate_up takes a weight [E, 2I, K] laid out with gate_up=True")
@@ -1008,7 +988,6 @@ class PreparedGateUp(_Prepared):
             _check_out(o0, "out codes", (cap, iq), torch.uint8, dev)
             _check_out(o1, "out scale", (cap, I // 32), torch.uint8, dev)
             out = (o0, o1)
-        scratch = _expert_scratch(scratch, M, topk, 0, dev)
         p.sorted_rows = int(sorted_rows)
         p.w13, p.w13_scale = w13.codes.data_ptr(), w13.packed.data_ptr()
         p.E, p.I, p.K, p.format = w13.E, I, w13.K, QUANT_FORMAT[w13.format]
@@ -1016,15 +995,13 @@ class PreparedGateUp(_Prepared):
         p.n_blocks, p.block, p.M, p.topk = n, block, M, topk
         p.out_format, p.act = QUANT_FORMAT[quant], o0.data_ptr()
         p.act_scale = None if quant is None else o1.data_ptr()
-        p.scratch, p.scratch_bytes = scratch.ptr, scratch.nbytes
-        self.out, self.device, self._keep = out, dev, (q, scale, w13, sorted_token_ids, expert_ids, scratch)
+        self.out, self.device, self._keep = out, dev, (q, scale, w13, sorted_token_ids, expert_ids)
         self._ref = ctypes.byref(p)
         self._fn, self._name = _load().mr_moe_gate_up, "mr_moe_gate_up"
 
 
 def moe_gate_up(q, scale, w13: MxWeight, sorted_token_ids, expert_ids, topk: int, block: int,
-                num_tokens: int | None = None, sorted_rows: bool = False, quant=None, out=None,
-                scratch: ExpertScratch | None = None, stream=None):
+                num_tokens: int | None = None, sorted_rows: bool = False, quant=None, out=None, stream=None):
     """Stage 1 of the routed experts (mr_moe_gate_up): silu(x . gate^T) *
     (x . up^T) of every assignment, at its sorted position.  q, scale: the
     quantised tokens [M, ...], or with sorted_rows the rows at the sorted
@@ -1033,7 +1010,7 @@ def moe_gate_up(q, scale, w13: MxWeight, sorted_token_ids, expert_ids, topk: int
     (codes, scales), as mxfp8_quant / mxfp4_quant of those rows.  Rows that
     hold no assignment are left as they were."""
     return PreparedGateUp(q, scale, w13, sorted_token_ids, expert_ids, topk, block, num_tokens, sorted_rows, quant,
-                          out, scratch)(stream)
+                          out)(stream)
 
 
 class PreparedDown(_Prepared):
@@ -1061,7 +1038,9 @@ class PreparedDown(_Prepared):
         if out is None:
             out = torch.empty((M, w2.R), dtype=torch.bfloat16, device=dev)
         _check_out(out, "out", (M, w2.R), torch.bfloat16, dev)
-        scratch = _expert_scratch(scratch, M, topk, w2.R, dev)
+        if scratch is None:
+            scratch = ExpertScratch(M, topk, w2.R, device=dev)
+        _check_scratch(scratch, dev)
         p.w2, p.w2_scale = w2.codes.data_ptr(), w2.packed.data_ptr()
         p.E, p.R, p.I, p.format = w2.E, w2.R, w2.K, QUANT_FORMAT[w2.format]
         p.sorted_token_ids, p.expert_ids = sorted_token_ids.data_ptr(), expert_ids.data_ptr()

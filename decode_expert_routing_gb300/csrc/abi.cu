@@ -635,11 +635,10 @@ int mr_mx_pack_scales(const uint8_t* scale, int E, int R, int K, int format, int
                                           as_stream(stream)));
 }
 
-size_t mr_expert_scratch_bytes(int M_max, int topk, int R, int down) {
-    if (M_max < 1 || topk < 1 || topk > MR_MAX_TOPK || (down && R < 1)) return 0;
+size_t mr_expert_scratch_bytes(int M_max, int topk, int R) {
+    if (M_max < 1 || topk < 1 || topk > MR_MAX_TOPK || R < 1) return 0;
     const int64_t mk = (int64_t)M_max * topk;
-    if (mk >= ((int64_t)1 << 30)) return 0;
-    return mr::expert_scratch_bytes(mk, down ? R : 0);
+    return mk < ((int64_t)1 << 30) ? mr::expert_scratch_bytes(mk, R) : 0;
 }
 
 int mr_mx_gemm(const mr_mx_gemm_params* p, void* stream) {
@@ -650,7 +649,6 @@ int mr_mx_gemm(const mr_mx_gemm_params* p, void* stream) {
         p->out == nullptr || !aligned(p->out, p->out_fp32 ? 4 : 2) || p->ldo < p->R)
         return MR_ERR_INVALID_ARG;
     if (p->M >= (1 << 30)) return MR_ERR_UNSUPPORTED;
-    if ((s = check_expert_scratch(p->scratch, p->scratch_bytes, mr::expert_scratch_bytes(p->M, 0))) != MR_OK) return s;
     mr::ExpertCall c{};
     c.op = 0;
     c.fp4 = p->format == MR_QUANT_MXFP4;
@@ -670,7 +668,6 @@ int mr_mx_gemm(const mr_mx_gemm_params* p, void* stream) {
     c.ldo = p->ldo;
     c.x_rows = p->M;
     c.out = p->out;
-    c.scratch = p->scratch;
     return run_expert(c, stream);
 }
 
@@ -691,8 +688,6 @@ int mr_moe_gate_up(const mr_moe_gate_up_params* p, void* stream) {
     if (p->act == nullptr || !aligned(p->act, of == MR_QUANT_NONE ? 16 : 8) ||
         (of != MR_QUANT_NONE && p->act_scale == nullptr))
         return MR_ERR_INVALID_ARG;
-    const int64_t mk = (int64_t)p->M * p->topk;
-    if ((s = check_expert_scratch(p->scratch, p->scratch_bytes, mr::expert_scratch_bytes(mk, 0))) != MR_OK) return s;
     mr::ExpertCall c{};
     c.op = 1;
     c.fp4 = p->format == MR_QUANT_MXFP4;
@@ -716,7 +711,6 @@ int mr_moe_gate_up(const mr_moe_gate_up_params* p, void* stream) {
     c.experts = p->expert_ids;
     c.out = p->act;
     c.out_scale = p->act_scale;
-    c.scratch = p->scratch;
     return run_expert(c, stream);
 }
 

@@ -10,8 +10,9 @@
 // is loaded once for up to 256 rows.
 //
 // Work: an expert's rows form column tiles of at most 256 rows; a tile is one
-// column tile times 128 weight rows, and its K range is cut into stages of
-// 128 bytes of codes a row (128 E4M3 or 256 E2M1 elements).  One CTA per SM
+// column tile times 128 weight rows, and its K range is cut into blocks of 128
+// bytes of codes a row (128 E4M3 or 256 E2M1 elements); a stage of the ring is
+// two of them while three such stages fit, else one.  One CTA per SM
 // walks the tiles.  Warp 0 copies the codes (tensor maps, 128-byte swizzle) and
 // the weights' scales (laid out once, see mx_pack_kernel), two warps the codes
 // of rows in token order, two the activations' scales (into the weights' scale
@@ -43,7 +44,7 @@ namespace mr {
 __host__ __device__ constexpr int ex_threads(int op) { return op == 1 ? 448 : 384; }
 constexpr int kExMaxStages = 12;
 constexpr int kExMaxN = 256;             // activation rows of a tile
-constexpr int kExWBytes = 128 * 128;     // one stage of weight codes
+constexpr int kExWBytes = 128 * 128;     // weight codes of one k-block (128 bytes a row)
 constexpr int kExSmemDyn = 214 * 1024;   // dynamic shared memory (one CTA per SM)
 constexpr int kExListMax = 1536;        // column tiles in the shared list
 constexpr int kExSfCol = 488;            // tensor-memory columns of the scale factors
@@ -59,7 +60,7 @@ struct ExpertArgs {
     CUtensorMap tm_w;        // weight codes, box of 128 rows x 128 bytes
     CUtensorMap tm_x;        // activation codes, box of 16 rows x 128 bytes (not with gather)
     CUtensorMap tm_x64;      // the same in boxes of 64 rows
-    const uint8_t* w_scale;  // packed: [E][row tile][stage][512 * words]
+    const uint8_t* w_scale;  // packed: [E][row tile][k-block][512 * words]
     const uint8_t* x_scale;  // [rows][lds] bytes
     int64_t lds;
     const int32_t* sorted;   // [cap] assignment of a sorted position
@@ -70,7 +71,7 @@ struct ExpertArgs {
     const uint8_t* x;        // activation codes (rows in token order)
     int64_t ldx;
     unsigned long long wait_ns;
-    int E, R, RT, KI, kb, kbytes;  // weight rows, row tiles, stages, scale and code bytes per row
+    int E, R, RT, KI, kb, kbytes;  // weight rows, row tiles, k-blocks, scale and code bytes per row
     int M, topk, mk, nblk, block;
     int gather;              // x rows in token order
     int sf_vec;              // bytes that the scale rows can be read in: 16, 8, 4 or 1
@@ -237,6 +238,17 @@ __device__ __forceinline__ bool ex_sync(int id, int threads, bool ok) {
     return r != 0;
 }
 
+// a / b for a < 2^23 (a quotient rounded to within one, then put right): the
+// general division is several times longer, and the ones between the tables
+// and the first copy are in every call's way.
+__device__ __forceinline__ unsigned ex_div(unsigned a, unsigned b) {
+    unsigned q = __float2uint_rz(__fdividef((float)a, (float)b));
+    const int r = (int)(a - q * b);
+    if (r < 0) --q;
+    else if (r >= (int)b) ++q;
+    return q;
+}
+
 // The experts' column tiles, built by every CTA from the route's outputs.
 struct ExTables {
     int* first;  // [E] first sorted position
@@ -254,15 +266,21 @@ __device__ __forceinline__ int ex_ncol(int rows) { return (rows + kExMaxN - 1) /
 template <bool PAIR>
 __device__ __forceinline__ int ex_round(int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; }
 template <bool PAIR>
-__device__ __forceinline__ int ex_share(int rows, int nct) { return ex_round<PAIR>((rows + nct - 1) / nct); }
+__device__ __forceinline__ int ex_share(int rows, int nct) {
+    return ex_round<PAIR>(nct <= 1 ? rows : (rows + nct - 1) / nct);
+}
 
-// Column tile ct of the list, or (a list that does not fit: more than some
+// Column tile ct: of the list, or (a list that does not fit: more than some
 // hundred thousand assignments) by a search over the experts.
-template <bool PAIR>
-__device__ __forceinline__ ExTile ex_tile(const ExTables& t, int E, int ct, int rt, bool listed) {
+template <bool PAIR, int OP>
+__device__ __forceinline__ ExTile ex_tile(const ExTables& t, int E, int ct, int rt, bool listed, int M, int per_gemm) {
     ExTile o;
     o.rt = rt;
-    if (listed) {
+    if (OP == kExGemm) {  // one expert, equal shares
+        o.e = 0;
+        o.r0 = ct * per_gemm;
+        o.rows = min(per_gemm, M - o.r0);
+    } else if (listed) {
         const int2 v = t.list[ct];
         o.r0 = __shfl_sync(kFull, v.x, 0);
         const int w = __shfl_sync(kFull, v.y, 0);
@@ -288,13 +306,11 @@ __device__ __forceinline__ ExTile ex_tile(const ExTables& t, int E, int ct, int 
 // The tiles of this CTA (or pair), every nth of n, row tiles fastest: the CTAs
 // at work share few activation rows and each weight is read once.
 struct ExWalk {
-    int ct, rt, dct, drt, RT;
-    __device__ __forceinline__ ExWalk(int me, int n, int row_tiles) : RT(row_tiles) {
-        ct = me / RT;
-        rt = me - ct * RT;
-        dct = n / RT;
-        drt = n - dct * RT;
-    }
+    int ct, rt, dct, drt, RT, end;
+    __device__ __forceinline__ ExWalk(int me, int n, int row_tiles)
+        : ct(me / row_tiles), rt(me - me / row_tiles * row_tiles), dct(n / row_tiles),
+          drt(n - n / row_tiles * row_tiles), RT(row_tiles), end(0) {}
+    __device__ __forceinline__ bool more() const { return ct < end; }
     __device__ __forceinline__ void next() {
         ct += dct;
         rt += drt;
@@ -305,7 +321,7 @@ struct ExWalk {
 template <bool FP4, int OP, bool PAIR>
 __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_constant__ ExpertArgs a) {
     constexpr int kExThreads = ex_threads(OP);
-    constexpr int W = FP4 ? 2 : 1;  // scale words (of 4 bytes) per row and stage
+    constexpr int W = FP4 ? 2 : 1;  // scale words (of 4 bytes) per row and k-block
     extern __shared__ __align__(16) unsigned char dsm[];
     __shared__ __align__(8) unsigned long long s_full[kExMaxStages], s_empty[kExMaxStages], s_tfull[2], s_tfree, s_drain;
     __shared__ uint32_t s_tmem;
@@ -317,24 +333,23 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
     const bool gather = OP == kExGateUp && a.gather;
     const int rank = PAIR ? (int)cluster_rank() : 0;
+    const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
 
     // ---- set-up that reads nothing of the kernel before
-    if (tid == 0) {
-        for (int s = 0; s < kExMaxStages; ++s) {
-            mbar_init(smem_u32(&s_full[s]), (gather ? 5 : 3) + (PAIR && rank == 0 ? 1 : 0));  // (one from the peer)
-            mbar_init(smem_u32(&s_empty[s]), 1);
-            if (OP == kExGateUp) {
-                mbar_init(smem_u32(&s_land[0][s]), 32);
-                mbar_init(smem_u32(&s_land[1][s]), 32);
-            }
+    if (tid < kExMaxStages) {
+        mbar_init(full0 + 8u * tid, (gather ? 5 : 3) + (PAIR && rank == 0 ? 1 : 0));  // (one from the peer)
+        mbar_init(empty0 + 8u * tid, 1);
+        if (OP == kExGateUp) {
+            mbar_init(smem_u32(&s_land[0][tid]), 32);
+            mbar_init(smem_u32(&s_land[1][tid]), 32);
         }
-        mbar_init(smem_u32(&s_tfull[0]), 1);
-        mbar_init(smem_u32(&s_tfull[1]), 1);
-        mbar_init(smem_u32(&s_tfree), PAIR ? 16 : 8);
-        mbar_init(smem_u32(&s_drain), 1);
+        if (tid < 2) mbar_init(smem_u32(&s_tfull[tid]), 1);
+        if (tid == 2) mbar_init(smem_u32(&s_tfree), PAIR ? 16 : 8);
+        if (tid == 3) mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        s_abort = 0;
-        s_nmax = 16;
+        if (tid == 4) s_abort = 0, s_nmax = 16;
+    }
+    if (tid == 64) {
         tma_prefetch_map(&a.tm_w);
         if (!gather) {
             tma_prefetch_map(&a.tm_x);
@@ -357,46 +372,42 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     t.first = reinterpret_cast<int*>(t.list + a.list_cap);
     t.rows = t.first + a.E;
     t.pre = t.rows + a.E;
-    for (int e = tid; e < a.E; e += kExThreads) {
-        t.first[e] = OP == kExGemm ? 0 : -1;
-        t.rows[e] = OP == kExGemm ? a.M : 0;
-    }
+    if (OP != kExGemm)
+        for (int e = tid; e < a.E; e += kExThreads) t.first[e] = -1, t.rows[e] = 0;
+    // a pair takes two row tiles at a time, one in each CTA
+    ExWalk walk((int)blockIdx.x >> (PAIR ? 1 : 0), (int)gridDim.x >> (PAIR ? 1 : 0), PAIR ? (a.RT + 1) >> 1 : a.RT);
     pdl_trigger();
     pdl_wait();
-    __syncthreads();
-
-    // ---- the experts' runs of blocks: first block and the block behind the last
     if (OP != kExGemm) {
-        for (int b = tid; b < a.nblk; b += kExThreads) {
-            const int e = a.experts[b];
-            const int before = b > 0 ? a.experts[b - 1] : -1, after = b < a.nblk - 1 ? a.experts[b + 1] : -1;
+        // ---- the experts' runs of blocks.  A thread reads a block's expert, its neighbours', and every 16th of its
+        // positions (the assignments of a block stand before its padding, so these tell to 16 rows where a run
+        // ends): independent loads, one latency
+        for (int b0 = 0; b0 < a.nblk; b0 += kExThreads) {
+            const int b = b0 + tid;
+            int e = -1, before = -1, after = -1, rows = a.block;
+            if (b < a.nblk) {
+                e = a.experts[b];
+                if (b > 0) before = a.experts[b - 1];
+                if (b + 1 < a.nblk) after = a.experts[b + 1];
+                const int32_t* s = a.sorted + (int64_t)b * a.block;
+#pragma unroll 4
+                for (int j = 16; j < a.block; j += 16)
+                    if (s[j] >= a.mk) rows = min(rows, j);
+            }
+            if (b0 == 0) __syncthreads();  // (the tables' initial values)
             if (e < 0 || e >= a.E) continue;
             if (before != e) t.first[e] = b * a.block;
-            if (after != e) t.rows[e] = b + 1;
-        }
-        __syncthreads();
-        for (int e = tid; e < a.E; e += kExThreads)
-            if (t.first[e] >= 0) t.rows[e] = max(t.rows[e] * a.block - t.first[e], 0);
-        // the assignments of a block stand before its padding: every 16th
-        // entry of a run's last block tells where the run's rows may end
-        const int probes = (a.block - 1) / 16;
-        if (probes > 0) {
-            __syncthreads();
-            for (int i = tid; i < a.E * probes; i += kExThreads) {
-                const int e = i / probes, j = (i - e * probes + 1) * 16, f = t.first[e];
-                if (f < 0) continue;
-                // the run's end: a cut leaves at least 16 rows of its last block
-                const int last = (f + t.rows[e] + a.block - 1) / a.block * a.block - a.block;
-                if (last >= f && a.sorted[last + j] >= a.mk) atomicMin(&t.rows[e], last + j - f);
-            }
+            if (after != e) t.rows[e] = b * a.block + rows;
         }
         __syncthreads();
     }
-    {  // column tiles before each expert; the widest tile
+    if (OP != kExGemm) {  // column tiles before each expert; the widest tile
         int run = 0;
         for (int e0 = 0; e0 < a.E; e0 += kExThreads) {
             const int e = e0 + tid;
-            const int rows = e < a.E ? t.rows[e] : 0, c = ex_ncol(rows);
+            int rows = e < a.E ? t.rows[e] : 0;  // (the end of the expert's run so far)
+            if (e < a.E) t.rows[e] = rows = t.first[e] >= 0 ? max(rows - t.first[e], 0) : 0;
+            const int c = ex_ncol(rows);
             int v = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -404,7 +415,8 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 if (lane >= o) v += u;
             }
             if (lane == 31) s_warp[warp] = v;
-            if (c > 0) atomicMax(&s_nmax, ex_share<PAIR>(rows, c));
+            const int wide = __reduce_max_sync(kFull, c > 0 ? ex_share<PAIR>(rows, c) : 0);
+            if (lane == 0) atomicMax(&s_nmax, wide);
             __syncthreads();
             int before = run;
             for (int w = 0; w < kExThreads / 32; ++w) {
@@ -431,7 +443,8 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     else __syncthreads();
     tc_fence_after();
 
-    const int total = __shfl_sync(kFull, s_total, 0), xrows = __shfl_sync(kFull, s_nmax, 0);
+    const int total = OP == kExGemm ? ex_ncol(a.M) : __shfl_sync(kFull, s_total, 0);
+    const int xrows = OP == kExGemm ? ex_share<PAIR>(a.M, total) : __shfl_sync(kFull, s_nmax, 0);
     const bool listed = total <= a.list_cap;
     const int H = (xrows + 127) >> 7;  // 128-row groups of the activations' scales
     const uint32_t tmem = __shfl_sync(kFull, s_tmem, 0);
@@ -439,46 +452,51 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     const uint32_t dyn = smem_u32(dsm);
     const uint32_t base = (dyn + (uint32_t)a.list_cap * 8u + (uint32_t)(3 * a.E + 1) * 4u + 1023u) & ~1023u;
     const uint32_t code_bytes = (uint32_t)(kExWBytes + xrows * (PAIR ? 64 : 128)), sf_bytes = (uint32_t)(W * 512 * (1 + H));
-    const int nst = min(kExMaxStages, (int)((dyn + (uint32_t)kExSmemDyn - base) / (code_bytes + sf_bytes)));
-    const uint32_t sf_base = base + (uint32_t)nst * code_bytes;
-    const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
+    // k-blocks that fit, in stages of D: a stage has its waits and its arrivals whatever it holds
+    const int fit = (int)ex_div(dyn + (uint32_t)kExSmemDyn - base, code_bytes + sf_bytes);
+    const int D = fit >= 6 ? 2 : 1, nst = min(kExMaxStages, D == 2 ? fit >> 1 : fit);
+    const uint32_t stage_bytes = (uint32_t)D * code_bytes, sf_stage = (uint32_t)D * sf_bytes;
+    const uint32_t sf_base = base + (uint32_t)nst * stage_bytes;
+    walk.end = total;
     int st = 0;       // stage of the ring
     unsigned ph = 0;  // its phase
-    // a pair takes two row tiles at a time, one in each CTA
-    ExWalk walk((int)blockIdx.x >> (PAIR ? 1 : 0), (int)gridDim.x >> (PAIR ? 1 : 0), PAIR ? (a.RT + 1) >> 1 : a.RT);
-#define EX_TILE ex_tile<PAIR>(t, a.E, walk.ct, PAIR ? walk.rt * 2 + rank : walk.rt, listed)
+#define EX_TILE ex_tile<PAIR, OP>(t, a.E, walk.ct, PAIR ? walk.rt * 2 + rank : walk.rt, listed, a.M, xrows)
 
     if (warp == 0) {
         // ---- codes, and the weights' scales
         int issued = 0;
         bool ok = true;
-        for (; ok && walk.ct < total; walk.next()) {
+        for (; ok && walk.more(); walk.next()) {
             const ExTile o = EX_TILE;
             // (a pair's second row tile may lie past the weight: its codes read as zeros, and no scale is read there)
             const uint8_t* ws = a.w_scale + ((int64_t)o.e * a.RT + min(o.rt, a.RT - 1)) * a.KI * (W * 512);
             const int nx = PAIR ? o.n >> 1 : o.n, rx = o.r0 + rank * nx;  // this CTA's activation rows
             const unsigned tx = (unsigned)(kExWBytes + W * 512 + (gather ? 0 : nx * 128));
-            for (int ki = 0; ki < a.KI; ++ki) {
+            for (int ki = 0; ki < a.KI; ki += D) {
                 if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
                 }
-                const uint32_t full = full0 + 8u * st, wsm = base + (uint32_t)st * code_bytes;
+                const uint32_t full = full0 + 8u * st;
+                uint32_t wsm = base + (uint32_t)st * stage_bytes, ssm = sf_base + (uint32_t)st * sf_stage;
                 if (ex_elect()) {
-                    mbar_expect_tx(full, tx + (((a.flags & 2) && issued == 0) ? 16u : 0u));
-                    if (OP == kExGateUp) tma_load_5d(wsm, &a.tm_w, ki * 128, 0, 0, o.rt * 4, o.e, full);
-                    else tma_load_3d(wsm, &a.tm_w, ki * 128, o.rt * 128, o.e, full);
-                    bulk_load(sf_base + (uint32_t)st * sf_bytes, ws, W * 512, full);
-                    if (!gather) {
-                        int r = 0;
-                        for (; r + 64 <= nx; r += 64)
-                            tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x64, ki * 128, rx + r, full);
-                        for (; r < nx; r += 16)
-                            tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x, ki * 128, rx + r, full);
+                    const int nd = min(D, a.KI - ki);
+                    mbar_expect_tx(full, tx * nd + (((a.flags & 2) && issued == 0) ? 16u : 0u));
+                    for (int b = 0; b < nd; ++b, wsm += code_bytes, ssm += sf_bytes) {
+                        const int x = (ki + b) * 128;
+                        if (OP == kExGateUp) tma_load_5d(wsm, &a.tm_w, x, 0, 0, o.rt * 4, o.e, full);
+                        else tma_load_3d(wsm, &a.tm_w, x, o.rt * 128, o.e, full);
+                        bulk_load(ssm, ws + (int64_t)(ki + b) * (W * 512), W * 512, full);
+                        if (!gather) {
+                            int r = 0;
+                            for (; r + 64 <= nx; r += 64)
+                                tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x64, x, rx + r, full);
+                            for (; r < nx; r += 16)
+                                tma_load_2d(wsm + kExWBytes + (uint32_t)r * 128u, &a.tm_x, x, rx + r, full);
+                        }
                     }
                 }
                 __syncwarp();
-                ws += W * 512;
                 ++issued;
                 if (++st == nst) st = 0, ph ^= 1u;
             }
@@ -496,8 +514,8 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
         // ---- a pair's products are issued by its first CTA: told when this CTA's operands are in place
         bool ok = true;
         const uint32_t peer = map_rank(full0, 0);
-        for (; ok && walk.ct < total; walk.next()) {
-            for (int ki = 0; ki < a.KI; ++ki) {
+        for (; ok && walk.more(); walk.next()) {
+            for (int ki = 0; ki < a.KI; ki += D) {
                 if (!ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
@@ -511,7 +529,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
         // ---- products
         bool ok = true;
         const uint32_t sfa = tmem + kExSfCol, sfb = sfa + 4 * W;
-        for (int it = 0; ok && walk.ct < total; walk.next(), ++it) {
+        for (int it = 0; ok && walk.more(); walk.next(), ++it) {
             const ExTile o = EX_TILE;
             const uint32_t d = tmem + ((it & 1) ? kExBuf1 : 0);
             const uint32_t idesc = ex_idesc<FP4, PAIR>(o.n);
@@ -519,31 +537,34 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 ok = ex_wait(smem_u32(&s_tfree), (unsigned)(it - 1) & 1u, a.wait_ns, &s_abort);
                 tc_fence_after();
             }
-            for (int ki = 0; ok && ki < a.KI; ++ki) {
+            for (int ki = 0; ok && ki < a.KI; ki += D) {
                 if (!ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t wa = base + (uint32_t)st * code_bytes;
-                const uint32_t sa = sf_base + (uint32_t)st * sf_bytes;
+                uint32_t wa = base + (uint32_t)st * stage_bytes, sa = sf_base + (uint32_t)st * sf_stage;
                 if (ex_elect()) {
-                    const unsigned long long da = ex_desc(kExDescCodes, wa), db = ex_desc(kExDescCodes, wa + kExWBytes);
+                    const int nd = min(D, a.KI - ki);
+                    for (int b = 0; b < nd; ++b, wa += code_bytes, sa += sf_bytes) {
+                        const unsigned long long da = ex_desc(kExDescCodes, wa);
+                        const unsigned long long db = ex_desc(kExDescCodes, wa + kExWBytes);
 #pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        ex_copy_sf<PAIR>(sfa + 4 * w, sa + 512 * w);
-                        ex_copy_sf<PAIR>(sfb + 4 * w * H, sa + 512 * (W + w * H));
-                        if (o.n > 128) ex_copy_sf<PAIR>(sfb + 4 * w * H + 4, sa + 512 * (W + w * H) + 512);
-                    }
+                        for (int w = 0; w < W; ++w) {
+                            ex_copy_sf<PAIR>(sfa + 4 * w, sa + 512 * w);
+                            ex_copy_sf<PAIR>(sfb + 4 * w * H, sa + 512 * (W + w * H));
+                            if (o.n > 128) ex_copy_sf<PAIR>(sfb + 4 * w * H + 4, sa + 512 * (W + w * H) + 512);
+                        }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int w = FP4 ? j >> 1 : 0;
-                        const uint32_t sel = FP4 ? (uint32_t)(j & 1) * 2 : (uint32_t)j;
-                        ex_mma<FP4, PAIR>(d, da + 2 * j, db + 2 * j, idesc, sel, sfa + 4 * w, sfb + 4 * w * H,
-                                    ki > 0 || j > 0);
+                        for (int j = 0; j < 4; ++j) {
+                            const int w = FP4 ? j >> 1 : 0;
+                            const uint32_t sel = FP4 ? (uint32_t)(j & 1) * 2 : (uint32_t)j;
+                            ex_mma<FP4, PAIR>(d, da + 2 * j, db + 2 * j, idesc, sel, sfa + 4 * w, sfb + 4 * w * H,
+                                              ki > 0 || b > 0 || j > 0);
+                        }
                     }
                     ex_commit<PAIR>(empty0 + 8u * st);
-                    if (ki == a.KI - 1) ex_commit<PAIR>(smem_u32(&s_tfull[it & 1]));
+                    if (ki + D >= a.KI) ex_commit<PAIR>(smem_u32(&s_tfull[it & 1]));
                 }
                 __syncwarp();
                 if (++st == nst) st = 0, ph ^= 1u;
@@ -551,11 +572,11 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
         }
     } else if (warp == 2 || warp == 3) {
         // ---- the activations' scales, as [32 rows][4 groups of 32 rows] words: one warp for rows 0-127 of the
-        // tile, one for rows 128-255.  16 bytes of each row are read at a time (B stages), one time ahead.
+        // tile, one for rows 128-255.  16 bytes of each row are read at a time (B k-blocks), one time ahead.
         bool ok = true;
         constexpr int B = 4 / W;
         const int half = warp == 2 ? 0 : 1;
-        for (; ok && walk.ct < total; walk.next()) {
+        for (; ok && walk.more(); walk.next()) {
             const ExTile o = EX_TILE;
             const uint8_t* row[4];
             const int G = max(0, min(4, ((o.n + 31) >> 5) - 4 * half));  // groups of 32 rows that are this warp's
@@ -602,9 +623,11 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
 #pragma unroll
                 for (int s = 0; s < B; ++s) {
                     if (k0 + s >= a.KI) return true;
-                    if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) return false;
-                    const uint32_t sb = sf_base + (uint32_t)st * sf_bytes + (W + half) * 512 + 16u * lane;
+                    const int b = D == 2 ? (k0 + s) & 1 : 0;  // its place in the stage
+                    if (b == 0 && !ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) return false;
                     if (G > 0) {
+                        const uint32_t sb = sf_base + (uint32_t)st * sf_stage + (uint32_t)b * sf_bytes +
+                                            (W + half) * 512 + 16u * lane;
 #pragma unroll
                         for (int w = 0; w < W; ++w) {
                             const int i = s * W + w;
@@ -613,8 +636,9 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                                          "r"(word(v[0])), "r"(word(v[1])), "r"(word(v[2])), "r"(word(v[3]))
                                          : "memory");
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
+                    if (b != D - 1 && k0 + s + 1 < a.KI) continue;
+                    if (G > 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full0 + 8u * st);
                     if (++st == nst) st = 0, ph ^= 1u;
@@ -646,7 +670,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
         int f[4];  // assignments of the tile's rows 8 i + 4 which + 0..3, i < 32 (those of this CTA)
         ExTile o{};
         auto fetch = [&] {
-            if (!ok || walk.ct >= total) return;
+            if (!ok || !walk.more()) return;
             o = EX_TILE;
             const int nx = PAIR ? o.n >> 1 : o.n;
 #pragma unroll
@@ -663,7 +687,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             --late;
         };
         fetch();
-        while (ok && walk.ct < total) {
+        while (ok && walk.more()) {
             const int nx = PAIR ? o.n >> 1 : o.n;
             __syncwarp();
 #pragma unroll
@@ -672,7 +696,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             __syncwarp();
             walk.next();
             fetch();  // the next tile's, while this one is copied
-            for (int ki = 0; ok && ki < a.KI; ++ki) {
+            for (int ki = 0; ok && ki < a.KI; ki += D) {
                 unsigned long long t0 = 0;
                 for (int turn = 1; !__all_sync(kFull, mbar_test(empty0 + 8u * st, ph ^ 1u)); ++turn) {
                     if (late > 0 && __all_sync(kFull, mbar_test(land0 + 8u * lst, lph))) {
@@ -691,12 +715,17 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                     }
                 }
                 if (!ok) break;
-                const uint32_t xsm = base + (uint32_t)st * code_bytes + kExWBytes;
-                const int at = ki * 128 + chunk * 16, bytes = at < a.kbytes ? 16 : 0;
-                const uint8_t* x = a.x + (bytes ? at : 0);
-                for (int i = quad; i < nx / 2; i += 4) {
-                    const int r = (i >> 2) * 8 + which * 4 + quad;
-                    ex_cp_async16(xsm + (uint32_t)(r * 128 + ((chunk ^ (r & 7)) << 4)), x + (int64_t)tok[i] * a.ldx, bytes);
+                const int nd = min(D, a.KI - ki);
+                for (int b = 0; b < nd; ++b) {
+                    const uint32_t xsm = base + (uint32_t)st * stage_bytes + (uint32_t)b * code_bytes + kExWBytes;
+                    const int at = (ki + b) * 128 + chunk * 16, bytes = at < a.kbytes ? 16 : 0;
+                    const uint8_t* x = a.x + (bytes ? at : 0);
+#pragma unroll 4
+                    for (int i = quad; i < nx / 2; i += 4) {
+                        const int r = (i >> 2) * 8 + which * 4 + quad;
+                        ex_cp_async16(xsm + (uint32_t)(r * 128 + ((chunk ^ (r & 7)) << 4)), x + (int64_t)tok[i] * a.ldx,
+                                      bytes);
+                    }
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(land0 + 8u * st) : "memory");
                 ++late;
@@ -716,7 +745,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             if (PAIR) mbar_arrive_remote(tfree);
             else mbar_arrive(tfree);
         };
-        for (int it = 0; walk.ct < total; walk.next(), ++it) {
+        for (int it = 0; walk.more(); walk.next(), ++it) {
             const ExTile o = EX_TILE;
             int* f = s_f[it & 1];
             if (OP != kExGemm && et < o.n) f[et] = et < o.rows ? a.sorted[o.r0 + et] : a.mk;

@@ -20,23 +20,16 @@ inline ExpertShape expert_shape(int R, int K, bool fp4, bool gate_up) {
     return s;
 }
 
-// Scratch behind the counter prefix (32 KiB, zero between calls): two partial
-// tiles of 128 rows x the widest column tile per CTA (an expert has at most mk
-// rows, mk the assignments of the call), then the down products [mk][R] in
-// bf16.
-constexpr int kExMaxCtas = 160;
-inline size_t expert_part_bytes(int64_t mk) {
-    const int64_t n = mk >= 256 ? 256 : (mk + 15) / 16 * 16;
-    return (size_t)(kExMaxCtas * 2 * 128 * 4) * (size_t)n;
-}
-inline size_t expert_scratch_bytes(int64_t mk, int R) {
-    return 32768 + expert_part_bytes(mk) + ((size_t)mk * (size_t)R * 2 + 255) / 256 * 256;
-}
+// Scratch of a down call: its products of mk assignments in bf16, rows of R.
+inline size_t expert_scratch_bytes(int64_t mk, int R) { return ((size_t)mk * (size_t)R * 2 + 255) / 256 * 256; }
 
-// Whether two CTAs share their activation rows (256 weight rows a tile):
-// where an expert has 16 rows or more on average (256 tokens x 8 over 128
-// experts, E4M3 gate/up: 199 us as pairs, 252 alone).
-inline bool expert_pair(int64_t mk, int E) { return mk >= 16 * (int64_t)E; }
+// Whether two CTAs share their activation rows (256 weight rows a tile): where
+// an expert has 16 rows or more on average (256 tokens x 8 over 128 experts,
+// E4M3 gate/up: 199 us as pairs, 252 alone) and there is a tile for every CTA.
+inline bool expert_pair(int64_t mk, int E, int RT, int ctas) {
+    const int64_t tiles = ((mk < E ? mk : E) + mk / 256) * RT;
+    return mk >= 16 * (int64_t)E && tiles >= ctas;
+}
 
 // One launch of the expert kernel (op: 0 gemm, 1 gate/up, 2 down).
 struct ExpertCall {

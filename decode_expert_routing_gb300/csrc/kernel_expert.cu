@@ -182,7 +182,8 @@ cudaError_t launch_one(const ExpertArgs& a, int grid, cudaStream_t st) {
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = (launch_flags() & 1) ? 1 : 0;
+    // whatever the launch options: the kernel reads and writes nothing before it has waited for the one before it
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = 2;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
@@ -255,16 +256,16 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
         if (a.kb % v == 0 && c.lds % v == 0 && reinterpret_cast<uintptr_t>(c.x_scale) % v == 0) a.sf_vec = v;
     {  // column tiles: one per expert with rows, and one for every further 256 rows
         const int64_t mk = (int64_t)c.M * c.topk, most = (mk < c.E ? mk : c.E) + mk / kExMaxN + 1;
-        a.list_cap = most <= kExListMax ? (int)most : 0;
+        a.list_cap = c.op != kExGemm && most <= kExListMax ? (int)most : 0;
     }
     a.out_fmt = c.out_fmt;
     a.flags = launch_flags();
     a.x = c.x;
     a.ldx = c.ldx;
     a.kbytes = (int)kbytes;
-    if (c.op == kExDown) a.out = static_cast<char*>(c.scratch) + kWorkOffset + expert_part_bytes(a.mk);
-    const int grid = sms < kExMaxCtas ? sms : kExMaxCtas;
-    const bool pair = expert_pair(a.mk, c.E);
+    if (c.op == kExDown) a.out = c.scratch;
+    const int grid = sms;
+    const bool pair = expert_pair(a.mk, c.E, s.RT, sms);
     cudaError_t e = c.op == kExGemm     ? launch_op<kExGemm>(a, fp4, pair, grid, st)
                           : c.op == kExGateUp ? launch_op<kExGateUp>(a, fp4, pair, grid, st)
                                               : launch_op<kExDown>(a, fp4, pair, grid, st);

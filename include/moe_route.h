@@ -529,15 +529,13 @@ int mr_mx_pack_scales(const uint8_t *scale, int E, int R, int K, int format, int
                       void *stream);
 
 /*
- * Scratch bytes for calls of up to M_max rows and top-k slots: of
- * mr_moe_down with R output columns (down != 0), or of mr_mx_gemm (topk 1)
- * and mr_moe_gate_up (down == 0, R ignored).  The first
- * MR_SCRATCH_COUNTER_BYTES hold counters; the rules of every scratch buffer
- * hold (zeroed once, then left reusable; not shared by calls that may run
- * concurrently, captured graphs among them).  Returns 0 for out-of-range
- * arguments.  Pure host function.
+ * Scratch bytes of mr_moe_down for up to M_max tokens of topk slots and R
+ * output columns: the products of every slot on their way to the sum.  The
+ * buffer need not be zeroed and holds nothing between calls; calls that may
+ * run concurrently (captured graphs among them) must not share it.  Returns 0
+ * for out-of-range arguments.  Pure host function.
  */
-size_t mr_expert_scratch_bytes(int M_max, int topk, int R, int down);
+size_t mr_expert_scratch_bytes(int M_max, int topk, int R);
 
 /*
  * Product of microscaled operands:
@@ -558,8 +556,6 @@ typedef struct mr_mx_gemm_params {
     void *out;
     int64_t ldo;
     int out_fp32;
-    void *scratch;
-    size_t scratch_bytes;
 } mr_mx_gemm_params;
 int mr_mx_gemm(const mr_mx_gemm_params *params, void *stream);
 
@@ -597,8 +593,6 @@ typedef struct mr_moe_gate_up_params {
     int out_format;
     void *act;
     uint8_t *act_scale;
-    void *scratch;
-    size_t scratch_bytes;
 } mr_moe_gate_up_params;
 int mr_moe_gate_up(const mr_moe_gate_up_params *params, void *stream);
 
@@ -612,7 +606,8 @@ int mr_moe_gate_up(const mr_moe_gate_up_params *params, void *stream);
  * nothing); w2: [E, R, I].  Slots whose id in topk_ids is outside [0, E) add
  * nothing; a token without any gives add, or zero.  topk_ids, topk_weights:
  * [M, topk]; add: bf16 [M, R] or NULL; out: bf16 [M, R], may be add itself.
- * scratch: mr_expert_scratch_bytes(M, topk, R, 1).  Two launches.
+ * scratch: mr_expert_scratch_bytes(M, topk, R), 256-byte aligned.  Two
+ * launches.
  */
 typedef struct mr_moe_down_params {
     const uint8_t *q;
