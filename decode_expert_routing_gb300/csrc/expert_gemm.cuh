@@ -418,12 +418,9 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             const int wide = __reduce_max_sync(kFull, c > 0 ? ex_share<PAIR>(rows, c) : 0);
             if (lane == 0) atomicMax(&s_nmax, wide);
             __syncthreads();
-            int before = run;
-            for (int w = 0; w < kExThreads / 32; ++w) {
-                if (w < warp) before += s_warp[w];
-                run += s_warp[w];
-            }
-            before += v - c;
+            const int of_warp = lane < kExThreads / 32 ? s_warp[lane] : 0;
+            const int before = run + (int)__reduce_add_sync(kFull, lane < warp ? of_warp : 0) + v - c;
+            run += (int)__reduce_add_sync(kFull, of_warp);
             if (e < a.E) {
                 t.pre[e] = before;
                 for (int i = 0; i < c && before + i < a.list_cap; ++i) {
