@@ -47,6 +47,7 @@ constexpr int kExMaxN = 256;             // activation rows of a tile
 constexpr int kExWBytes = 128 * 128;     // weight codes of one k-block (128 bytes a row)
 constexpr int kExSmemDyn = 214 * 1024;   // dynamic shared memory (one CTA per SM)
 constexpr int kExListMax = 1536;        // column tiles in the shared list
+constexpr int kExFewRows = 4;           // rows in token order that are copied one by one
 constexpr int kExSfCol = 488;            // tensor-memory columns of the scale factors
 constexpr int kExBuf1 = 232;             // first column of the second accumulator
 // The two accumulators share columns 232-255 (256 + 256 + 24 columns of
@@ -58,7 +59,7 @@ enum { kExGemm = 0, kExGateUp = 1, kExDown = 2 };
 
 struct ExpertArgs {
     CUtensorMap tm_w;        // weight codes, box of 128 rows x 128 bytes
-    CUtensorMap tm_x;        // activation codes, box of 16 rows x 128 bytes (not with gather)
+    CUtensorMap tm_x;        // activation codes, box of 16 rows (gather: 1 row) x 128 bytes
     CUtensorMap tm_x64;      // the same in boxes of 64 rows
     const uint8_t* w_scale;  // packed: [E][row tile][k-block][512 * words]
     const uint8_t* x_scale;  // [rows][lds] bytes
@@ -351,10 +352,8 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     }
     if (tid == 64) {
         tma_prefetch_map(&a.tm_w);
-        if (!gather) {
-            tma_prefetch_map(&a.tm_x);
-            tma_prefetch_map(&a.tm_x64);
-        }
+        tma_prefetch_map(&a.tm_x);
+        if (!gather) tma_prefetch_map(&a.tm_x64);
     }
     if (warp == 1) {
         if (PAIR) {
@@ -656,7 +655,9 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
         // ---- codes of rows in token order: two warps, four rows (of 128 bytes) of every eight each.  A stage's
         // copies arrive on a barrier of the warp; once they are there the warp passes the stage on (the proxy fence
         // has to be its own), in between waiting for the next stage to come free.
-        // (Four-row tensor-map gathers took some 90 cycles each: 495 instead of 350 us for 1001 tokens.)
+        // (Four-row tensor-map gathers took some 90 cycles each: 495 instead of 350 us for 1001 tokens.)  A tile of
+        // up to four rows, as decode steps have them, takes a tensor-map copy of each instead, which counts on the
+        // stage's own barrier without the detour by the warp (one token's gate/up: 17.0 instead of 20.7 us).
         const int which = warp - 12;
         int* tok = s_tok[which];
         const int quad = lane >> 3, chunk = lane & 7;  // this lane's row of four and 16-byte chunk
@@ -665,6 +666,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
         int late = 0, lst = 0;  // stages not passed on yet, and the first of them
         unsigned lph = 0;
         int f[4];  // assignments of the tile's rows 8 i + 4 which + 0..3, i < 32 (those of this CTA)
+        int f16 = 0;  // (a tile of 16 columns) the assignment of row lane
         ExTile o{};
         auto fetch = [&] {
             if (!ok || !walk.more()) return;
@@ -675,6 +677,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 const int i = lane + 32 * u, r = rank * nx + (i >> 2) * 8 + which * 4 + (i & 3);
                 f[u] = i < nx / 2 && r < o.rows ? a.sorted[o.r0 + r] : 0;
             }
+            f16 = !PAIR && o.n == 16 && lane < o.rows ? a.sorted[o.r0 + lane] : a.mk;
         };
         auto pass_on = [&] {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -691,8 +694,40 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             for (int u = 0; u < 4; ++u)  // (positions past the real ones take any token: their columns are not used)
                 if (lane + 32 * u < nx / 2) tok[lane + 32 * u] = (unsigned)f[u] < (unsigned)a.mk ? f[u] / a.topk : 0;
             __syncwarp();
+            const bool mine = (unsigned)f16 < (unsigned)a.mk;
+            const unsigned real = __ballot_sync(kFull, mine);
+            const bool few = !PAIR && o.n == 16 && __popc(real) <= kExFewRows;
+            const int token = mine ? f16 / a.topk : 0;
             walk.next();
             fetch();  // the next tile's, while this one is copied
+            if (few) {
+                while (ok && late > 0) {
+                    ok = ex_wait(land0 + 8u * lst, lph, a.wait_ns, &s_abort);
+                    if (ok) pass_on();
+                }
+                for (int ki = 0; ok && ki < a.KI; ki += D) {
+                    if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = full0 + 8u * st, xsm = base + (uint32_t)st * stage_bytes + kExWBytes;
+                    const int nd = min(D, a.KI - ki);
+                    if (which == 0) {
+                        if (lane == 0) mbar_expect_tx(full, (unsigned)(__popc(real) * nd * 128));
+                        __syncwarp();
+                        if (mine)
+                            for (int b = 0; b < nd; ++b)
+                                tma_load_2d(xsm + (uint32_t)b * code_bytes + (uint32_t)lane * 128u, &a.tm_x,
+                                            (ki + b) * 128, token, full);
+                    } else if (lane == 0) {
+                        mbar_arrive(full);
+                    }
+                    mbar_arrive(land0 + 8u * st);  // (every stage is a phase of this barrier too)
+                    __syncwarp();
+                    if (++st == nst) st = 0, ph ^= 1u;
+                }
+                continue;
+            }
             for (int ki = 0; ok && ki < a.KI; ki += D) {
                 unsigned long long t0 = 0;
                 for (int turn = 1; !__all_sync(kFull, mbar_test(empty0 + 8u * st, ph ^ 1u)); ++turn) {
@@ -725,7 +760,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                     }
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(land0 + 8u * st) : "memory");
-                ++late;
+                if (late++ == 0) lst = st, lph = ph;
                 if (__all_sync(kFull, mbar_test(land0 + 8u * lst, lph))) pass_on();
                 if (++st == nst) st = 0, ph ^= 1u;
             }

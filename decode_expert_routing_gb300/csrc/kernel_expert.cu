@@ -227,8 +227,9 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
         }
         const cuuint64_t dims[2] = {kbytes, (cuuint64_t)c.x_rows};
         const cuuint64_t strides[1] = {(cuuint64_t)c.ldx};
-        const cuuint32_t box[2] = {128, 16}, box64[2] = {128, 64};
-        if (!c.gather && (!encode(&a.tm_x, c.x, 2, dims, strides, box) || !encode(&a.tm_x64, c.x, 2, dims, strides, box64)))
+        const cuuint32_t box[2] = {128, c.gather ? 1u : 16u}, box64[2] = {128, 64};
+        if (!encode(&a.tm_x, c.x, 2, dims, strides, box) ||
+            (!c.gather && !encode(&a.tm_x64, c.x, 2, dims, strides, box64)))
             return MR_ERR_UNSUPPORTED;
     }
     a.w_scale = c.w_scale;
