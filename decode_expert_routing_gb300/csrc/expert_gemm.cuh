@@ -14,7 +14,7 @@
 // bytes of codes a row (128 E4M3 or 256 E2M1 elements); a stage of the ring is
 // two of them while three such stages fit, else one.  One CTA per SM
 // walks the tiles.  Warp 0 copies the codes (tensor maps, 128-byte swizzle) and
-// the weights' scales (laid out once, see mx_pack_kernel), two warps the codes
+// the weights' scales (laid out once, see mx_pack_kernel), four warps the codes
 // of rows in token order, two the activations' scales (into the weights' scale
 // layout), warp 1 copies scales to tensor memory and issues the products, and
 // warps 4-11 read the accumulator back while the next tile is computed into
@@ -40,12 +40,12 @@
 
 namespace mr {
 
-// Warps: 0 copies, 1 products, 2-3 scales, 4-11 read back, and for gate/up 12-13 gather.
-__host__ __device__ constexpr int ex_threads(int op) { return op == 1 ? 448 : 384; }
+// Warps: 0 copies, 1 products, 2-3 scales, 4-11 read back, and for gate/up 12-15 gather.
+__host__ __device__ constexpr int ex_threads(int op) { return op == 1 ? 512 : 384; }
 constexpr int kExMaxStages = 12;
 constexpr int kExMaxN = 256;             // activation rows of a tile
 constexpr int kExWBytes = 128 * 128;     // weight codes of one k-block (128 bytes a row)
-constexpr int kExSmemDyn = 214 * 1024;   // dynamic shared memory (one CTA per SM)
+constexpr int kExSmemDyn = 211 * 1024;   // dynamic shared memory (one CTA per SM)
 constexpr int kExListMax = 1536;        // column tiles in the shared list
 constexpr int kExFewRows = 4;           // rows in token order that are copied one by one
 constexpr int kExSfCol = 488;            // tensor-memory columns of the scale factors
@@ -89,18 +89,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, unsigned parity) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// The same without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, unsigned parity) {
-    unsigned ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -328,8 +316,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_total, s_nmax, s_warp[kExThreads / 32];
     __shared__ __align__(16) int s_f[2][OP == kExGemm ? 4 : kExMaxN];
-    __shared__ __align__(8) unsigned long long s_land[2][OP == kExGateUp ? kExMaxStages : 1];  // gathered codes are there
-    __shared__ int s_tok[2][OP == kExGateUp ? kExMaxN / 2 : 1];  // tokens of the rows that a warp gathers
+    __shared__ int s_tok[4][OP == kExGateUp ? kExMaxN : 1];  // (each gathering warp) tokens of the tile's rows
     __shared__ __align__(16) unsigned char s_act[OP == kExGateUp ? 4 * 16 * kExStagePitch : 16];
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
     const bool gather = OP == kExGateUp && a.gather;
@@ -338,12 +325,8 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
 
     // ---- set-up that reads nothing of the kernel before
     if (tid < kExMaxStages) {
-        mbar_init(full0 + 8u * tid, (gather ? 5 : 3) + (PAIR && rank == 0 ? 1 : 0));  // (one from the peer)
+        mbar_init(full0 + 8u * tid, (gather ? 4 : 3) + (PAIR && rank == 0 ? 1 : 0));  // (one from the peer)
         mbar_init(empty0 + 8u * tid, 1);
-        if (OP == kExGateUp) {
-            mbar_init(smem_u32(&s_land[0][tid]), 32);
-            mbar_init(smem_u32(&s_land[1][tid]), 32);
-        }
         if (tid < 2) mbar_init(smem_u32(&s_tfull[tid]), 1);
         if (tid == 2) mbar_init(smem_u32(&s_tfree), PAIR ? 16 : 8);
         if (tid == 3) mbar_init(smem_u32(&s_drain), 1);
@@ -652,121 +635,83 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             }
         }
     } else if (OP == kExGateUp && warp >= 12) {
-        // ---- codes of rows in token order: two warps, four rows (of 128 bytes) of every eight each.  A stage's
-        // copies arrive on a barrier of the warp; once they are there the warp passes the stage on (the proxy fence
-        // has to be its own), in between waiting for the next stage to come free.
-        // (Four-row tensor-map gathers took some 90 cycles each: 495 instead of 350 us for 1001 tokens.)  A tile of
-        // up to four rows, as decode steps have them, takes a tensor-map copy of each instead, which counts on the
-        // stage's own barrier without the detour by the warp (one token's gate/up: 17.0 instead of 20.7 us).
-        const int which = warp - 12;
+        // ---- codes of rows in token order: the stages in turn, one of up to four warps each, which copies the rows
+        // (16 bytes a lane), waits for them and passes the stage on; the others' stages are under way meanwhile.
+        // (With more of them in flight in one warp its proxy fence, which has to be its own, waits for all.)  A tile
+        // of up to four rows, as decode steps have them, takes a tensor-map copy of each instead, which counts on
+        // the stage's own barrier (one token's gate/up: 17.0 instead of 20.7 us).
+        // At most nst warps: the one before it in a warp's turn tells that a stage's slot is at most one use behind,
+        // as a wait by parity needs it.
+        const int takers = min(4, nst), which = warp - 12;
         int* tok = s_tok[which];
         const int quad = lane >> 3, chunk = lane & 7;  // this lane's row of four and 16-byte chunk
-        const uint32_t land0 = smem_u32(&s_land[which][0]);
-        bool ok = gather;
-        int late = 0, lst = 0;  // stages not passed on yet, and the first of them
-        unsigned lph = 0;
-        int f[4];  // assignments of the tile's rows 8 i + 4 which + 0..3, i < 32 (those of this CTA)
-        int f16 = 0;  // (a tile of 16 columns) the assignment of row lane
+        bool ok = gather && which < takers;
+        int turn = 0;  // whose stage is next
+        int f[8];      // assignments of this CTA's rows lane, lane + 32, ...
         ExTile o{};
         auto fetch = [&] {
             if (!ok || !walk.more()) return;
             o = EX_TILE;
             const int nx = PAIR ? o.n >> 1 : o.n;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = lane + 32 * u, r = rank * nx + (i >> 2) * 8 + which * 4 + (i & 3);
-                f[u] = i < nx / 2 && r < o.rows ? a.sorted[o.r0 + r] : 0;
+            for (int u = 0; u < 8; ++u) {
+                const int i = lane + 32 * u, r = rank * nx + i;
+                f[u] = i < nx && r < o.rows ? a.sorted[o.r0 + r] : a.mk;
             }
-            f16 = !PAIR && o.n == 16 && lane < o.rows ? a.sorted[o.r0 + lane] : a.mk;
-        };
-        auto pass_on = [&] {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full0 + 8u * lst);
-            if (++lst == nst) lst = 0, lph ^= 1u;
-            --late;
         };
         fetch();
         while (ok && walk.more()) {
             const int nx = PAIR ? o.n >> 1 : o.n;
-            __syncwarp();
-#pragma unroll
-            for (int u = 0; u < 4; ++u)  // (positions past the real ones take any token: their columns are not used)
-                if (lane + 32 * u < nx / 2) tok[lane + 32 * u] = (unsigned)f[u] < (unsigned)a.mk ? f[u] / a.topk : 0;
-            __syncwarp();
-            const bool mine = (unsigned)f16 < (unsigned)a.mk;
+            // (positions past the real ones take any token: their columns are not used)
+            const bool mine = (unsigned)f[0] < (unsigned)a.mk;
+            const int token = mine ? f[0] / a.topk : 0;
             const unsigned real = __ballot_sync(kFull, mine);
             const bool few = !PAIR && o.n == 16 && __popc(real) <= kExFewRows;
-            const int token = mine ? f16 / a.topk : 0;
+            if (!few) {
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (lane + 32 * u < nx) tok[lane + 32 * u] = (unsigned)f[u] < (unsigned)a.mk ? f[u] / a.topk : 0;
+                __syncwarp();
+            }
             walk.next();
             fetch();  // the next tile's, while this one is copied
-            if (few) {
-                while (ok && late > 0) {
-                    ok = ex_wait(land0 + 8u * lst, lph, a.wait_ns, &s_abort);
-                    if (ok) pass_on();
-                }
-                for (int ki = 0; ok && ki < a.KI; ki += D) {
+            for (int ki = 0; ok && ki < a.KI; ki += D) {
+                if (turn == which) {
                     if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t full = full0 + 8u * st, xsm = base + (uint32_t)st * stage_bytes + kExWBytes;
+                    const uint32_t full = full0 + 8u * st, xst = base + (uint32_t)st * stage_bytes + kExWBytes;
                     const int nd = min(D, a.KI - ki);
-                    if (which == 0) {
+                    if (few) {
                         if (lane == 0) mbar_expect_tx(full, (unsigned)(__popc(real) * nd * 128));
                         __syncwarp();
                         if (mine)
                             for (int b = 0; b < nd; ++b)
-                                tma_load_2d(xsm + (uint32_t)b * code_bytes + (uint32_t)lane * 128u, &a.tm_x,
+                                tma_load_2d(xst + (uint32_t)b * code_bytes + (uint32_t)lane * 128u, &a.tm_x,
                                             (ki + b) * 128, token, full);
-                    } else if (lane == 0) {
-                        mbar_arrive(full);
-                    }
-                    mbar_arrive(land0 + 8u * st);  // (every stage is a phase of this barrier too)
-                    __syncwarp();
-                    if (++st == nst) st = 0, ph ^= 1u;
-                }
-                continue;
-            }
-            for (int ki = 0; ok && ki < a.KI; ki += D) {
-                unsigned long long t0 = 0;
-                for (int turn = 1; !__all_sync(kFull, mbar_test(empty0 + 8u * st, ph ^ 1u)); ++turn) {
-                    if (late > 0 && __all_sync(kFull, mbar_test(land0 + 8u * lst, lph))) {
-                        pass_on();
-                        continue;
-                    }
-                    if ((turn & 63) != 0) continue;
-                    if (t0 == 0) t0 = global_ns();
-                    if (__any_sync(kFull, global_ns() - t0 >= a.wait_ns)) {
-                        *(volatile int*)&s_abort = 1;
-                        atomicExch(&g_ex_timeout, 1);
-                    }
-                    if (__any_sync(kFull, *(volatile int*)&s_abort != 0)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                if (!ok) break;
-                const int nd = min(D, a.KI - ki);
-                for (int b = 0; b < nd; ++b) {
-                    const uint32_t xsm = base + (uint32_t)st * stage_bytes + (uint32_t)b * code_bytes + kExWBytes;
-                    const int at = (ki + b) * 128 + chunk * 16, bytes = at < a.kbytes ? 16 : 0;
-                    const uint8_t* x = a.x + (bytes ? at : 0);
+                        __syncwarp();
+                    } else {
+                        for (int b = 0; b < nd; ++b) {
+                            const uint32_t xsm = xst + (uint32_t)b * code_bytes;
+                            const int at = (ki + b) * 128 + chunk * 16, bytes = at < a.kbytes ? 16 : 0;
+                            const uint8_t* x = a.x + (bytes ? at : 0);
 #pragma unroll 4
-                    for (int i = quad; i < nx / 2; i += 4) {
-                        const int r = (i >> 2) * 8 + which * 4 + quad;
-                        ex_cp_async16(xsm + (uint32_t)(r * 128 + ((chunk ^ (r & 7)) << 4)), x + (int64_t)tok[i] * a.ldx,
-                                      bytes);
+                            for (int r = quad; r < nx; r += 4)
+                                ex_cp_async16(xsm + (uint32_t)(r * 128 + ((chunk ^ (r & 7)) << 4)),
+                                              x + (int64_t)tok[r] * a.ldx, bytes);
+                        }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full);
                     }
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(land0 + 8u * st) : "memory");
-                if (late++ == 0) lst = st, lph = ph;
-                if (__all_sync(kFull, mbar_test(land0 + 8u * lst, lph))) pass_on();
+                if (++turn == takers) turn = 0;
                 if (++st == nst) st = 0, ph ^= 1u;
             }
         }
-        while (late > 0 && ex_wait(land0 + 8u * lst, lph, a.wait_ns, &s_abort)) pass_on();
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ---- accumulator -> outputs: warps 4-7 and 8-11 take alternate chunks of 16 columns
         const int wq = warp & 3, grp = (warp >> 2) - 1, et = tid - 128, gt = et & 127;
