@@ -62,7 +62,7 @@ struct ExpertArgs {
     CUtensorMap tm_x;        // activation codes, box of 16 rows (gather: 1 row) x 128 bytes
     CUtensorMap tm_x64;      // the same in boxes of 64 rows
     const uint8_t* w_scale;  // packed: [E][row tile][k-block][512 * words]
-    const uint8_t* x_scale;  // [rows][lds] bytes
+    const uint8_t *x_scale, *x_scale_end;  // [rows][lds] bytes
     int64_t lds;
     const int32_t* sorted;   // [cap] assignment of a sorted position
     const int32_t* experts;  // [nblk] expert of a block
@@ -74,8 +74,9 @@ struct ExpertArgs {
     unsigned long long wait_ns;
     int E, R, RT, KI, kb, kbytes;  // weight rows, row tiles, k-blocks, scale and code bytes per row
     int M, topk, mk, nblk, block;
+    int per;                 // kExGemm: rows of a column tile
     int gather;              // x rows in token order
-    int sf_vec;              // bytes that the scale rows can be read in: 16, 8, 4 or 1
+    int sf_vec;              // bytes that the scale rows can be read in: 16, 8, else any
     int list_cap;            // column tiles that the shared list holds (0: none, they are searched for)
     int out_fmt;             // 0 bf16, 1 MXFP8, 2 MXFP4, 3 fp32
     int flags;
@@ -265,7 +266,7 @@ template <bool PAIR, int OP>
 __device__ __forceinline__ ExTile ex_tile(const ExTables& t, int E, int ct, int rt, bool listed, int M, int per_gemm) {
     ExTile o;
     o.rt = rt;
-    if (OP == kExGemm) {  // one expert, equal shares
+    if (OP == kExGemm) {  // one expert, tiles of per rows
         o.e = 0;
         o.r0 = ct * per_gemm;
         o.rows = min(per_gemm, M - o.r0);
@@ -422,8 +423,8 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     else __syncthreads();
     tc_fence_after();
 
-    const int total = OP == kExGemm ? ex_ncol(a.M) : __shfl_sync(kFull, s_total, 0);
-    const int xrows = OP == kExGemm ? ex_share<PAIR>(a.M, total) : __shfl_sync(kFull, s_nmax, 0);
+    const int total = OP == kExGemm ? (a.M + a.per - 1) / a.per : __shfl_sync(kFull, s_total, 0);
+    const int xrows = OP == kExGemm ? a.per : __shfl_sync(kFull, s_nmax, 0);
     const bool listed = total <= a.list_cap;
     const int H = (xrows + 127) >> 7;  // 128-row groups of the activations' scales
     const uint32_t tmem = __shfl_sync(kFull, s_tmem, 0);
@@ -583,18 +584,31 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                         if (b + 8 < a.kb) hi = __ldg(reinterpret_cast<const uint2*>(row[g] + b + 8));
                         v[g] = make_uint4(lo.x, lo.y, hi.x, hi.y);
                     } else {
-                        uint32_t x[4] = {0u, 0u, 0u, 0u};
+                        // from the five words around them (of which only the bytes of the scales are read at the
+                        // ends of the array)
+                        const uint8_t* at = row[g] + b;
+                        const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(at) & 3u);
+                        uint32_t x[5];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int at = b + 4 * i;
-                            if (a.sf_vec == 4) {
-                                if (at < a.kb) x[i] = __ldg(reinterpret_cast<const uint32_t*>(row[g] + at));
+                        for (int i = 0; i < 5; ++i) {
+                            const uint8_t* p = at - off + 4 * i;
+                            x[i] = 0u;
+                            if (b + 4 * i - (int)off >= a.kb) continue;
+                            if (p >= a.x_scale && p + 4 <= a.x_scale_end) {
+                                x[i] = __ldg(reinterpret_cast<const uint32_t*>(p));
                             } else {
                                 for (int u = 0; u < 4; ++u)
-                                    if (at + u < a.kb) x[i] |= (uint32_t)__ldg(row[g] + at + u) << (8 * u);
+                                    if (p + u >= a.x_scale && p + u < a.x_scale_end) x[i] |= (uint32_t)__ldg(p + u) << (8 * u);
                             }
                         }
-                        v[g] = make_uint4(x[0], x[1], x[2], x[3]);
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int left = a.kb - b - 4 * i;  // scales of the row from here on
+                            w[i] = __funnelshift_r(x[i], x[i + 1], off * 8u);
+                            if (left < 4) w[i] = left <= 0 ? 0u : w[i] & ((1u << (8 * left)) - 1u);
+                        }
+                        v[g] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             };
@@ -811,9 +825,13 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             tc_fence_before();
         }
     }
-    __syncwarp();
-    if (PAIR) ex_cluster_sync();  // (no CTA leaves while its peer may still use its memory)
-    else __syncthreads();
+    __syncthreads();
+    if (PAIR) {
+        if (tid == 0 && s_abort)  // a wait that ran out here ends the peer's work too
+            asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(map_rank(smem_u32(&s_abort), (unsigned)rank ^ 1u)) : "memory");
+        __syncwarp();
+        ex_cluster_sync();  // (no CTA leaves while its peer may still use its memory)
+    }
     if (warp == 1) {
         if (s_abort) {
             // products already issued are waited for before their tensor memory goes

@@ -24,11 +24,28 @@ inline ExpertShape expert_shape(int R, int K, bool fp4, bool gate_up) {
 inline size_t expert_scratch_bytes(int64_t mk, int R) { return ((size_t)mk * (size_t)R * 2 + 255) / 256 * 256; }
 
 // Whether two CTAs share their activation rows (256 weight rows a tile): where
-// an expert has 16 rows or more on average (256 tokens x 8 over 128 experts,
-// E4M3 gate/up: 199 us as pairs, 252 alone) and there is a tile for every CTA.
-inline bool expert_pair(int64_t mk, int E, int RT, int ctas) {
-    const int64_t tiles = ((mk < E ? mk : E) + mk / 256) * RT;
-    return mk >= 16 * (int64_t)E && tiles >= ctas;
+// an expert has 16 rows or more on average, and there are 64 in all.  Gate/up
+// of 1001 tokens x 8 over 128 experts, E2M1: 118 us as pairs, 139 alone; of 256
+// tokens, E4M3: 191 and 200; of 128: 179 and 178.  A product of 64 rows with
+// 6144 x 6144, E4M3: 11.9 and 12.5; of 33, E2M1: 7.8 and 7.5.
+inline bool expert_pair(int64_t mk, int E) { return mk >= 64 && mk >= 16 * (int64_t)E; }
+
+// Rows of a gemm's column tiles (a multiple of 16, of 32 for pairs; at most
+// 256): of the sizes, the one whose rounds of tiles cost least, a round taken
+// as 256 + rows (the loads of a stage: its weight rows and its activation
+// rows).  4096 x 6144 x 6144, E2M1: tiles of 224 rows, 6 full rounds, 51.5 us;
+// of 256, 5.05 of 6 rounds, 54.5.
+inline int expert_gemm_rows(int M, int RT, bool pair, int ctas) {
+    const int step = pair ? 32 : 16;
+    if (M <= 256) return (M + step - 1) / step * step;
+    const int slots = pair ? ctas / 2 : ctas, rows = pair ? (RT + 1) / 2 : RT;
+    int best = 256;
+    int64_t least = INT64_MAX;
+    for (int per = 256; per >= 128; per -= step) {
+        const int64_t tiles = ((int64_t)M + per - 1) / per * rows, cost = (tiles + slots - 1) / slots * (256 + per);
+        if (cost < least) least = cost, best = per;
+    }
+    return best;
 }
 
 // One launch of the expert kernel (op: 0 gemm, 1 gate/up, 2 down).

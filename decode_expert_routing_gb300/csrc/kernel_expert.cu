@@ -234,6 +234,7 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     }
     a.w_scale = c.w_scale;
     a.x_scale = c.x_scale;
+    a.x_scale_end = c.x_scale + (c.x_rows - 1) * c.lds + K / 32;
     a.lds = c.lds;
     a.sorted = c.sorted;
     a.experts = c.experts;
@@ -253,7 +254,7 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     a.block = c.block;
     a.gather = c.gather;
     a.sf_vec = 1;
-    for (int v = 4; v <= 16; v *= 2)  // rows whose bytes end on the boundary too: no read past a row
+    for (int v = 8; v <= 16; v *= 2)  // rows whose bytes end on the boundary too: no read past a row
         if (a.kb % v == 0 && c.lds % v == 0 && reinterpret_cast<uintptr_t>(c.x_scale) % v == 0) a.sf_vec = v;
     {  // column tiles: one per expert with rows, and one for every further 256 rows
         const int64_t mk = (int64_t)c.M * c.topk, most = (mk < c.E ? mk : c.E) + mk / kExMaxN + 1;
@@ -266,7 +267,8 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     a.kbytes = (int)kbytes;
     if (c.op == kExDown) a.out = c.scratch;
     const int grid = sms;
-    const bool pair = expert_pair(a.mk, c.E, s.RT, sms);
+    const bool pair = expert_pair(a.mk, c.E);
+    if (c.op == kExGemm) a.per = expert_gemm_rows(c.M, s.RT, pair, sms);
     cudaError_t e = c.op == kExGemm     ? launch_op<kExGemm>(a, fp4, pair, grid, st)
                           : c.op == kExGateUp ? launch_op<kExGateUp>(a, fp4, pair, grid, st)
                                               : launch_op<kExDown>(a, fp4, pair, grid, st);

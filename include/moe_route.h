@@ -130,8 +130,9 @@ int mr_set_launch_flags(int flags);
 int mr_get_launch_flags(void);
 
 /*
- * Bounded waits.  The router GEMV for M <= 64 and the one-launch route hand
- * data between the CTAs of a thread-block cluster (split-K partials to the
+ * Bounded waits.  (The expert products' waits, for their own copies and
+ * products, are bounded and reported in the same way.)  The router GEMV for
+ * M <= 64 and the one-launch route hand data between the CTAs of a thread-block cluster (split-K partials to the
  * CTA that owns a token, chosen ids to the CTA that sorts).  Each receiving
  * CTA waits for the bytes it expects at most the wait limit (default 1 s).
  * When a wait runs out the kernel sets a device-side flag and returns early;

@@ -300,6 +300,122 @@ def test_pdl_flag_gives_the_same_bits(mr):
         mr.set_launch_flags(0)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_one_expert_of_many_takes_all(mr, fmt):
+    """The largest tables beside the widest tiles."""
+    M, E, topk, K, I, block = 601, 1024, 1, 416, 64, 64
+    ids = torch.full((M, topk), 1000, dtype=torch.int32, device="cuda")
+    wts = torch.full((M, topk), 0.5, device="cuda")
+    st, ex, _ = mr.moe_sort(ids, E, block)
+    w13, w2 = ref.random_mx((E, 2 * I, K), fmt, 1, 117, 122), ref.random_mx((E, K, I), fmt, 2, 117, 122)
+    q = quant(mr, torch.randn(M, K, generator=torch.Generator("cpu").manual_seed(3)).to(BF16).cuda(), fmt)
+    one = [t[1000:1001].contiguous() for t in w13], [t[1000:1001].contiguous() for t in w2]
+    act, tol = ref.swiglu(ref.value64(*q, fmt), ref.value64(one[0][0][0], one[0][1][0], fmt))
+    out = mr.moe_gate_up(*q, mr.MxWeight(*w13, fmt, gate_up=True), st, ex, topk, block)
+    ref.assert_close(out[:M], act, tol + ref.half_step(BF16) * (act.abs() + tol))
+    c, s = mr.moe_gate_up(*q, mr.MxWeight(*w13, fmt, gate_up=True), st, ex, topk, block, quant=fmt)
+    want = ref.value64(c[:M], s[:M], fmt) @ ref.value64(one[1][0][0], one[1][1][0], fmt).T
+    got = mr.moe_down(c, s, mr.MxWeight(*w2, fmt), ids, wts, st, ex, block)
+    d = ref.sum_bound(I) * (ref.value64(c[:M], s[:M], fmt).abs() @ ref.value64(one[1][0][0], one[1][1][0], fmt).abs().T)
+    half = ref.half_step(BF16)
+    tol = 0.5 * (d + half * (want.abs() + d)) + 2.0 ** -23 * want.abs()
+    ref.assert_close(got, 0.5 * want, tol + half * (0.5 * want.abs() + tol))
+
+
+def test_offsets_past_32_bits(mr):
+    """420 000 assignments: more column tiles than the kernel lists, and rows
+    of y and of the gate/up output past 2^31 elements."""
+    fmt, M, E, topk, K, I, block = "mxfp4", 70000, 4, 6, 32, 5216, 64
+    g = torch.Generator("cuda").manual_seed(1)
+    ids = torch.randint(0, E, (M, topk), generator=g, device="cuda", dtype=torch.int32)
+    wts = torch.rand(M, topk, generator=g, device="cuda")
+    st, ex, _ = mr.moe_sort(ids, E, block)
+    assert st.numel() * I > 1 << 31
+    w13 = ref.random_mx((E, 2 * I, K), fmt, 1, 117, 122)
+    q = quant(mr, torch.randn(M, K, generator=g, device="cuda").to(BF16), fmt)
+    out = mr.moe_gate_up(*q, mr.MxWeight(*w13, fmt, gate_up=True), st, ex, topk, block)
+    pos = torch.cat([torch.arange(40, device="cuda"), torch.nonzero(st < M * topk)[-40:, 0]])
+    f, e = st[pos].long(), ex[pos // block].long()
+    xv, wv = ref.value64(*q, fmt), ref.value64(*w13, fmt)
+    for i in range(pos.numel()):
+        act, tol = ref.swiglu(xv[f[i] // topk][None], wv[e[i]])
+        ref.assert_close(out[pos[i]][None], act, tol + ref.half_step(BF16) * (act.abs() + tol))
+    del out
+    I, R = 32, 5216  # the other way round: y has M * topk rows of R
+    w2 = ref.random_mx((E, R, I), fmt, 2, 117, 122)
+    a = torch.randint(0, 256, (st.numel(), I // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.randint(120, 126, (st.numel(), 1), generator=g, device="cuda", dtype=torch.uint8)
+    got = mr.moe_down(a, s, mr.MxWeight(*w2, fmt), ids, wts, st, ex, block)
+    place = torch.empty(M * topk, dtype=torch.long, device="cuda")
+    real = torch.nonzero(st < M * topk)[:, 0]
+    place[st[real].long()] = real
+    wv = ref.value64(*w2, fmt)
+    for m in (0, 1, 777, M // 2, M - 2, M - 1):
+        p = place[m * topk:(m + 1) * topk]
+        rows = ref.value64(a[p], s[p], fmt)
+        y = torch.stack([rows[j] @ wv[int(ids[m, j])].T for j in range(topk)])
+        d = ref.sum_bound(I) * torch.stack([rows[j].abs() @ wv[int(ids[m, j])].abs().T for j in range(topk)])
+        d = d + ref.half_step(BF16) * (y.abs() + d)
+        w = wts[m].double()[:, None]
+        want, tol = (w * y).sum(0), (w * d).sum(0) + (topk + 1) * 2.0 ** -24 * (w * y.abs()).sum(0)
+        ref.assert_close(got[m], want, tol + ref.half_step(BF16) * (want.abs() + tol))
+
+
+def test_weights_past_32_bits(mr):
+    """Weight codes of more than 4 GB: the last expert's."""
+    fmt, M, E, topk, K, I, block = "mxfp8", 5, 700, 2, 4096, 768, 16
+    g = torch.Generator("cuda").manual_seed(2)
+    codes = torch.randint(0, 120, (E, 2 * I, K), generator=g, device="cuda", dtype=torch.uint8)
+    scale = torch.randint(112, 116, (E, 2 * I, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    assert codes.numel() > 1 << 32
+    W = mr.MxWeight(codes, scale, fmt, gate_up=True)
+    ids = torch.tensor([[699, 3], [698, 699], [0, 699], [350, 698], [699, 1]], dtype=torch.int32, device="cuda")
+    st, ex, _ = mr.moe_sort(ids, E, block)
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF16) * 0.1
+    q = quant(mr, x, fmt)
+    out = mr.moe_gate_up(*q, W, st, ex, topk, block)
+    xv = ref.value64(*q, fmt)
+    pos, f = ref.used_positions(st, M * topk)
+    for p, a in zip(pos.tolist(), f.tolist()):
+        e = int(ex[p // block])
+        act, tol = ref.swiglu(xv[a // topk][None], ref.value64(codes[e], scale[e], fmt))
+        ref.assert_close(out[p][None], act, tol + ref.half_step(BF16) * (act.abs() + tol))
+
+
+def test_scales_at_any_alignment(mr):
+    """Scale rows whose length, stride and first byte are odd, at the ends of their array."""
+    for fmt in FMTS:
+        for K, extra, first in ((2976, 0, 0), (2976, 2, 1), (160, 0, 3), (32, 0, 1), (1056, 5, 2)):
+            M, R = 37, 130
+            x, w = ref.random_mx((M, K), fmt, K), ref.random_mx((R, K), fmt, 4)
+            kb = K // 32
+            buf = torch.full((first + M * (kb + extra),), 255, dtype=torch.uint8, device="cuda")
+            s = buf[first:].view(M, kb + extra)[:, :kb]
+            s.copy_(x[1])
+            out = mr.mx_gemm(x[0], s, mr.MxWeight(*w, fmt), out_dtype=torch.float32)
+            ref.assert_close(out, *ref.product(ref.value64(*x, fmt), ref.value64(*w, fmt), torch.float32), f"{fmt} {K}")
+
+
+@pytest.mark.parametrize("M", [8, 300])
+def test_a_wait_that_runs_out_is_reported(mr, M):
+    """The first stage expects bytes that nobody sends: the call ends, the flag tells, and the next call is right."""
+    x, w = ref.random_mx((M, 512), "mxfp8", 1), ref.random_mx((256, 512), "mxfp8", 2)
+    W = mr.MxWeight(*w)
+    want = mr.mx_gemm(*x, W)
+    torch.cuda.synchronize()
+    try:
+        mr.set_wait_limit_ns(20_000_000)
+        mr.set_launch_flags(mr.LAUNCH_TEST_STALL)
+        mr.mx_gemm(*x, W)
+        torch.cuda.synchronize()
+    finally:
+        mr.set_launch_flags(0)
+        mr.set_wait_limit_ns(1_000_000_000)
+    assert mr.device_error(clear=True) == mr.MR_ERR_TIMEOUT
+    assert torch.equal(mr.mx_gemm(*x, W), want)
+    assert mr.device_error() == mr.MR_OK
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_python_refusals(mr):
