@@ -26,6 +26,13 @@
 // bound tiles of many rows, so it takes them: gate/up of 32768 rows 302 -> 275
 // us, the E2M1 product 4096 x 6144 x 6144 62 -> 56 us.
 //
+// SPLIT: where there are too few tiles for the SMs, the CTAs of a cluster share
+// a tile's K range.  Each keeps its sums in its tensor memory; then every CTA
+// sends them to the CTA that owns the columns (16 of them in turn, through
+// distributed shared memory, into the ring's room) and adds those it owns in
+// K order.  (Through global memory, with a ticket and the last CTA adding, the
+// same split cost more than it gave.)
+//
 // The loops of warps 0 and 1 are uniform over the warp (waits end in a vote,
 // one elected lane issues): as code of a single lane, the copies and products
 // of a stage took 700 and 850 cycles to issue, in uniform registers a
@@ -75,6 +82,7 @@ struct ExpertArgs {
     int E, R, RT, KI, kb, kbytes;  // weight rows, row tiles, k-blocks, scale and code bytes per row
     int M, topk, mk, nblk, block;
     int per;                 // kExGemm: rows of a column tile
+    int slices, slice_len;   // SPLIT: CTAs of a cluster, k-blocks of each
     int gather;              // x rows in token order
     int sf_vec;              // bytes that the scale rows can be read in: 16, 8, else any
     int list_cap;            // column tiles that the shared list holds (0: none, they are searched for)
@@ -183,6 +191,10 @@ __device__ __forceinline__ void ex_commit(uint32_t bar) {
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                      : "memory");
+}
+// The same from code that not every warp is in at once.
+__device__ __forceinline__ void ex_cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ void ex_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -297,18 +309,19 @@ __device__ __forceinline__ ExTile ex_tile(const ExTables& t, int E, int ct, int 
 // at work share few activation rows and each weight is read once.
 struct ExWalk {
     int ct, rt, dct, drt, RT, end;
-    __device__ __forceinline__ ExWalk(int me, int n, int row_tiles)
+    bool once;  // one tile, whatever the tables say (SPLIT: its CTAs meet twice)
+    __device__ __forceinline__ ExWalk(int me, int n, int row_tiles, bool single)
         : ct(me / row_tiles), rt(me - me / row_tiles * row_tiles), dct(n / row_tiles),
-          drt(n - n / row_tiles * row_tiles), RT(row_tiles), end(0) {}
+          drt(n - n / row_tiles * row_tiles), RT(row_tiles), end(0), once(single) {}
     __device__ __forceinline__ bool more() const { return ct < end; }
     __device__ __forceinline__ void next() {
-        ct += dct;
+        ct = once ? end : ct + dct;
         rt += drt;
         if (rt >= RT) rt -= RT, ++ct;
     }
 };
 
-template <bool FP4, int OP, bool PAIR>
+template <bool FP4, int OP, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_constant__ ExpertArgs a) {
     constexpr int kExThreads = ex_threads(OP);
     constexpr int W = FP4 ? 2 : 1;  // scale words (of 4 bytes) per row and k-block
@@ -321,7 +334,9 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     __shared__ __align__(16) unsigned char s_act[OP == kExGateUp ? 4 * 16 * kExStagePitch : 16];
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
     const bool gather = OP == kExGateUp && a.gather;
-    const int rank = PAIR ? (int)cluster_rank() : 0;
+    const int rank = PAIR ? (int)cluster_rank() : 0, slice = SPLIT ? (int)cluster_rank() : 0;
+    // this CTA's k-blocks
+    const int kb0 = SPLIT ? slice * a.slice_len : 0, kb1 = SPLIT ? min(a.KI, kb0 + a.slice_len) : a.KI;
     const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
 
     // ---- set-up that reads nothing of the kernel before
@@ -358,7 +373,9 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     if (OP != kExGemm)
         for (int e = tid; e < a.E; e += kExThreads) t.first[e] = -1, t.rows[e] = 0;
     // a pair takes two row tiles at a time, one in each CTA
-    ExWalk walk((int)blockIdx.x >> (PAIR ? 1 : 0), (int)gridDim.x >> (PAIR ? 1 : 0), PAIR ? (a.RT + 1) >> 1 : a.RT);
+    // (a cluster that splits its K range has one tile at most)
+    const int of = PAIR ? 2 : SPLIT ? a.slices : 1;
+    ExWalk walk((int)blockIdx.x / of, (int)gridDim.x / of, PAIR ? (a.RT + 1) >> 1 : a.RT, SPLIT);
     pdl_trigger();
     pdl_wait();
     if (OP != kExGemm) {
@@ -452,7 +469,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             const uint8_t* ws = a.w_scale + ((int64_t)o.e * a.RT + min(o.rt, a.RT - 1)) * a.KI * (W * 512);
             const int nx = PAIR ? o.n >> 1 : o.n, rx = o.r0 + rank * nx;  // this CTA's activation rows
             const unsigned tx = (unsigned)(kExWBytes + W * 512 + (gather ? 0 : nx * 128));
-            for (int ki = 0; ki < a.KI; ki += D) {
+            for (int ki = kb0; ki < kb1; ki += D) {
                 if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
@@ -460,7 +477,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 const uint32_t full = full0 + 8u * st;
                 uint32_t wsm = base + (uint32_t)st * stage_bytes, ssm = sf_base + (uint32_t)st * sf_stage;
                 if (ex_elect()) {
-                    const int nd = min(D, a.KI - ki);
+                    const int nd = min(D, kb1 - ki);
                     mbar_expect_tx(full, tx * nd + (((a.flags & 2) && issued == 0) ? 16u : 0u));
                     for (int b = 0; b < nd; ++b, wsm += code_bytes, ssm += sf_bytes) {
                         const int x = (ki + b) * 128;
@@ -495,7 +512,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
         bool ok = true;
         const uint32_t peer = map_rank(full0, 0);
         for (; ok && walk.more(); walk.next()) {
-            for (int ki = 0; ki < a.KI; ki += D) {
+            for (int ki = kb0; ki < kb1; ki += D) {
                 if (!ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
@@ -517,7 +534,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 ok = ex_wait(smem_u32(&s_tfree), (unsigned)(it - 1) & 1u, a.wait_ns, &s_abort);
                 tc_fence_after();
             }
-            for (int ki = 0; ok && ki < a.KI; ki += D) {
+            for (int ki = kb0; ok && ki < kb1; ki += D) {
                 if (!ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
@@ -525,7 +542,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 tc_fence_after();
                 uint32_t wa = base + (uint32_t)st * stage_bytes, sa = sf_base + (uint32_t)st * sf_stage;
                 if (ex_elect()) {
-                    const int nd = min(D, a.KI - ki);
+                    const int nd = min(D, kb1 - ki);
                     for (int b = 0; b < nd; ++b, wa += code_bytes, sa += sf_bytes) {
                         const unsigned long long da = ex_desc(kExDescCodes, wa);
                         const unsigned long long db = ex_desc(kExDescCodes, wa + kExWBytes);
@@ -540,11 +557,11 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                             const int w = FP4 ? j >> 1 : 0;
                             const uint32_t sel = FP4 ? (uint32_t)(j & 1) * 2 : (uint32_t)j;
                             ex_mma<FP4, PAIR>(d, da + 2 * j, db + 2 * j, idesc, sel, sfa + 4 * w, sfb + 4 * w * H,
-                                              ki > 0 || b > 0 || j > 0);
+                                              ki > kb0 || b > 0 || j > 0);
                         }
                     }
                     ex_commit<PAIR>(empty0 + 8u * st);
-                    if (ki + D >= a.KI) ex_commit<PAIR>(smem_u32(&s_tfull[it & 1]));
+                    if (ki + D >= kb1) ex_commit<PAIR>(smem_u32(&s_tfull[it & 1]));
                 }
                 __syncwarp();
                 if (++st == nst) st = 0, ph ^= 1u;
@@ -615,7 +632,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             auto store = [&](const uint4 (&v)[4], int k0) {
 #pragma unroll
                 for (int s = 0; s < B; ++s) {
-                    if (k0 + s >= a.KI) return true;
+                    if (k0 + s >= kb1) return true;
                     const int b = D == 2 ? (k0 + s) & 1 : 0;  // its place in the stage
                     if (b == 0 && !ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) return false;
                     if (G > 0) {
@@ -630,7 +647,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                                          : "memory");
                         }
                     }
-                    if (b != D - 1 && k0 + s + 1 < a.KI) continue;
+                    if (b != D - 1 && k0 + s + 1 < kb1) continue;
                     if (G > 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full0 + 8u * st);
@@ -639,11 +656,11 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 return true;
             };
             uint4 v0[4], v1[4];
-            load(v0, 0);
-            for (int k0 = 0; ok && k0 < a.KI; k0 += 2 * B) {
+            load(v0, kb0 * W * 4);
+            for (int k0 = kb0; ok && k0 < kb1; k0 += 2 * B) {
                 load(v1, (k0 + B) * W * 4);
                 ok = store(v0, k0);
-                if (!ok || k0 + B >= a.KI) break;
+                if (!ok || k0 + B >= kb1) break;
                 load(v0, (k0 + 2 * B) * W * 4);
                 ok = store(v1, k0 + B);
             }
@@ -690,14 +707,14 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             }
             walk.next();
             fetch();  // the next tile's, while this one is copied
-            for (int ki = 0; ok && ki < a.KI; ki += D) {
+            for (int ki = kb0; ok && ki < kb1; ki += D) {
                 if (turn == which) {
                     if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
                         ok = false;
                         break;
                     }
                     const uint32_t full = full0 + 8u * st, xst = base + (uint32_t)st * stage_bytes + kExWBytes;
-                    const int nd = min(D, a.KI - ki);
+                    const int nd = min(D, kb1 - ki);
                     if (few) {
                         if (lane == 0) mbar_expect_tx(full, (unsigned)(__popc(real) * nd * 128));
                         __syncwarp();
@@ -736,24 +753,62 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             if (PAIR) mbar_arrive_remote(tfree);
             else mbar_arrive(tfree);
         };
+        bool met = false;
         for (int it = 0; walk.more(); walk.next(), ++it) {
             const ExTile o = EX_TILE;
             int* f = s_f[it & 1];
             if (OP != kExGemm && et < o.n) f[et] = et < o.rows ? a.sorted[o.r0 + et] : a.mk;
             const bool ok = ex_wait(smem_u32(&s_tfull[it & 1]), (unsigned)(it >> 1) & 1u, a.wait_ns, &s_abort);
-            if (!ex_sync(1, 256, ok)) break;
+            const bool all_ok = ex_sync(1, 256, ok);
+            if (!SPLIT && !all_ok) break;
             tc_fence_after();
             const uint32_t d = tmem + lanes + ((it & 1) ? kExBuf1 : 0);
             const int nch = o.n >> 4;
+            if (SPLIT) {
+                // every CTA's products are done, so its ring's room is free: [sender][its chunks of mine][16][128]
+                ex_cluster_meet();
+                const int most = (nch + a.slices - 1) / a.slices;
+                for (int i = grp; i < nch; i += 2) {
+                    const int owner = i % a.slices;
+                    if (owner == slice) continue;
+                    uint32_t v[16];
+                    ex_ld16(v, d + (uint32_t)i * 16u);
+                    const uint32_t to = map_rank(base, (unsigned)owner) +
+                                        (uint32_t)((slice * most + i / a.slices) * 16 * 128 + wq * 32 + lane) * 4u;
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 512u * q), "r"(v[q]) : "memory");
+                }
+                ex_cluster_meet();
+                met = true;
+                if (!all_ok) break;
+            }
             // the shared columns first: the chunks after which the next tile may start
-            const bool from_top = !(it & 1) && o.n > kExBuf1;
-            const int need = from_top ? nch - kExBuf1 / 16 : (it & 1) ? min(2, nch) : 0;
+            const bool from_top = !SPLIT && !(it & 1) && o.n > kExBuf1;
+            const int need = SPLIT ? 0 : from_top ? nch - kExBuf1 / 16 : (it & 1) ? min(2, nch) : 0;
             if (need <= grp && lane == 0) release();
             const int r = o.rt * 128 + wq * 32 + lane;
-            for (int i = grp; i < nch; i += 2) {
+            for (int i = SPLIT ? slice + grp * a.slices : grp; i < nch; i += SPLIT ? 2 * a.slices : 2) {
                 const int c0 = (from_top ? nch - 1 - i : i) * 16;
                 uint32_t v[16];
                 ex_ld16(v, d + (uint32_t)c0);
+                if (SPLIT) {
+                    const int most = (nch + a.slices - 1) / a.slices;
+                    float sum[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) sum[q] = 0.0f;
+                    for (int c = 0; c < a.slices; ++c) {
+                        const uint32_t from = base + (uint32_t)((c * most + i / a.slices) * 16 * 128 + wq * 32 + lane) * 4u;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            float x = __uint_as_float(v[q]);
+                            if (c != slice) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(from + 512u * q) : "memory");
+                            sum[q] = __fadd_rn(sum[q], x);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(sum[q]);
+                }
                 if (i < need && i + 2 >= need) {
                     tc_fence_before();
                     __syncwarp();
@@ -824,6 +879,15 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             }
             tc_fence_before();
         }
+        if (SPLIT && !met) {
+            ex_cluster_meet();
+            ex_cluster_meet();
+        }
+    }
+    if (SPLIT && (warp < 4 || warp >= 12)) {  // the two meetings of the CTAs that hand sums over (tile or no tile)
+        __syncwarp();
+        ex_cluster_meet();
+        ex_cluster_meet();
     }
     __syncthreads();
     if (PAIR) {

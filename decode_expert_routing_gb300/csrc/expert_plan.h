@@ -30,6 +30,30 @@ inline size_t expert_scratch_bytes(int64_t mk, int R) { return ((size_t)mk * (si
 // 6144 x 6144, E4M3: 11.9 and 12.5; of 33, E2M1: 7.8 and 7.5.
 inline bool expert_pair(int64_t mk, int E) { return mk >= 64 && mk >= 16 * (int64_t)E; }
 
+// CTAs that share a tile's K range (1: none do), where the tiles leave SMs
+// without work: 2, 4 or 8 (clusters of 3 and 6 were placed so that some had to
+// wait), with a tile for every cluster; *len is each one's k-blocks, a multiple
+// of those whose scales are 16 bytes of a row.  A k-block takes 0.2 us or more;
+// handing the sums over 1.5 us and the columns' way through distributed shared
+// memory (some 90 bytes a cycle for a cluster).  64 x 500 x 6144, E4M3: 6.2 us
+// in 8 slices, 10.8 in one; 300 x 2000 x 2976: 16.7 in 4, 20.4 in one.
+inline int expert_slices(int64_t mk, int E, const ExpertShape& s, int ctas, int* len) {
+    // (a run of blocks has at most 15 rows more than assignments)
+    const int64_t hit = mk < E ? mk : E, tiles = (hit + (mk + 15 * hit) / 256) * s.RT;
+    const int64_t rows = mk / hit < 256 ? mk / hit : 256;
+    const int group = 4 / s.W;
+    int best = 1;
+    double most = 0.0;
+    *len = s.KI;
+    for (int n = 2; n <= 8; n *= 2) {
+        if (tiles * n * 10 > (int64_t)ctas * 9) break;
+        const int l = ((s.KI + n - 1) / n + group - 1) / group * group;
+        const double gain = 0.2 * (s.KI - l) - 1.5 - 0.003 * (double)rows * (n - 1);
+        if ((int64_t)l * (n - 1) < s.KI && gain > most) most = gain, best = n, *len = l;  // (every slice has k-blocks)
+    }
+    return best;
+}
+
 // Rows of a gemm's column tiles (a multiple of 16, of 32 for pairs; at most
 // 256): of the sizes, the one whose rounds of tiles cost least, a round taken
 // as 256 + rows (the loads of a stage: its weight rows and its activation

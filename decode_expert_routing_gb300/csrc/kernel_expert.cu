@@ -162,21 +162,22 @@ bool encode(CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP4, int OP, bool PAIR>
+template <bool FP4, int OP, bool PAIR, bool SPLIT>
 cudaError_t launch_one(const ExpertArgs& a, int grid, cudaStream_t st) {
     static int prepared[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    const auto kernel = expert_kernel<FP4, OP, PAIR>;
+    const auto kernel = expert_kernel<FP4, OP, PAIR, SPLIT>;
     if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmemDyn);
         if (e != cudaSuccess) return e;
         __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(PAIR ? grid & ~1 : grid));
+    const int of = PAIR ? 2 : SPLIT ? a.slices : 1;  // CTAs of a cluster
+    cfg.gridDim = dim3((unsigned)(grid / of * of));
     cfg.blockDim = dim3(ex_threads(OP));
     cfg.dynamicSmemBytes = kExSmemDyn;
     cfg.stream = st;
@@ -185,17 +186,19 @@ cudaError_t launch_one(const ExpertArgs& a, int grid, cudaStream_t st) {
     // whatever the launch options: the kernel reads and writes nothing before it has waited for the one before it
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.x = (unsigned)of;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = PAIR ? 2 : 1;
+    cfg.numAttrs = PAIR || SPLIT ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kernel, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <int OP>
 cudaError_t launch_op(const ExpertArgs& a, bool fp4, bool pair, int grid, cudaStream_t st) {
-    if (fp4) return pair ? launch_one<true, OP, true>(a, grid, st) : launch_one<true, OP, false>(a, grid, st);
-    return pair ? launch_one<false, OP, true>(a, grid, st) : launch_one<false, OP, false>(a, grid, st);
+    if (a.slices > 1)
+        return fp4 ? launch_one<true, OP, false, true>(a, grid, st) : launch_one<false, OP, false, true>(a, grid, st);
+    if (fp4) return pair ? launch_one<true, OP, true, false>(a, grid, st) : launch_one<true, OP, false, false>(a, grid, st);
+    return pair ? launch_one<false, OP, true, false>(a, grid, st) : launch_one<false, OP, false, false>(a, grid, st);
 }
 
 }  // namespace
@@ -267,7 +270,8 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     a.kbytes = (int)kbytes;
     if (c.op == kExDown) a.out = c.scratch;
     const int grid = sms;
-    const bool pair = expert_pair(a.mk, c.E);
+    a.slices = expert_slices(a.mk, c.E, s, sms, &a.slice_len);
+    const bool pair = a.slices == 1 && expert_pair(a.mk, c.E);
     if (c.op == kExGemm) a.per = expert_gemm_rows(c.M, s.RT, pair, sms);
     cudaError_t e = c.op == kExGemm     ? launch_op<kExGemm>(a, fp4, pair, grid, st)
                           : c.op == kExGateUp ? launch_op<kExGateUp>(a, fp4, pair, grid, st)
