@@ -251,6 +251,36 @@ __device__ __forceinline__ unsigned ex_div(unsigned a, unsigned b) {
     return q;
 }
 
+// Up to 16 scale bytes of a row from any address at (the rest zeros), left of
+// them in the row: out of lo and hi, the two aligned 16 bytes around them, or
+// (whole false: those would leave the array) byte by byte.
+__device__ __forceinline__ uint4 ex_scales16(const uint8_t* at, int left, uint4 lo, uint4 hi, bool whole) {
+    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(at) & 15u);
+    uint32_t w[4];
+    if (whole) {
+        uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) x[i] = (off & 8u) ? x[i + 2] : x[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) x[i] = (off & 4u) ? x[i + 1] : x[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], (off & 3u) * 8u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = 0u;
+            for (int u = 0; u < 4; ++u)
+                if (4 * i + u < left) w[i] |= (uint32_t)__ldg(at + 4 * i + u) << (8 * u);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = left - 4 * i;
+        if (n < 4) w[i] = n <= 0 ? 0u : w[i] & ((1u << (8 * n)) - 1u);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The experts' column tiles, built by every CTA from the route's outputs.
 struct ExTables {
     int* first;  // [E] first sorted position
@@ -589,43 +619,34 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 row[g] = a.x_scale + src * a.lds;
             }
             auto load = [&](uint4 (&v)[4], int b) {  // b: first scale byte
+                if (a.sf_vec == 1) {
+                    uint4 lo[4], hi[4];
+                    bool whole[4];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {  // (every group's loads before the first use)
+                        const uint8_t* p = row[g] + b - (reinterpret_cast<uintptr_t>(row[g] + b) & 15u);
+                        whole[g] = p >= a.x_scale && p + 32 <= a.x_scale_end;
+                        const bool get = whole[g] && g < G && b < a.kb;
+                        lo[g] = get ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+                        hi[g] = get ? __ldg(reinterpret_cast<const uint4*>(p) + 1) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        v[g] = g < G && b < a.kb ? ex_scales16(row[g] + b, a.kb - b, lo[g], hi[g], whole[g])
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+                    return;
+                }
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     v[g] = make_uint4(0u, 0u, 0u, 0u);
                     if (g >= G) continue;
                     if (a.sf_vec == 16) {
                         if (b < a.kb) v[g] = __ldg(reinterpret_cast<const uint4*>(row[g] + b));
-                    } else if (a.sf_vec == 8) {
+                    } else {
                         uint2 lo = make_uint2(0u, 0u), hi = make_uint2(0u, 0u);
                         if (b < a.kb) lo = __ldg(reinterpret_cast<const uint2*>(row[g] + b));
                         if (b + 8 < a.kb) hi = __ldg(reinterpret_cast<const uint2*>(row[g] + b + 8));
                         v[g] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                    } else {
-                        // from the five words around them (of which only the bytes of the scales are read at the
-                        // ends of the array)
-                        const uint8_t* at = row[g] + b;
-                        const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(at) & 3u);
-                        uint32_t x[5];
-#pragma unroll
-                        for (int i = 0; i < 5; ++i) {
-                            const uint8_t* p = at - off + 4 * i;
-                            x[i] = 0u;
-                            if (b + 4 * i - (int)off >= a.kb) continue;
-                            if (p >= a.x_scale && p + 4 <= a.x_scale_end) {
-                                x[i] = __ldg(reinterpret_cast<const uint32_t*>(p));
-                            } else {
-                                for (int u = 0; u < 4; ++u)
-                                    if (p + u >= a.x_scale && p + u < a.x_scale_end) x[i] |= (uint32_t)__ldg(p + u) << (8 * u);
-                            }
-                        }
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int left = a.kb - b - 4 * i;  // scales of the row from here on
-                            w[i] = __funnelshift_r(x[i], x[i + 1], off * 8u);
-                            if (left < 4) w[i] = left <= 0 ? 0u : w[i] & ((1u << (8 * left)) - 1u);
-                        }
-                        v[g] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             };
