@@ -1054,7 +1054,8 @@ class PreparedDown(_Prepared):
         p.out = out.data_ptr()
         p.scratch, p.scratch_bytes = scratch.ptr, scratch.nbytes
         self.out, self.device = out, dev
-        self._keep = (q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, add, scratch)
+        self._keep = (q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, add)
+        self.scratch = scratch
         self._ref = ctypes.byref(p)
         self._fn, self._name = _load().mr_moe_down, "mr_moe_down"
 
@@ -1066,5 +1067,12 @@ def moe_down(q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, e
     act @ w2^T.  q, scale: act's codes and scales at the sorted positions, as
     moe_gate_up(..., quant=...) returns them.  Slots whose id is outside
     [0, E) add nothing."""
-    return PreparedDown(q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, block, add, out,
-                        scratch)(stream)
+    call = PreparedDown(q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, block, add, out, scratch)
+    call(stream)
+    if scratch is None and stream is not None:
+        # its memory goes back to the current stream's pool when this returns, but not before the call's own stream
+        # is done with it
+        torch = _torch()
+        own = torch.cuda.ExternalStream(stream, device=call.device) if isinstance(stream, int) else stream
+        call.scratch.tensor.record_stream(own)
+    return call.out

@@ -648,7 +648,9 @@ int mr_mx_gemm(const mr_mx_gemm_params* p, void* stream) {
     if (p->w == nullptr || !aligned(p->w, 16) || p->w_scale == nullptr || !aligned(p->w_scale, 16) ||
         p->out == nullptr || !aligned(p->out, p->out_fp32 ? 4 : 2) || p->ldo < p->R)
         return MR_ERR_INVALID_ARG;
-    if (p->M >= (1 << 30)) return MR_ERR_UNSUPPORTED;
+    // (column tiles have 128 rows or more)
+    if (p->M >= (1 << 30) || ((int64_t)p->M / 128 + 1) * ((p->R + 127) / 128) >= ((int64_t)1 << 31))
+        return MR_ERR_UNSUPPORTED;
     mr::ExpertCall c{};
     c.op = 0;
     c.fp4 = p->format == MR_QUANT_MXFP4;
@@ -658,7 +660,6 @@ int mr_mx_gemm(const mr_mx_gemm_params* p, void* stream) {
     c.K = p->K;
     c.M = p->M;
     c.topk = 1;
-    if (((int64_t)p->M / 256 + 1) * ((p->R + 127) / 128) >= ((int64_t)1 << 31)) return MR_ERR_UNSUPPORTED;
     c.w = p->w;
     c.w_scale = static_cast<const uint8_t*>(p->w_scale);
     c.x = p->q;

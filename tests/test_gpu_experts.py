@@ -416,6 +416,148 @@ def test_a_wait_that_runs_out_is_reported(mr, M):
     assert mr.device_error() == mr.MR_OK
 
 
+# ------------------------------------------------------------------ few tiles of a long K: several CTAs to a tile
+
+LONG = [  # M, R, K: one row of tiles and several, odd numbers of k-blocks, several column tiles
+    (1, 128, 6144), (8, 256, 6144), (33, 1000, 6144), (33, 6144, 6144), (64, 500, 4128), (129, 130, 12320),
+    (250, 300, 2976), (256, 100, 20480), (600, 200, 8192), (1, 1, 16416),
+]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,R,K", LONG)
+def test_mx_gemm_of_few_tiles(mr, fmt, M, R, K):
+    test_mx_gemm(mr, fmt, M, R, K)
+    x, W = ref.random_mx((M, K), fmt, 1), mr.MxWeight(*ref.random_mx((R, K), fmt, 2), fmt)
+    assert torch.equal(mr.mx_gemm(*x, W), mr.mx_gemm(*x, W))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,E,topk,K,I,block,invalid,skew", [
+    (1, 8, 2, 6144, 64, 16, 0.0, 0), (5, 4, 2, 4128, 96, 16, 0.3, 0), (40, 2, 2, 5152, 32, 8, 0.0, 0),
+    (130, 3, 1, 12320, 160, 64, 0.1, 2), (3, 1, 1, 8192, 32, 1, 0.0, 0), (300, 1, 1, 6176, 64, 128, 0.0, 0)])
+def test_experts_of_few_tiles(mr, fmt, M, E, topk, K, I, block, invalid, skew):
+    test_gate_up(mr, fmt, M, E, topk, K, I, block, invalid, skew)
+    test_down(mr, fmt, M, E, topk, I + 5, K, block, invalid, skew)
+
+
+def test_a_wait_of_one_slice_that_runs_out_is_reported(mr):
+    """As above where the CTAs of a cluster share a tile's K range."""
+    M, E, topk, K, I, block = 8, 2, 1, 6144, 64, 16
+    x, w = ref.random_mx((M, K), "mxfp8", 1), ref.random_mx((256, K), "mxfp8", 2)
+    ids, wts = routed(M, E, topk, 1)
+    st, ex, _ = mr.moe_sort(ids, E, block)
+    gemm = mr.PreparedMxGemm(*x, mr.MxWeight(*w))
+    up = mr.PreparedGateUp(*x, mr.MxWeight(*ref.random_mx((E, 2 * I, K), "mxfp8", 3, 117, 122), gate_up=True), st, ex,
+                           topk, block)
+    a = ref.random_mx((st.numel(), K), "mxfp8", 4)
+    down = mr.PreparedDown(*a, mr.MxWeight(*ref.random_mx((E, I, K), "mxfp8", 5)), ids, wts, st, ex, block)
+    up.out.zero_()
+    for call in (gemm, up, down):
+        want = call().clone()
+        torch.cuda.synchronize()
+        try:
+            mr.set_wait_limit_ns(20_000_000)
+            mr.set_launch_flags(mr.LAUNCH_TEST_STALL)
+            call()
+            torch.cuda.synchronize()
+        finally:
+            mr.set_launch_flags(0)
+            mr.set_wait_limit_ns(1_000_000_000)
+        assert mr.device_error(clear=True) == mr.MR_ERR_TIMEOUT
+        assert torch.equal(call(), want)
+        assert mr.device_error() == mr.MR_OK
+
+
+# ------------------------------------------------------------------ streams and graphs
+
+def test_down_on_another_stream_without_scratch(mr):
+    """The scratch that the call makes itself stays its own until that stream is done with it."""
+    M, E, topk, R, I, block = 64, 8, 4, 1024, 256, 16
+    ids, wts = routed(M, E, topk, 3)
+    st, ex, _ = mr.moe_sort(ids, E, block)
+    a, W = ref.random_mx((st.numel(), I), "mxfp8", 1), mr.MxWeight(*ref.random_mx((E, R, I), "mxfp8", 2))
+    want = mr.moe_down(*a, W, ids, wts, st, ex, block)
+    n = mr.ExpertScratch(M, topk, R).nbytes
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        out = torch.zeros_like(want)
+        torch.cuda.current_stream().synchronize()
+        mr.moe_down(*a, W, ids, wts, st, ex, block, out=out, stream=stream)
+        other = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert all((o == 255).all() for o in other), "the call's scratch was handed on before it ran"
+
+
+def test_captured_after_copies_and_a_fork(mr):
+    """In a graph the calls follow a copy, another stream's work and each other."""
+    M, E, topk, K, I, block, fmt = 12, 8, 2, 512, 64, 16, "mxfp8"
+    ids, wts = routed(M, E, topk, 5)
+    st, ex, _ = mr.moe_sort(ids, E, block)
+    xs = [ref.random_mx((M, K), fmt, i) for i in range(3)]
+    q, sc = torch.zeros_like(xs[0][0]), torch.zeros_like(xs[0][1])
+    src = [torch.zeros_like(q), torch.zeros_like(sc)]
+    w13 = mr.MxWeight(*ref.random_mx((E, 2 * I, K), fmt, 7, 112, 116), gate_up=True)
+    w2, wg = mr.MxWeight(*ref.random_mx((E, K, I), fmt, 8)), mr.MxWeight(*ref.random_mx((200, K), fmt, 9))
+    up = mr.PreparedGateUp(q, sc, w13, st, ex, topk, block, quant=fmt)
+    down = mr.PreparedDown(*up.out, w2, ids, wts, st, ex, block)
+    gemm = mr.PreparedMxGemm(q, sc, wg)
+    side = torch.cuda.Stream()
+    main = torch.cuda.Stream()
+
+    def step():
+        now = torch.cuda.current_stream()
+        q.copy_(src[0])
+        sc.copy_(src[1])
+        side.wait_stream(now)
+        gemm(side)
+        up()
+        down()
+        now.wait_stream(side)
+        gemm.out.mul_(2.0)
+        down.out.add_(1.0)
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        step()
+    for x in xs:
+        src[0].copy_(x[0])
+        src[1].copy_(x[1])
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = gemm.out.clone(), down.out.clone()
+        assert torch.equal(got[0], mr.mx_gemm(*x, wg) * 2.0)
+        act = mr.moe_gate_up(*x, w13, st, ex, topk, block, quant=fmt)
+        assert torch.equal(got[1], mr.moe_down(*act, w2, ids, wts, st, ex, block) + 1.0)
+
+
+def test_beside_the_router_on_another_stream(mr):
+    """Both kinds of kernel that take tensor memory at once."""
+    N, K, M = 256, 2048, 512
+    g = torch.Generator("cpu").manual_seed(0)
+    x, w = torch.randn(M, K, generator=g).to(BF16).cuda(), (torch.randn(N, K, generator=g) * 0.02).to(BF16).cuda()
+    mx, W = ref.random_mx((300, K), "mxfp4", 1), mr.MxWeight(*ref.random_mx((1000, K), "mxfp4", 2), "mxfp4")
+    gemm, scratch = mr.PreparedMxGemm(*mx, W), mr.Scratch(M, N, K, 8)
+    want = gemm().clone(), mr.router_gemv(x, w, scratch=scratch)
+    out = torch.empty_like(want[1])
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(200):
+        gemm(s[0])
+        mr.router_gemv(x, w, out=out, scratch=scratch, stream=s[1])
+    torch.cuda.synchronize()
+    assert torch.equal(gemm.out, want[0]) and torch.equal(out, want[1])
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_python_refusals(mr):
