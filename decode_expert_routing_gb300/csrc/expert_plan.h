@@ -7,8 +7,8 @@
 namespace mr {
 
 // Tiles of a weight [R, K]: RT tiles of 128 rows (gate/up: of 64 features,
-// both of their rows), KI stages of 128 code bytes, W scale words per row and
-// stage.
+// both of their rows), KI k-blocks of 128 code bytes a row, W scale words per
+// row and k-block.
 struct ExpertShape {
     int RT, KI, W;
 };
@@ -20,7 +20,10 @@ inline ExpertShape expert_shape(int R, int K, bool fp4, bool gate_up) {
     return s;
 }
 
-// Scratch of a down call: its products of mk assignments in bf16, rows of R.
+// Scratch of a down call: its products of mk assignments, rows of R.  They are
+// rounded to bf16 (half a step, 2^-8 of each, the precision of the result
+// itself): written and read once, they are the call's largest traffic next to
+// the weights.  4096 tokens x 8 x 6144: 265 us, of fp32 products 457.
 inline size_t expert_scratch_bytes(int64_t mk, int R) { return ((size_t)mk * (size_t)R * 2 + 255) / 256 * 256; }
 
 // Whether two CTAs share their activation rows (256 weight rows a tile): where

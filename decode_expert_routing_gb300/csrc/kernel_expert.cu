@@ -11,8 +11,8 @@ namespace mr {
 
 // One 32-bit word (four scales of one weight row) per thread, into the order
 // in which the tensor core takes them: for each expert, 128-row tile and
-// stage, words [32 lanes][4 groups of 32 rows] (twice for E2M1: a stage is two
-// words wide).  Tile row i of a gate/up weight is, 16 rows of either in turn,
+// k-block, words [32 lanes][4 groups of 32 rows] (twice for E2M1: a k-block is
+// two words wide).  Tile row i of a gate/up weight is, 16 rows of either in turn,
 // gate row or up row of the tile's 64 features.  Scales past the weight's
 // edge are zero bytes; they meet zero codes.
 __global__ void __launch_bounds__(256) mx_pack_kernel(const uint8_t* scale, uint32_t* packed, int64_t words, int R,
@@ -59,10 +59,19 @@ cudaError_t launch_mx_pack(const uint8_t* scale, int64_t E, int R, int K, int fp
 // ascending in fp32; slots whose id is outside [0, E) are skipped, whatever y
 // holds there.  A thread takes eight columns of a row (VEC; else one): eight
 // slots' rows are in flight at a time.  Bound by reading y: 4096 tokens x 8 x
-// 6144 is 403 MB.  Launched so that its CTAs are in place when the products
-// end (the wait is for all of them, and for the memory they wrote).
+// 6144 is 403 MB, 72 us (78 % of the peak bandwidth).  Launched so that its
+// CTAs are in place when the products end (the wait is for all of them, and
+// for the memory they wrote): CTAs of 64 threads find room for their registers
+// beside a CTA of the products; of 256 they did not, and started after them
+// (one token: 12.0 us for both launches, 12.7 with those).
+//
+// A launch of its own: added by the products' kernel, tokens finish when the
+// last of their experts does, and the CTA that sees it has all their sums to
+// do (4096 tokens: 4.0 ms; by panels of columns behind a grid barrier 339-433
+// us; the two launches 265).
+constexpr int kCombineThreads = 64;
 template <bool VEC>
-__global__ void __launch_bounds__(256) expert_combine_kernel(const __nv_bfloat16* y, const int32_t* ids,
+__global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(const __nv_bfloat16* y, const int32_t* ids,
                                                              const float* weights, const __nv_bfloat16* add,
                                                              __nv_bfloat16* out, int64_t M, int topk, int R, int E) {
     constexpr int N = VEC ? 8 : 1;
@@ -131,11 +140,11 @@ cudaError_t launch_combine(const ExpertCall& c, const __nv_bfloat16* y, int sms,
     auto* out = static_cast<__nv_bfloat16*>(c.out);
     const bool vec = c.R % 8 == 0 && (reinterpret_cast<uintptr_t>(add) | reinterpret_cast<uintptr_t>(out)) % 16 == 0;
     const int64_t work = (int64_t)c.M * (c.R / (vec ? 8 : 1));
-    int64_t ctas = (work + 255) / 256;
-    if (ctas > (int64_t)sms * 8) ctas = (int64_t)sms * 8;
+    int64_t ctas = (work + kCombineThreads - 1) / kCombineThreads;
+    if (ctas > (int64_t)sms * 32) ctas = (int64_t)sms * 32;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -274,8 +283,8 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     const bool pair = a.slices == 1 && expert_pair(a.mk, c.E);
     if (c.op == kExGemm) a.per = expert_gemm_rows(c.M, s.RT, pair, sms);
     cudaError_t e = c.op == kExGemm     ? launch_op<kExGemm>(a, fp4, pair, grid, st)
-                          : c.op == kExGateUp ? launch_op<kExGateUp>(a, fp4, pair, grid, st)
-                                              : launch_op<kExDown>(a, fp4, pair, grid, st);
+                    : c.op == kExGateUp ? launch_op<kExGateUp>(a, fp4, pair, grid, st)
+                                        : launch_op<kExDown>(a, fp4, pair, grid, st);
     if (e == cudaSuccess && c.op == kExDown) e = launch_combine(c, static_cast<const __nv_bfloat16*>(a.out), sms, st);
     *err = e;
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;

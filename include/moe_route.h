@@ -105,7 +105,9 @@ typedef enum mr_quant_format {
  * gate weight w at once, and waits for that kernel to complete before it
  * touches anything else (x, logits, ids, scratch, outputs).  The caller must
  * then not write w in the kernel launched just before the routing call on
- * the same stream.  With MR_LAUNCH_LEGACY_MMA the router GEMV of more than
+ * the same stream (where that one is a call of this library: nor in the one
+ * before it).  The expert products are always launched so, whatever the
+ * flags; they touch nothing before that wait.  With MR_LAUNCH_LEGACY_MMA the router GEMV of more than
  * 64 rows runs as the split-K GEMV with last-arriver fixup on warp-level
  * mma.sync instead of the tcgen05 cluster kernel (the two sum the split-K
  * partials in different orders, so their logits agree within fp32 rounding,
@@ -130,11 +132,11 @@ int mr_set_launch_flags(int flags);
 int mr_get_launch_flags(void);
 
 /*
- * Bounded waits.  (The expert products' waits, for their own copies and
- * products, are bounded and reported in the same way.)  The router GEMV for
- * M <= 64 and the one-launch route hand data between the CTAs of a thread-block cluster (split-K partials to the
+ * Bounded waits.  The router GEMV for M <= 64 and the one-launch route hand
+ * data between the CTAs of a thread-block cluster (split-K partials to the
  * CTA that owns a token, chosen ids to the CTA that sorts).  Each receiving
- * CTA waits for the bytes it expects at most the wait limit (default 1 s).
+ * CTA waits for the bytes it expects at most the wait limit (default 1 s);
+ * the expert products wait so for their own copies and products.
  * When a wait runs out the kernel sets a device-side flag and returns early;
  * the outputs of that call are undefined, and after a call with M > 16 the
  * scratch counters must be zeroed again (mr_scratch_reset).
