@@ -493,6 +493,22 @@ def test_down_on_another_stream_without_scratch(mr):
         assert all((o == 255).all() for o in other), "the call's scratch was handed on before it ran"
 
 
+@pytest.mark.parametrize("R", [64, 1024, 1032, 130])
+def test_down_touches_its_own_rows_of_the_scratch_only(mr, R):
+    """A call of fewer tokens than the scratch is made for, again and again beside other uses of its rest."""
+    M, E, topk, I, block = 19, 8, 3, 256, 16
+    ids, wts = routed(M, E, topk, 3, invalid=0.2)
+    st, ex, _ = mr.moe_sort(ids, E, block)
+    a, W = ref.random_mx((st.numel(), I), "mxfp4", 1), mr.MxWeight(*ref.random_mx((E, R, I), "mxfp4", 2), "mxfp4")
+    want = mr.moe_down(*a, W, ids, wts, st, ex, block)
+    scratch = mr.ExpertScratch(4 * M, topk, R)
+    rest = scratch.tensor[M * topk * R * 2:]
+    for i in range(20):
+        rest.fill_(i)
+        assert torch.equal(mr.moe_down(*a, W, ids, wts, st, ex, block, scratch=scratch), want)
+        assert (rest == i).all()
+
+
 def test_captured_after_copies_and_a_fork(mr):
     """In a graph the calls follow a copy, another stream's work and each other."""
     M, E, topk, K, I, block, fmt = 12, 8, 2, 512, 64, 16, "mxfp8"
