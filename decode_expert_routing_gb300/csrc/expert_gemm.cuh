@@ -14,7 +14,7 @@
 // bytes of codes a row (128 E4M3 or 256 E2M1 elements); a stage of the ring is
 // two of them while three such stages fit, else one.  One CTA per SM
 // walks the tiles.  Warp 0 copies the codes (tensor maps, 128-byte swizzle) and
-// the weights' scales (laid out once, see mx_pack_kernel), four warps the codes
+// the weights' scales (laid out once, see mx_pack_kernel), six warps the codes
 // of rows in token order, two the activations' scales (into the weights' scale
 // layout), warp 1 copies scales to tensor memory and issues the products, and
 // warps 4-11 read the accumulator back while the next tile is computed into
@@ -57,12 +57,14 @@
 
 namespace mr {
 
-// Warps: 0 copies, 1 products, 2-3 scales, 4-11 read back, and for gate/up 12-15 gather.
-__host__ __device__ constexpr int ex_threads(int op) { return op == 1 ? 512 : 384; }
+// Warps: 0 copies, 1 products, 2-3 scales, 4-11 read back, and for gate/up 12-17 gather.
+constexpr int kExGatherWarps = 6;
+__host__ __device__ constexpr int ex_threads(int op) { return op == 1 ? 384 + 32 * kExGatherWarps : 384; }
 constexpr int kExMaxStages = 12;
 constexpr int kExMaxN = 256;             // activation rows of a tile
 constexpr int kExWBytes = 128 * 128;     // weight codes of one k-block (128 bytes a row)
-constexpr int kExSmemDyn = 211 * 1024;   // dynamic shared memory (one CTA per SM)
+// Dynamic shared memory (one CTA per SM; what gate/up's static arrays leave).
+__host__ __device__ constexpr int ex_smem(int op) { return (op == 1 ? 209 : 211) * 1024; }
 constexpr int kExListMax = 1536;        // column tiles in the shared list
 constexpr int kExFewRows = 4;           // rows in token order that are copied one by one
 constexpr int kExSfCol = 488;            // tensor-memory columns of the scale factors
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_total, s_nmax, s_warp[kExThreads / 32];
     __shared__ __align__(16) int s_f[2][OP == kExGemm ? 4 : kExMaxN];
-    __shared__ int s_tok[4][OP == kExGateUp ? kExMaxN : 1];  // (each gathering warp) tokens of the tile's rows
+    __shared__ int s_tok[kExGatherWarps][OP == kExGateUp ? kExMaxN : 1];  // (each gathering warp) tokens of the tile's rows
     __shared__ __align__(16) unsigned char s_act[OP == kExGateUp ? 4 * 16 * kExStagePitch : 16];
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
     const bool gather = OP == kExGateUp && a.gather;
@@ -502,9 +504,11 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
     const uint32_t dyn = smem_u32(dsm);
     const uint32_t base = (dyn + (uint32_t)a.list_cap * 8u + (uint32_t)(3 * a.E + 1) * 4u + 1023u) & ~1023u;
     const uint32_t code_bytes = (uint32_t)(kExWBytes + xrows * (PAIR ? 64 : 128)), sf_bytes = (uint32_t)(W * 512 * (1 + H));
-    // k-blocks that fit, in stages of D: a stage has its waits and its arrivals whatever it holds
-    const int fit = (int)ex_div(dyn + (uint32_t)kExSmemDyn - base, code_bytes + sf_bytes);
-    const int D = fit >= 6 ? 2 : 1, nst = min(kExMaxStages, D == 2 ? fit >> 1 : fit);
+    // k-blocks that fit, in stages of D: a stage has its waits and its arrivals whatever it holds.  (One of a tile of
+    // many gathered rows holds one k-block, so that every gathering warp has its own: gate/up of 2048 tokens in token
+    // order, E4M3, 210 us, of stages of two 252.)
+    const int fit = (int)ex_div(dyn + (uint32_t)ex_smem(OP) - base, code_bytes + sf_bytes);
+    const int D = fit >= 6 && !(gather && xrows >= 128) ? 2 : 1, nst = min(kExMaxStages, D == 2 ? fit >> 1 : fit);
     const uint32_t stage_bytes = (uint32_t)D * code_bytes, sf_stage = (uint32_t)D * sf_bytes;
     const uint32_t sf_base = base + (uint32_t)nst * stage_bytes;
     walk.end = total;
@@ -711,14 +715,14 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
             }
         }
     } else if (OP == kExGateUp && warp >= 12) {
-        // ---- codes of rows in token order: the stages in turn, one of up to four warps each, which copies the rows
+        // ---- codes of rows in token order: the stages in turn, one of up to six warps each, which copies the rows
         // (16 bytes a lane), waits for them and passes the stage on; the others' stages are under way meanwhile.
         // (With more of them in flight in one warp its proxy fence, which has to be its own, waits for all.)  A tile
         // of up to four rows, as decode steps have them, takes a tensor-map copy of each instead, which counts on
         // the stage's own barrier (one token's gate/up: 17.0 instead of 20.7 us).
         // At most nst warps: the one before it in a warp's turn tells that a stage's slot is at most one use behind,
         // as a wait by parity needs it.
-        const int takers = min(4, nst), which = warp - 12;
+        const int takers = min(kExGatherWarps, nst), which = warp - 12;
         int* tok = s_tok[which];
         const int quad = lane >> 3, chunk = lane & 7;  // this lane's row of four and 16-byte chunk
         bool ok = gather && which < takers;

@@ -197,7 +197,7 @@ cudaError_t launch_one(const ExpertArgs& a, int grid, cudaStream_t st) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     const auto kernel = expert_kernel<FP4, OP, PAIR, SPLIT>;
     if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmemDyn);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ex_smem(OP));
         if (e != cudaSuccess) return e;
         __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
     }
@@ -205,7 +205,7 @@ cudaError_t launch_one(const ExpertArgs& a, int grid, cudaStream_t st) {
     const int of = PAIR ? 2 : SPLIT ? a.slices : 1;  // CTAs of a cluster
     cfg.gridDim = dim3((unsigned)(grid / of * of));
     cfg.blockDim = dim3(ex_threads(OP));
-    cfg.dynamicSmemBytes = kExSmemDyn;
+    cfg.dynamicSmemBytes = ex_smem(OP);
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
