@@ -62,10 +62,12 @@ inline int expert_slices(int64_t mk, int E, const ExpertShape& s, int ctas, int*
 // as 256 + rows (the loads of a stage: its weight rows and its activation
 // rows).  4096 x 6144 x 6144, E2M1: tiles of 224 rows, 6 full rounds, 51.5 us;
 // of 256, 5.05 of 6 rounds, 54.5.
-inline int expert_gemm_rows(int M, int RT, bool pair, int ctas) {
+// Where slices CTAs share a tile, the clusters are all there is: one round, which
+// tiles of 256 rows fit (expert_slices) and is cheaper than any two.
+inline int expert_gemm_rows(int M, int RT, bool pair, int slices, int ctas) {
     const int step = pair ? 32 : 16;
     if (M <= 256) return (M + step - 1) / step * step;
-    const int slots = pair ? ctas / 2 : ctas, rows = pair ? (RT + 1) / 2 : RT;
+    const int slots = ctas / (pair ? 2 : slices), rows = pair ? (RT + 1) / 2 : RT;
     int best = 256;
     int64_t least = INT64_MAX;
     for (int per = 256; per >= 128; per -= step) {

@@ -298,7 +298,7 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     const int grid = sms;
     a.slices = expert_slices(a.mk, c.E, s, sms, &a.slice_len);
     const bool pair = a.slices == 1 && expert_pair(a.mk, c.E);
-    if (c.op == kExGemm) a.per = expert_gemm_rows(c.M, s.RT, pair, sms);
+    if (c.op == kExGemm) a.per = expert_gemm_rows(c.M, s.RT, pair, a.slices, sms);
     cudaError_t e = c.op == kExGemm     ? launch_op<kExGemm>(a, fp4, pair, grid, st)
                     : c.op == kExGateUp ? launch_op<kExGateUp>(a, fp4, pair, grid, st)
                                         : launch_op<kExDown>(a, fp4, pair, grid, st);

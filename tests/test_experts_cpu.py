@@ -2,6 +2,8 @@
 refusals, the binding's parameter blocks.  No call here reaches a kernel."""
 
 import ctypes
+import os
+import subprocess
 
 import pytest
 
@@ -102,3 +104,63 @@ def test_null_parameter_blocks(lib):
     assert lib.mr_mx_pack_scales(None, 1, 128, 128, 1, 0, P, None) == mr.MR_ERR_INVALID_ARG
     assert lib.mr_mx_pack_scales(P, 1, 128, 128, 1, 0, P + 8, None) == mr.MR_ERR_INVALID_ARG
     assert lib.mr_mx_pack_scales(P, 1, 128, 100, 1, 0, P, None) == mr.MR_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ the launch's shape
+
+PROBE = r'''
+#include <cstdio>
+#include "expert_plan.h"
+static unsigned seed = 1;
+static int rnd(int n) { seed = seed * 1664525u + 1013904223u; return (int)((seed >> 8) % (unsigned)n); }
+int main() {
+    long split = 0, bad = 0;
+    for (int i = 0; i < 400000; ++i) {
+        const bool fp4 = rnd(2), gate_up = rnd(3) == 0;
+        const int R = gate_up ? 64 * (1 + rnd(40)) : 1 + rnd(rnd(2) ? 300 : 6144), K = 32 * (1 + rnd(600));
+        const int ctas = rnd(3) ? 152 : 16 + rnd(140);
+        const mr::ExpertShape s = mr::expert_shape(R, K, fp4, gate_up);
+        const bool gemm = !gate_up && rnd(2);
+        const int E = gemm ? 1 : 1 + rnd(rnd(2) ? 8 : 200), mk = 1 + rnd(rnd(2) ? 64 : 3000);
+        int len = 0;
+        const int n = mr::expert_slices(mk, E, s, ctas, &len);
+        const bool pair = n == 1 && mr::expert_pair(mk, E);
+        if (n > 1) {
+            ++split;
+            const int group = 4 / s.W;
+            if ((n != 2 && n != 4 && n != 8) || len % group != 0 || (long)len * (n - 1) >= s.KI || (long)len * n < s.KI) ++bad;
+        } else if (len != s.KI) ++bad;
+        long tiles = 0;
+        if (gemm) {
+            const int per = mr::expert_gemm_rows(mk, s.RT, pair, n, ctas);
+            if (per < 16 || per > 256 || per % (pair ? 32 : 16)) ++bad;
+            tiles = ((long)mk + per - 1) / per * s.RT;
+        } else {  // any distribution of the assignments over the experts; a run has up to 15 rows more
+            int left = mk;
+            for (int e = 0; e < E && left > 0; ++e) {
+                int rows = e + 1 == E ? left : rnd(3) == 0 ? 1 + rnd(left) : 1 + rnd(left < 300 ? left : 300);
+                if (rows > left) rows = left;
+                left -= rows;
+                tiles += ((rows + 15) / 16 * 16 + 255) / 256;
+            }
+            tiles *= s.RT;
+        }
+        if (n > 1 && tiles > ctas / n) {
+            if (++bad < 5) printf("E %d mk %d R %d K %d fp4 %d ctas %d: %ld tiles, %d slices\n", E, mk, R, K, fp4, ctas, tiles, n);
+        }
+    }
+    printf("%ld %ld\n", split, bad);
+}
+'''
+
+
+def test_every_tile_of_a_split_has_a_cluster(tmp_path):
+    """A cluster whose CTAs share a tile's K range takes one tile: the host's rule leaves none over."""
+    src, exe = tmp_path / "probe.cpp", tmp_path / "probe"
+    src.write_text(PROBE)
+    csrc = os.path.join(os.path.dirname(os.path.abspath(mr.__file__)), "csrc")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(mrbuild.nvcc())), "include")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", csrc, "-I", cuda, "-o", str(exe), str(src)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
+    split, bad = map(int, out.split("\n")[-2].split())
+    assert split > 1000 and bad == 0, out

@@ -432,6 +432,13 @@ def test_mx_gemm_of_few_tiles(mr, fmt, M, R, K):
     assert torch.equal(mr.mx_gemm(*x, W), mr.mx_gemm(*x, W))
 
 
+@pytest.mark.parametrize("fmt,M,R,K", [
+    ("mxfp8", 895, 1420, 4736), ("mxfp4", 895, 1420, 9472), ("mxfp8", 520, 1700, 6144), ("mxfp8", 400, 700, 8192)])
+def test_mx_gemm_of_few_tiles_of_many_rows(mr, fmt, M, R, K):
+    """Where narrower tiles would fill the CTAs, but not the clusters that share a tile's K range."""
+    test_mx_gemm(mr, fmt, M, R, K)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,E,topk,K,I,block,invalid,skew", [
     (1, 8, 2, 6144, 64, 16, 0.0, 0), (5, 4, 2, 4128, 96, 16, 0.3, 0), (40, 2, 2, 5152, 32, 8, 0.0, 0),
