@@ -646,24 +646,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 }
                 row[g] = a.x_scale + src * a.lds;
             }
-            auto load = [&](uint4 (&v)[4], int b) {  // b: first scale byte
-                if (a.sf_vec == 1) {
-                    uint4 lo[4], hi[4];
-                    bool whole[4];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {  // (every group's loads before the first use)
-                        const uint8_t* p = row[g] + b - (reinterpret_cast<uintptr_t>(row[g] + b) & 15u);
-                        whole[g] = p >= a.x_scale && p + 32 <= a.x_scale_end;
-                        const bool get = whole[g] && g < G && b < a.kb;
-                        lo[g] = get ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
-                        hi[g] = get ? __ldg(reinterpret_cast<const uint4*>(p) + 1) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        v[g] = g < G && b < a.kb ? ex_scales16(row[g] + b, a.kb - b, lo[g], hi[g], whole[g])
-                                                 : make_uint4(0u, 0u, 0u, 0u);
-                    return;
-                }
+            auto load = [&](uint4 (&v)[4], int b) {  // b: first scale byte (rows that are read in 8 or 16 bytes)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     v[g] = make_uint4(0u, 0u, 0u, 0u);
@@ -677,6 +660,25 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                         v[g] = make_uint4(lo.x, lo.y, hi.x, hi.y);
                     }
                 }
+            };
+            // rows that start anywhere: the two aligned 16 bytes around the ones from byte b (near: where they do not
+            // leave the array), shifted into place only when they are due
+            auto near = [&](int g, int b) { return row[g] + b - (reinterpret_cast<uintptr_t>(row[g] + b) & 15u); };
+            auto whole = [&](const uint8_t* p) { return p >= a.x_scale && p + 32 <= a.x_scale_end; };
+            auto load_any = [&](uint4 (&lo)[4], uint4 (&hi)[4], int b) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const uint8_t* p = near(g, b);
+                    const bool get = whole(p) && g < G && b < a.kb;
+                    lo[g] = get ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+                    hi[g] = get ? __ldg(reinterpret_cast<const uint4*>(p) + 1) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            auto shift = [&](uint4 (&v)[4], const uint4 (&lo)[4], const uint4 (&hi)[4], int b) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    v[g] = g < G && b < a.kb ? ex_scales16(row[g] + b, a.kb - b, lo[g], hi[g], whole(near(g, b)))
+                                             : make_uint4(0u, 0u, 0u, 0u);
             };
             auto store = [&](const uint4 (&v)[4], int k0) {
 #pragma unroll
@@ -705,6 +707,16 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 return true;
             };
             uint4 v0[4], v1[4];
+            if (a.sf_vec == 1) {
+                uint4 v[4];
+                load_any(v0, v1, kb0 * W * 4);
+                for (int k0 = kb0; ok && k0 < kb1; k0 += B) {
+                    shift(v, v0, v1, k0 * W * 4);
+                    load_any(v0, v1, (k0 + B) * W * 4);
+                    ok = store(v, k0);
+                }
+                continue;
+            }
             load(v0, kb0 * W * 4);
             for (int k0 = kb0; ok && k0 < kb1; k0 += 2 * B) {
                 load(v1, (k0 + B) * W * 4);
