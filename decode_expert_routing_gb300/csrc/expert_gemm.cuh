@@ -33,8 +33,8 @@
 // PAIR: two CTAs of a cluster form tiles of 256 weight rows, each with its own
 // 128 and half of the activation rows (cta_group::2): a stage is 16 KB + 64 n
 // bytes instead of 16 KB + 128 n.  Loads from L2 (about 16 TB/s over all SMs)
-// bound tiles of many rows, so it takes them: gate/up of 32768 rows 302 -> 275
-// us, the E2M1 product 4096 x 6144 x 6144 62 -> 56 us.
+// bound tiles of many rows, so it takes them: gate/up of 32768 rows, E4M3, 280
+// us (314 alone), the E2M1 product 4096 x 6144 x 6144 50 us (60 alone).
 //
 // SPLIT: where there are too few tiles for the SMs, the CTAs of a cluster share
 // a tile's K range.  Each keeps its sums in its tensor memory; then every CTA
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
         // (16 bytes a lane), waits for them and passes the stage on; the others' stages are under way meanwhile.
         // (With more of them in flight in one warp its proxy fence, which has to be its own, waits for all.)  A tile
         // of up to four rows, as decode steps have them, takes a tensor-map copy of each instead, which counts on
-        // the stage's own barrier (one token's gate/up: 17.0 instead of 20.7 us).
+        // the stage's own barrier (one token's gate/up: 16.8 instead of 20.3 us).
         // At most nst warps: the one before it in a warp's turn tells that a stage's slot is at most one use behind,
         // as a wait by parity needs it.
         const int takers = min(kExGatherWarps, nst), which = warp - 12;

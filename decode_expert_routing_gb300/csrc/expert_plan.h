@@ -28,9 +28,9 @@ inline size_t expert_scratch_bytes(int64_t mk, int R) { return ((size_t)mk * (si
 
 // Whether two CTAs share their activation rows (256 weight rows a tile): where
 // an expert has 16 rows or more on average, and there are 64 in all.  Gate/up
-// of 1001 tokens x 8 over 128 experts, E2M1: 118 us as pairs, 139 alone; of 256
-// tokens, E4M3: 191 and 200; of 128: 179 and 178.  A product of 64 rows with
-// 6144 x 6144, E4M3: 11.9 and 12.5; of 33, E2M1: 7.8 and 7.5.
+// of 1001 tokens x 8 over 128 experts, E2M1: 119 us as pairs, 139 alone; of 256
+// tokens, E4M3: 190 and 199; of 128: 177 and 176.  A product of 64 rows with
+// 6144 x 6144, E4M3, not split: 12.2 and 12.7; of 33, E2M1: 7.8 and 7.6.
 inline bool expert_pair(int64_t mk, int E) { return mk >= 64 && mk >= 16 * (int64_t)E; }
 
 // CTAs that share a tile's K range (1: none do), where the tiles leave SMs
@@ -38,8 +38,8 @@ inline bool expert_pair(int64_t mk, int E) { return mk >= 64 && mk >= 16 * (int6
 // wait), with a tile for every cluster; *len is each one's k-blocks, a multiple
 // of those whose scales are 16 bytes of a row.  A k-block takes 0.2 us or more;
 // handing the sums over 1.5 us and the columns' way through distributed shared
-// memory (some 90 bytes a cycle for a cluster).  64 x 500 x 6144, E4M3: 6.2 us
-// in 8 slices, 10.8 in one; 300 x 2000 x 2976: 16.7 in 4, 20.4 in one.
+// memory (some 90 bytes a cycle for a cluster).  64 x 500 x 6144, E4M3: 6.7 us
+// in slices, 11.2 in one; 33 x 6144 x 6144: 10.4 in 2, 12.2 in one.
 inline int expert_slices(int64_t mk, int E, const ExpertShape& s, int ctas, int* len) {
     // (a run of blocks has at most 15 rows more than assignments)
     const int64_t hit = mk < E ? mk : E, tiles = (hit + (mk + 15 * hit) / 256) * s.RT;
@@ -60,8 +60,8 @@ inline int expert_slices(int64_t mk, int E, const ExpertShape& s, int ctas, int*
 // Rows of a gemm's column tiles (a multiple of 16, of 32 for pairs; at most
 // 256): of the sizes, the one whose rounds of tiles cost least, a round taken
 // as 256 + rows (the loads of a stage: its weight rows and its activation
-// rows).  4096 x 6144 x 6144, E2M1: tiles of 224 rows, 6 full rounds, 51.5 us;
-// of 256, 5.05 of 6 rounds, 54.5.
+// rows).  4096 x 6144 x 6144, E2M1: tiles of 224 rows, 6 full rounds, 50.4 us;
+// of 256, 5.05 of 6 rounds, 52.9.
 // Where slices CTAs share a tile, the clusters are all there is: one round, which
 // tiles of 256 rows fit (expert_slices) and is cheaper than any two.
 inline int expert_gemm_rows(int M, int RT, bool pair, int slices, int ctas) {
