@@ -83,6 +83,17 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same where the receiver goes on to use this CTA's shared memory: first
+// a release at cluster scope of what was written there, by this thread or by
+// others that it has waited for, so that a wait that acquires has it before
+// it.  The fence is restricted to this CTA's shared memory: it need not wait
+// for anyone's writes to global memory, as the arrival's own release does.
+__device__ __forceinline__ void mbar_arrive_remote_shared(uint32_t bar) {
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+        : "memory");
+}
 // One arrival on a local mbarrier.
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
