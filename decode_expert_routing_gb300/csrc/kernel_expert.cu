@@ -15,8 +15,14 @@ namespace mr {
 // two words wide).  Tile row i of a gate/up weight is, 16 rows of either in turn,
 // gate row or up row of the tile's 64 features.  Scales past the weight's
 // edge are zero bytes; they meet zero codes.
+//
+// Nothing is touched before the kernel launched before has ended: it may be
+// the quantiser that writes scale, or a product that still reads packed.  The
+// kernel after this one relies on the same wait: its own covers this kernel,
+// and so all before.
 __global__ void __launch_bounds__(256) mx_pack_kernel(const uint8_t* scale, uint32_t* packed, int64_t words, int R,
                                                       int RT, int KI, int kb, int W, int gate_up) {
+    pdl_wait();
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += (int64_t)gridDim.x * blockDim.x) {
         const int row = (int)(i & 3) * 32 + (int)((i >> 2) & 31);
         int64_t u = i >> 7;
