@@ -660,10 +660,65 @@ def shared_gate_up(x, w13, w13_scale, out=None, stream=None):
     return out
 
 
+def _torch_stream(device, raw: int):
+    """The torch stream of a raw cudaStream_t (0 and 1: the default stream,
+    which ExternalStream does not take)."""
+    torch = _torch()
+    return torch.cuda.default_stream(device) if raw in (0, 1) else torch.cuda.ExternalStream(raw, device=device)
+
+
+def _given_stream(device, stream):
+    """A torch stream of a call's stream argument (a torch stream or a raw
+    cudaStream_t of that device), or None."""
+    if stream is None:
+        return None
+    if isinstance(stream, int):
+        return _torch_stream(device, stream)
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}")
+    return stream
+
+
 class _Prepared:
     """A call over fixed buffers: its parameter block is built and checked
     once, and each call is one ABI call on the given (or torch's current)
-    stream.  The tensors are referenced for the object's life."""
+    stream.  The tensors are referenced for the object's life.  Outputs and
+    scratch that an expert product's object makes itself are memory of the
+    stream that is current then, and may be used on any."""
+
+    _home, _made, _weights, _ready, _captured, _streams = None, (), (), None, False, None
+
+    def _own(self, made, weights, once):
+        """made: the buffers that the object made itself, on the stream that
+        is current now.  Their memory may have been given back there a moment
+        ago, with work on it still to run, and goes back there when the object
+        goes: the first call on another stream waits for what is queued now,
+        and is waited for then.  weights: the call's MxWeights, whose packed
+        scales are kept for each stream likewise.  once: the object is called
+        at once and on the current stream only."""
+        torch = _torch()
+        self._home = torch._C._cuda_getCurrentRawStream(self.device.index)
+        self._made, self._weights, self._streams = [t for t in made if t is not None], weights, set()
+        if self._made and not once:
+            with _launch_ctx(self.device):
+                self._captured = torch.cuda.is_current_stream_capturing()
+                self._ready = torch.cuda.Event()
+                self._ready.record()
+
+    def _first_on(self, sp):
+        """The object's first call on the stream sp."""
+        torch = _torch()
+        if sp != self._home and self._made:
+            own = _torch_stream(self.device, sp)
+            with torch.cuda.stream(own):
+                # (a capture takes no event from outside; what was queued before it has run when the graph does)
+                if self._ready is not None and torch.cuda.is_current_stream_capturing() == self._captured:
+                    own.wait_event(self._ready)
+            for t in self._made:
+                t.record_stream(own)
+        for w in self._weights:
+            w._used_on(sp)
+        self._streams.add(sp)
 
     def __call__(self, stream=None):
         """Launch on the buffers' device; stream: a torch stream of that
@@ -679,6 +734,8 @@ class _Prepared:
             if stream.device != self.device:
                 raise ValueError(f"stream must be on {self.device}")
             sp = stream.cuda_stream
+        if self._streams is not None and sp not in self._streams:
+            self._first_on(sp)
         if torch.cuda.current_device() == index:
             status = self._fn(self._ref, sp)
         else:
@@ -814,12 +871,32 @@ def moe_sort_quant(topk_ids, x, num_experts: int, block: int, quant: str = "mxfp
 
 # ---------------------------------------------------------------- expert products
 
+def _call_once(device, stream, make):
+    """One call of make(), a prepared form, on the given (or torch's current)
+    stream.  Buffers that it makes itself come from that stream's memory, as
+    if it were the current one; the result is kept for the current one too."""
+    own = _given_stream(device, stream)
+    if own is None:
+        return make()()
+    torch = _torch()
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(own):
+        call = make()
+        call()
+    if here != own:
+        for t in call.out if isinstance(call.out, tuple) else (call.out,):
+            if any(t is m for m in call._made):
+                t.record_stream(here)
+    return call.out
+
+
 class MxWeight:
     """An MX weight of mx_gemm ([R, K]) or of the experts ([E, R, K]): codes
     uint8 (E4M3 [..., K], or E2M1 [..., K/2] as mxfp4_quant packs them) and
     E8M0 scale bytes [..., K/32], both contiguous.  The codes are used where
     they are; the scales are laid out once for the tensor core, here, on the
-    given (or torch's current) stream (refresh() after changing them).
+    given (or torch's current) stream (refresh() after changing them), in
+    memory of that stream; calls on other streams have to come after it.
     gate_up: the weight of moe_gate_up, R = 2I with the gate rows first."""
 
     def __init__(self, codes, scale, format: str = "mxfp8", gate_up: bool = False, stream=None):
@@ -840,16 +917,28 @@ class MxWeight:
         n = int(_load().mr_mx_packed_scale_bytes(self.E, self.R, self.K, QUANT_FORMAT[format], int(self.gate_up)))
         if n == 0:
             raise MoeRouteUnsupported(MR_ERR_UNSUPPORTED, "mr_mx_packed_scale_bytes")
-        self.packed = torch.empty(n, dtype=torch.uint8, device=dev)
+        with torch.cuda.stream(_given_stream(dev, stream)):
+            self.packed = torch.empty(n, dtype=torch.uint8, device=dev)
+            self._streams = {torch._C._cuda_getCurrentRawStream(dev.index)}
         self.refresh(stream)
 
     def refresh(self, stream=None):
         """Lay the scales out again (after they were changed in place)."""
+        torch = _torch()
+        own = _given_stream(self.device, stream) or torch.cuda.current_stream(self.device)
+        self._used_on(own.cuda_stream)
         with _launch_ctx(self.device):
             _check(_load().mr_mx_pack_scales(ctypes.c_void_p(self.scale.data_ptr()), self.E, self.R, self.K,
                                              QUANT_FORMAT[self.format], int(self.gate_up),
                                              ctypes.c_void_p(self.packed.data_ptr()),
-                                             _stream_on(self.device, stream)), "mr_mx_pack_scales")
+                                             ctypes.c_void_p(own.cuda_stream)), "mr_mx_pack_scales")
+
+    def _used_on(self, sp):
+        """The packed scales are used on the stream sp: their memory is not
+        given to others before that stream is done with them."""
+        if sp not in self._streams:
+            self.packed.record_stream(_torch_stream(self.device, sp))
+            self._streams.add(sp)
 
 
 class ExpertScratch:
@@ -923,14 +1012,15 @@ def _check_sorted(st, ex, block, dev):
 class PreparedMxGemm(_Prepared):
     """mx_gemm over fixed buffers; arguments as mx_gemm."""
 
-    def __init__(self, q, scale, w: MxWeight, out=None, out_dtype=None):
+    def __init__(self, q, scale, w: MxWeight, out=None, out_dtype=None, _once=False):
         torch = _torch()
         if w.codes.dim() != 2 or w.gate_up:
             raise ValueError("mx_gemm takes a weight [R, K] laid out without gate_up")
         dev = _one_device(q=q, scale=scale, w=w.codes, out=out)
         p = self.p = MxGemmParams()
         M = _mx_rows(p, q, scale, w.K, w.format)
-        if out is None:
+        made = out is None
+        if made:
             out = torch.empty((M, w.R), dtype=out_dtype or torch.bfloat16, device=dev)
         elif out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
@@ -944,20 +1034,21 @@ class PreparedMxGemm(_Prepared):
         self.out, self.device, self._keep = out, dev, (q, scale, w)
         self._ref = ctypes.byref(p)
         self._fn, self._name = _load().mr_mx_gemm, "mr_mx_gemm"
+        self._own((out,) if made else (), (w,), _once)
 
 
 def mx_gemm(q, scale, w: MxWeight, out=None, out_dtype=None, stream=None):
     """Product of microscaled operands: [M, R] (bf16, or out_dtype fp32) =
     x [M, K] @ w [R, K]^T with x given as the codes q and scales of
     mxfp8_quant / mxfp4_quant, in the weight's format."""
-    return PreparedMxGemm(q, scale, w, out, out_dtype)(stream)
+    return _call_once(_one_device(q=q), stream, lambda: PreparedMxGemm(q, scale, w, out, out_dtype, _once=True))
 
 
 class PreparedGateUp(_Prepared):
     """moe_gate_up over fixed buffers; arguments as moe_gate_up."""
 
     def __init__(self, q, scale, w13: MxWeight, sorted_token_ids, expert_ids, topk: int, block: int,
-                 num_tokens: int | None = None, sorted_rows: bool = False, quant=None, out=None):
+                 num_tokens: int | None = None, sorted_rows: bool = False, quant=None, out=None, _once=False):
         torch = _torch()
         if w13.codes.dim() != 3 or not w13.gate_up:
             raise ValueError("moe_gate_up takes a weight [E, 2I, K] laid out with gate_up=True")
@@ -979,6 +1070,7 @@ class PreparedGateUp(_Prepared):
         M = num_tokens if sorted_rows else rows
         I = w13.R // 2
         cap = sorted_token_ids.numel()
+        made = out is None
         if quant is None:
             if o0 is None:
                 o0 = torch.empty((cap, I), dtype=torch.bfloat16, device=dev)
@@ -1002,6 +1094,7 @@ class PreparedGateUp(_Prepared):
         self.out, self.device, self._keep = out, dev, (q, scale, w13, sorted_token_ids, expert_ids)
         self._ref = ctypes.byref(p)
         self._fn, self._name = _load().mr_moe_gate_up, "mr_moe_gate_up"
+        self._own((o0, o1) if made else (), (w13,), _once)
 
 
 def moe_gate_up(q, scale, w13: MxWeight, sorted_token_ids, expert_ids, topk: int, block: int,
@@ -1013,15 +1106,16 @@ def moe_gate_up(q, scale, w13: MxWeight, sorted_token_ids, expert_ids, topk: int
     number of tokens).  quant None: bf16 [capacity, I]; "mxfp8" / "mxfp4":
     (codes, scales), as mxfp8_quant / mxfp4_quant of those rows.  Rows that
     hold no assignment are left as they were."""
-    return PreparedGateUp(q, scale, w13, sorted_token_ids, expert_ids, topk, block, num_tokens, sorted_rows, quant,
-                          out)(stream)
+    return _call_once(_one_device(q=q), stream,
+                      lambda: PreparedGateUp(q, scale, w13, sorted_token_ids, expert_ids, topk, block, num_tokens,
+                                             sorted_rows, quant, out, _once=True))
 
 
 class PreparedDown(_Prepared):
     """moe_down over fixed buffers; arguments as moe_down."""
 
     def __init__(self, q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, expert_ids, block: int,
-                 add=None, out=None, scratch: ExpertScratch | None = None):
+                 add=None, out=None, scratch: ExpertScratch | None = None, _once=False):
         torch = _torch()
         if w2.codes.dim() != 3 or w2.gate_up:
             raise ValueError("moe_down takes a weight [E, R, I] laid out without gate_up")
@@ -1039,11 +1133,14 @@ class PreparedDown(_Prepared):
         _check_out(topk_weights, "topk_weights", (M, topk), torch.float32, dev)
         if add is not None:
             _check_out(add, "add", (M, w2.R), torch.bfloat16, dev)
+        made = []
         if out is None:
             out = torch.empty((M, w2.R), dtype=torch.bfloat16, device=dev)
+            made.append(out)
         _check_out(out, "out", (M, w2.R), torch.bfloat16, dev)
         if scratch is None:
             scratch = ExpertScratch(M, topk, w2.R, device=dev)
+            made.append(scratch.tensor)
         _check_scratch(scratch, dev)
         p.w2, p.w2_scale = w2.codes.data_ptr(), w2.packed.data_ptr()
         p.E, p.R, p.I, p.format = w2.E, w2.R, w2.K, QUANT_FORMAT[w2.format]
@@ -1058,6 +1155,7 @@ class PreparedDown(_Prepared):
         self.scratch = scratch
         self._ref = ctypes.byref(p)
         self._fn, self._name = _load().mr_moe_down, "mr_moe_down"
+        self._own(made, (w2,), _once)
 
 
 def moe_down(q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, expert_ids, block: int, add=None,
@@ -1067,12 +1165,6 @@ def moe_down(q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, e
     act @ w2^T.  q, scale: act's codes and scales at the sorted positions, as
     moe_gate_up(..., quant=...) returns them.  Slots whose id is outside
     [0, E) add nothing."""
-    call = PreparedDown(q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, block, add, out, scratch)
-    call(stream)
-    if scratch is None and stream is not None:
-        # its memory goes back to the current stream's pool when this returns, but not before the call's own stream
-        # is done with it
-        torch = _torch()
-        own = torch.cuda.ExternalStream(stream, device=call.device) if isinstance(stream, int) else stream
-        call.scratch.tensor.record_stream(own)
-    return call.out
+    return _call_once(_one_device(q=q), stream,
+                      lambda: PreparedDown(q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, block, add,
+                                           out, scratch, _once=True))
