@@ -914,8 +914,12 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                         const float mine = __uint_as_float(hi ? v[2 * j + 1] : v[2 * j]);
                         const float other = __shfl_xor_sync(kFull, __uint_as_float(hi ? v[2 * j] : v[2 * j + 1]), 16);
                         const float gv = hi ? other : mine, uv = hi ? mine : other;
-                        // (the quotient is good to 2 ulps; where e^-g is past 2^126 it is 0, and silu below 2^-119)
-                        const float s = __fdividef(gv, 1.0f + expf(-gv)) * uv;
+                        // silu from t = e^-|g|, which cannot overflow: g / (1 + t), or g t / (1 + t) below 0.  The
+                        // divisor is 1 to 2, where the quotient is good to 2 ulps.  (g / (1 + e^-g) with this quotient
+                        // is 0 below -87.3, where silu times a large up value is not.  4096 tokens, E4M3: 287 us with this,
+                        // 286 with that; one token 16.4 and 16.5, 17.0 with that one's quotient rounded to nearest.)
+                        const float t = expf(-fabsf(gv));
+                        const float s = __fdividef(gv < 0.0f ? gv * t : gv, 1.0f + t) * uv;
                         *reinterpret_cast<__nv_bfloat16*>(put0 + 2 * j * kExStagePitch) = __float2bfloat16_rn(s);
                     }
                     ex_sync(2 + grp, 128, true);
