@@ -944,11 +944,11 @@ class MxWeight:
 class ExpertScratch:
     """A caller-owned scratch buffer of moe_down for up to M_max tokens of
     topk slots and R output columns (a torch uint8 tensor; its contents do
-    not matter between calls)."""
+    not matter between calls).  slots_fp32: also for calls with it."""
 
-    def __init__(self, M_max: int, topk: int, R: int, device=None):
+    def __init__(self, M_max: int, topk: int, R: int, device=None, slots_fp32: bool = False):
         torch = _torch()
-        self.nbytes = int(_load().mr_expert_scratch_bytes(M_max, topk, R))
+        self.nbytes = int(_load().mr_expert_scratch_bytes(M_max, topk, 2 * R if slots_fp32 else R))
         if self.nbytes == 0:
             raise ValueError("scratch size query rejected the arguments")
         self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=device if device is not None else "cuda")
@@ -977,7 +977,7 @@ class DownParams(ctypes.Structure):
     _fields_ = [("q", _P), ("ldq", _I64), ("scale", _P), ("lds", _I64), ("w2", _P), ("w2_scale", _P), ("E", _I),
                 ("R", _I), ("I", _I), ("format", _I), ("sorted_token_ids", _P), ("expert_ids", _P), ("n_blocks", _I),
                 ("block", _I), ("M", _I), ("topk", _I), ("topk_ids", _P), ("topk_weights", _P), ("add", _P),
-                ("out", _P), ("scratch", _P), ("scratch_bytes", _SZ)]
+                ("out", _P), ("scratch", _P), ("scratch_bytes", _SZ), ("slots_fp32", _I)]
 
 
 def _mx_rows(p, q, scale, K, fmt, what="q"):
@@ -1115,7 +1115,7 @@ class PreparedDown(_Prepared):
     """moe_down over fixed buffers; arguments as moe_down."""
 
     def __init__(self, q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, expert_ids, block: int,
-                 add=None, out=None, scratch: ExpertScratch | None = None, _once=False):
+                 add=None, out=None, scratch: ExpertScratch | None = None, slots_fp32: bool = False, _once=False):
         torch = _torch()
         if w2.codes.dim() != 3 or w2.gate_up:
             raise ValueError("moe_down takes a weight [E, R, I] laid out without gate_up")
@@ -1139,7 +1139,7 @@ class PreparedDown(_Prepared):
             made.append(out)
         _check_out(out, "out", (M, w2.R), torch.bfloat16, dev)
         if scratch is None:
-            scratch = ExpertScratch(M, topk, w2.R, device=dev)
+            scratch = ExpertScratch(M, topk, w2.R, device=dev, slots_fp32=slots_fp32)
             made.append(scratch.tensor)
         _check_scratch(scratch, dev)
         p.w2, p.w2_scale = w2.codes.data_ptr(), w2.packed.data_ptr()
@@ -1149,7 +1149,7 @@ class PreparedDown(_Prepared):
         p.topk_ids, p.topk_weights = topk_ids.data_ptr(), topk_weights.data_ptr()
         p.add = None if add is None else add.data_ptr()
         p.out = out.data_ptr()
-        p.scratch, p.scratch_bytes = scratch.ptr, scratch.nbytes
+        p.scratch, p.scratch_bytes, p.slots_fp32 = scratch.ptr, scratch.nbytes, int(slots_fp32)
         self.out, self.device = out, dev
         self._keep = (q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, add)
         self.scratch = scratch
@@ -1159,12 +1159,13 @@ class PreparedDown(_Prepared):
 
 
 def moe_down(q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, expert_ids, block: int, add=None,
-             out=None, scratch: ExpertScratch | None = None, stream=None):
+             out=None, scratch: ExpertScratch | None = None, stream=None, slots_fp32: bool = False):
     """Stage 2 of the routed experts and the combination (mr_moe_down): bf16
     [M, R] = add + sum over a token's slots of topk_weights times its row of
     act @ w2^T.  q, scale: act's codes and scales at the sorted positions, as
     moe_gate_up(..., quant=...) returns them.  Slots whose id is outside
-    [0, E) add nothing."""
+    [0, E) add nothing.  A slot's row is rounded to bf16 before it is weighted
+    and added, unless slots_fp32 (twice the scratch and its traffic)."""
     return _call_once(_one_device(q=q), stream,
                       lambda: PreparedDown(q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, block, add,
-                                           out, scratch, _once=True))
+                                           out, scratch, slots_fp32, _once=True))

@@ -63,7 +63,7 @@ cudaError_t launch_mx_pack(const uint8_t* scale, int64_t E, int R, int K, int fp
 
 // out[m, r] = bf16(add[m, r] + sum_j weights[m, j] y[m * topk + j, r]), j
 // ascending in fp32; slots whose id is outside [0, E) are skipped, whatever y
-// holds there.  A thread takes eight columns of a row (VEC; else one): eight
+// holds there.  A thread takes 16 bytes of y's row (VEC; else one column): eight
 // slots' rows are in flight at a time.  Bound by reading y: 4096 tokens x 8 x
 // 6144 is 403 MB, 72 us (78 % of the peak bandwidth).  Launched so that its
 // CTAs are in place when the products end (the wait is for all of them, and
@@ -83,22 +83,23 @@ constexpr int kCombineThreads = 64;
 __device__ __forceinline__ void discard_line(const void* line) {
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
 }
-template <bool VEC>
-__global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(__nv_bfloat16* y, const int32_t* ids,
+template <bool VEC, class Y>
+__global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(Y* y, const int32_t* ids,
                                                              const float* weights, const __nv_bfloat16* add,
                                                              __nv_bfloat16* out, int64_t M, int topk, int R, int E) {
-    constexpr int N = VEC ? 8 : 1;
-    const bool lines = R % 64 == 0;  // y's rows are whole lines of 128 bytes
+    constexpr bool F32 = sizeof(Y) == 4;
+    constexpr int N = VEC ? 16 / (int)sizeof(Y) : 1;
+    const bool lines = R % (128 / (int)sizeof(Y)) == 0;  // y's rows are whole lines of 128 bytes
     pdl_wait();
     const int per = R / N;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < M * per; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t m = i / per;
         const int r = (int)(i - m * per) * N;
         float s[N];
-        auto wide = [](uint4 q, float* f) {
+        auto wide = [](uint4 q, float* f) {  // bf16, N of them
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < N / 2; ++u) {
                 f[2 * u] = __uint_as_float(w[u] << 16);
                 f[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u);
             }
@@ -106,6 +107,9 @@ __global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(__nv_bf
         if (add == nullptr) {
 #pragma unroll
             for (int u = 0; u < N; ++u) s[u] = 0.0f;
+        } else if (VEC && F32) {
+            const uint2 q = *reinterpret_cast<const uint2*>(add + m * R + r);
+            wide(make_uint4(q.x, q.y, 0u, 0u), s);
         } else if (VEC) {
             wide(*reinterpret_cast<const uint4*>(add + m * R + r), s);
         } else {
@@ -120,18 +124,25 @@ __global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(__nv_bf
                 id[u] = -1;
                 if (j0 + u >= topk) continue;
                 const int64_t f = m * topk + j0 + u;
-                const __nv_bfloat16* p = y + f * R + r;
+                const Y* p = y + f * R + r;
                 id[u] = __ldg(ids + f);
                 w[u] = __ldg(weights + f);
                 if (VEC) v[u] = __ldcg(reinterpret_cast<const uint4*>(p));
+                else if (F32) v[u].x = *reinterpret_cast<const uint32_t*>(p);
                 else v[u].x = (uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16;
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 if ((unsigned)id[u] >= (unsigned)E) continue;
                 float f[8];
-                if (VEC) wide(v[u], f);
-                else f[0] = __uint_as_float(v[u].x);
+                if (VEC && !F32) {
+                    wide(v[u], f);
+                } else {
+                    f[0] = __uint_as_float(v[u].x);
+                    f[1] = __uint_as_float(v[u].y);
+                    f[2] = __uint_as_float(v[u].z);
+                    f[3] = __uint_as_float(v[u].w);
+                }
 #pragma unroll
                 for (int q = 0; q < N; ++q) s[q] = __fmaf_rn(w[u], f[q], s[q]);
             }
@@ -145,9 +156,14 @@ __global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(__nv_bf
                 }
             }
         }
-        if (VEC) {
+        if (VEC && F32) {
+            uint2 q;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.x) : "f"(s[1 % N]), "f"(s[0]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.y) : "f"(s[3 % N]), "f"(s[2 % N]));
+            *reinterpret_cast<uint2*>(out + m * R + r) = q;
+        } else if (VEC) {
             uint4 q;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.x) : "f"(s[1]), "f"(s[0]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.x) : "f"(s[1 % N]), "f"(s[0]));
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.y) : "f"(s[3 % N]), "f"(s[2 % N]));
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.z) : "f"(s[5 % N]), "f"(s[4 % N]));
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.w) : "f"(s[7 % N]), "f"(s[6 % N]));
@@ -158,11 +174,12 @@ __global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(__nv_bf
     }
 }
 
-cudaError_t launch_combine(const ExpertCall& c, __nv_bfloat16* y, int sms, cudaStream_t st) {
+template <class Y>
+cudaError_t launch_combine(const ExpertCall& c, Y* y, int sms, cudaStream_t st) {
     const auto* add = static_cast<const __nv_bfloat16*>(c.add);
     auto* out = static_cast<__nv_bfloat16*>(c.out);
     const bool vec = c.R % 8 == 0 && (reinterpret_cast<uintptr_t>(add) | reinterpret_cast<uintptr_t>(out)) % 16 == 0;
-    const int64_t work = (int64_t)c.M * (c.R / (vec ? 8 : 1));
+    const int64_t work = (int64_t)c.M * (c.R / (vec ? 16 / (int)sizeof(Y) : 1));
     int64_t ctas = (work + kCombineThreads - 1) / kCombineThreads;
     if (ctas > (int64_t)sms * 32) ctas = (int64_t)sms * 32;
     cudaLaunchConfig_t cfg = {};
@@ -175,7 +192,7 @@ cudaError_t launch_combine(const ExpertCall& c, __nv_bfloat16* y, int sms, cudaS
     cfg.attrs = at;
     cfg.numAttrs = 1;
     const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, vec ? expert_combine_kernel<true> : expert_combine_kernel<false>, y, c.topk_ids,
+        cudaLaunchKernelEx(&cfg, vec ? expert_combine_kernel<true, Y> : expert_combine_kernel<false, Y>, y, c.topk_ids,
                            c.topk_weights, add, out, (int64_t)c.M, c.topk, c.R, c.E);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -308,7 +325,9 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     cudaError_t e = c.op == kExGemm     ? launch_op<kExGemm>(a, fp4, pair, grid, st)
                     : c.op == kExGateUp ? launch_op<kExGateUp>(a, fp4, pair, grid, st)
                                         : launch_op<kExDown>(a, fp4, pair, grid, st);
-    if (e == cudaSuccess && c.op == kExDown) e = launch_combine(c, static_cast<__nv_bfloat16*>(a.out), sms, st);
+    if (e == cudaSuccess && c.op == kExDown)
+        e = c.out_fmt == 3 ? launch_combine(c, static_cast<float*>(a.out), sms, st)
+                           : launch_combine(c, static_cast<__nv_bfloat16*>(a.out), sms, st);
     *err = e;
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }
