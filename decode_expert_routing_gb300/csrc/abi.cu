@@ -638,7 +638,7 @@ int mr_mx_pack_scales(const uint8_t* scale, int E, int R, int K, int format, int
 size_t mr_expert_scratch_bytes(int M_max, int topk, int R) {
     if (M_max < 1 || topk < 1 || topk > MR_MAX_TOPK || R < 1) return 0;
     const int64_t mk = (int64_t)M_max * topk;
-    return mk < ((int64_t)1 << 30) ? mr::expert_scratch_bytes(mk, R, false) : 0;
+    return mk < ((int64_t)1 << 30) ? mr::expert_scratch_bytes(mk, R) : 0;
 }
 
 int mr_mx_gemm(const mr_mx_gemm_params* p, void* stream) {
@@ -727,12 +727,12 @@ int mr_moe_down(const mr_moe_down_params* p, void* stream) {
         !aligned(p->topk_weights, 4) || p->out == nullptr || !aligned(p->out, 2) || (p->add && !aligned(p->add, 2)))
         return MR_ERR_INVALID_ARG;
     const int64_t mk = (int64_t)p->M * p->topk;
-    const size_t need = mr::expert_scratch_bytes(mk, p->R, p->slots_fp32 != 0);
+    const size_t need = mr::expert_scratch_bytes(mk, p->R);
     if ((s = check_expert_scratch(p->scratch, p->scratch_bytes, need)) != MR_OK) return s;
+    if (p->scratch_low && (s = check_expert_scratch(p->scratch_low, p->scratch_low_bytes, need)) != MR_OK) return s;
     mr::ExpertCall c{};
     c.op = 2;
     c.fp4 = p->format == MR_QUANT_MXFP4;
-    c.out_fmt = p->slots_fp32 ? 3 : 0;
     c.E = p->E;
     c.R = p->R;
     c.K = p->I;
@@ -754,6 +754,7 @@ int mr_moe_down(const mr_moe_down_params* p, void* stream) {
     c.add = p->add;
     c.out = p->out;
     c.scratch = p->scratch;
+    c.scratch_low = p->scratch_low;
     return run_expert(c, stream);
 }
 

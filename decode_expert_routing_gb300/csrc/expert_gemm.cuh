@@ -85,7 +85,8 @@ struct ExpertArgs {
     int64_t lds;
     const int32_t* sorted;   // [cap] assignment of a sorted position
     const int32_t* experts;  // [nblk] expert of a block
-    void* out;               // bf16 (or fp32) rows, or E4M3 / E2M1 codes; kExDown: [assignments][R], bf16 or fp32
+    void* out;               // bf16 (or fp32) rows, or E4M3 / E2M1 codes; kExDown: bf16 [assignments][R]
+    uint16_t* out_low;       // kExDown: null, or the lower halves of the fp32 products, out then the upper ones
     uint8_t* out_scale;
     int64_t ldo;             // elements between output rows (kExGemm)
     const uint8_t* x;        // activation codes (rows in token order)
@@ -892,7 +893,8 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                             if (j < cols) *p = __float2bfloat16_rn(__uint_as_float(v[j]));
                     }
                 } else if (OP == kExDown) {
-                    auto put = [&](auto* y, auto value) {
+                    uint16_t* y = static_cast<uint16_t*>(a.out) + r;
+                    auto rows = [&](auto put) {
 #pragma unroll
                         for (int j4 = 0; j4 < 4; ++j4) {
                             const int4 as = *reinterpret_cast<const int4*>(f + c0 + 4 * j4);
@@ -900,11 +902,17 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 if ((unsigned)s4[j] < (unsigned)a.mk && r < a.R)
-                                    y[(int64_t)s4[j] * a.R] = value(__uint_as_float(v[4 * j4 + j]));
+                                    put((int64_t)s4[j] * a.R, v[4 * j4 + j]);
                         }
                     };
-                    if (a.out_fmt == 3) put(static_cast<float*>(a.out) + r, [](float x) { return x; });
-                    else put(static_cast<__nv_bfloat16*>(a.out) + r, [](float x) { return __float2bfloat16_rn(x); });
+                    if (a.out_low != nullptr) {
+                        uint16_t* low = a.out_low + r;
+                        rows([&](int64_t at, uint32_t bits) { y[at] = (uint16_t)(bits >> 16), low[at] = (uint16_t)bits; });
+                    } else {
+                        rows([&](int64_t at, uint32_t bits) {
+                            y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(bits)));
+                        });
+                    }
                 } else {
                     // lanes 0-15 hold gate rows and lanes 16-31 the up rows of
                     // the same features: lanes 0-15 take the even columns,

@@ -20,15 +20,13 @@ inline ExpertShape expert_shape(int R, int K, bool fp4, bool gate_up) {
     return s;
 }
 
-// Scratch of a down call: its products of mk assignments, rows of R.  Unless
-// the caller asks for fp32 they are rounded to bf16 (half a step, 2^-8 of each):
-// written and read once, they are the call's largest traffic next to the
-// weights.  128 experts x 6144 x 768, E4M3, top-8, bf16 and fp32: 1 token 12.6
-// and 13.0 us, 64 tokens 81.5 and 83.0, 256 100 and 105, 1001 127 and 167, 4096
-// 263 and 422.
-inline size_t expert_scratch_bytes(int64_t mk, int R, bool fp32) {
-    return ((size_t)mk * (size_t)R * (fp32 ? 4 : 2) + 255) / 256 * 256;
-}
+// Scratch of a down call: its products of mk assignments, rows of R, rounded to
+// bf16 (half a step, 2^-8 of each), or the upper halves of the fp32 products,
+// whose lower halves have a buffer as large.  Written and read once, they are
+// the call's largest traffic next to the weights.  128 experts x 6144 x 768,
+// E4M3, top-8, rounded and whole: 1 token 12.6 and 12.9 us, 64 tokens 82.1 and
+// 83.7, 256 101 and 105, 1001 127 and 164, 4096 260 and 417.
+inline size_t expert_scratch_bytes(int64_t mk, int R) { return ((size_t)mk * (size_t)R * 2 + 255) / 256 * 256; }
 
 // Whether two CTAs share their activation rows (256 weight rows a tile): where
 // an expert has 16 rows or more on average, and there are 64 in all.  Gate/up
@@ -83,7 +81,7 @@ inline int expert_gemm_rows(int M, int RT, bool pair, int slices, int ctas) {
 
 // One launch of the expert kernel (op: 0 gemm, 1 gate/up, 2 down).
 struct ExpertCall {
-    int op, fp4, gather, out_fmt;  // out_fmt: 0 bf16, 1 MXFP8, 2 MXFP4, 3 fp32 (down: of the products)
+    int op, fp4, gather, out_fmt;  // out_fmt: 0 bf16, 1 MXFP8, 2 MXFP4, 3 fp32
     int E, R, K, M, topk, nblk, block;
     const uint8_t *w, *w_scale, *x, *x_scale;
     int64_t ldx, lds, ldo, x_rows;
@@ -92,7 +90,7 @@ struct ExpertCall {
     const void* add;
     void* out;
     uint8_t* out_scale;
-    void* scratch;
+    void *scratch, *scratch_low;
 };
 int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err);
 cudaError_t launch_mx_pack(const uint8_t* scale, int64_t E, int R, int K, int fp4, int gate_up, void* packed,

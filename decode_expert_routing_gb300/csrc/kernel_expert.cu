@@ -63,8 +63,9 @@ cudaError_t launch_mx_pack(const uint8_t* scale, int64_t E, int R, int K, int fp
 
 // out[m, r] = bf16(add[m, r] + sum_j weights[m, j] y[m * topk + j, r]), j
 // ascending in fp32; slots whose id is outside [0, E) are skipped, whatever y
-// holds there.  A thread takes 16 bytes of y's row (VEC; else one column): eight
-// slots' rows are in flight at a time.  Bound by reading y: 4096 tokens x 8 x
+// holds there.  LOW: y and low are the halves of fp32 numbers.  A thread takes
+// eight columns of a row (VEC; else one): eight slots' rows are in flight at a
+// time.  Bound by reading y: 4096 tokens x 8 x
 // 6144 is 403 MB, 72 us (78 % of the peak bandwidth).  Launched so that its
 // CTAs are in place when the products end (the wait is for all of them, and
 // for the memory they wrote): CTAs of 64 threads find room for their registers
@@ -83,66 +84,58 @@ constexpr int kCombineThreads = 64;
 __device__ __forceinline__ void discard_line(const void* line) {
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
 }
-template <bool VEC, class Y>
-__global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(Y* y, const int32_t* ids,
-                                                             const float* weights, const __nv_bfloat16* add,
-                                                             __nv_bfloat16* out, int64_t M, int topk, int R, int E) {
-    constexpr bool F32 = sizeof(Y) == 4;
-    constexpr int N = VEC ? 16 / (int)sizeof(Y) : 1;
-    const bool lines = R % (128 / (int)sizeof(Y)) == 0;  // y's rows are whole lines of 128 bytes
+template <bool VEC, bool LOW>
+__global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(const uint16_t* y, const uint16_t* low,
+                                                             const int32_t* ids, const float* weights,
+                                                             const __nv_bfloat16* add, __nv_bfloat16* out, int64_t M,
+                                                             int topk, int R, int E) {
+    constexpr int N = VEC ? 8 : 1;
+    const bool lines = R % 64 == 0;  // y's rows are whole lines of 128 bytes
     pdl_wait();
     const int per = R / N;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < M * per; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t m = i / per;
         const int r = (int)(i - m * per) * N;
         float s[N];
-        auto wide = [](uint4 q, float* f) {  // bf16, N of them
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        auto wide = [](uint4 q, uint4 l, float* f) {  // upper and lower halves of eight numbers
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w}, k[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-            for (int u = 0; u < N / 2; ++u) {
-                f[2 * u] = __uint_as_float(w[u] << 16);
-                f[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u);
+            for (int u = 0; u < 4; ++u) {
+                f[2 * u] = __uint_as_float((w[u] << 16) | (k[u] & 0xFFFFu));
+                f[2 * u + 1] = __uint_as_float((w[u] & 0xFFFF0000u) | (k[u] >> 16));
             }
         };
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
         if (add == nullptr) {
 #pragma unroll
             for (int u = 0; u < N; ++u) s[u] = 0.0f;
-        } else if (VEC && F32) {
-            const uint2 q = *reinterpret_cast<const uint2*>(add + m * R + r);
-            wide(make_uint4(q.x, q.y, 0u, 0u), s);
         } else if (VEC) {
-            wide(*reinterpret_cast<const uint4*>(add + m * R + r), s);
+            wide(*reinterpret_cast<const uint4*>(add + m * R + r), none, s);
         } else {
             s[0] = __bfloat162float(add[m * R + r]);
         }
         for (int j0 = 0; j0 < topk; j0 += 8) {
-            uint4 v[8];
+            uint4 v[8], l[8];
             int id[8];
             float w[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 id[u] = -1;
                 if (j0 + u >= topk) continue;
-                const int64_t f = m * topk + j0 + u;
-                const Y* p = y + f * R + r;
+                const int64_t f = m * topk + j0 + u, at = f * R + r;
                 id[u] = __ldg(ids + f);
                 w[u] = __ldg(weights + f);
-                if (VEC) v[u] = __ldcg(reinterpret_cast<const uint4*>(p));
-                else if (F32) v[u].x = *reinterpret_cast<const uint32_t*>(p);
-                else v[u].x = (uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16;
+                if (VEC) v[u] = __ldcg(reinterpret_cast<const uint4*>(y + at));
+                else v[u].x = (uint32_t)y[at] << 16;
+                if (VEC && LOW) l[u] = __ldcg(reinterpret_cast<const uint4*>(low + at));
+                else if (LOW) v[u].x |= low[at];
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 if ((unsigned)id[u] >= (unsigned)E) continue;
                 float f[8];
-                if (VEC && !F32) {
-                    wide(v[u], f);
-                } else {
-                    f[0] = __uint_as_float(v[u].x);
-                    f[1] = __uint_as_float(v[u].y);
-                    f[2] = __uint_as_float(v[u].z);
-                    f[3] = __uint_as_float(v[u].w);
-                }
+                if (VEC) wide(v[u], LOW ? l[u] : none, f);
+                else f[0] = __uint_as_float(v[u].x);
 #pragma unroll
                 for (int q = 0; q < N; ++q) s[q] = __fmaf_rn(w[u], f[q], s[q]);
             }
@@ -151,19 +144,17 @@ __global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(Y* y, c
                 __syncwarp(0xFFu << (threadIdx.x & 24u));
                 if ((threadIdx.x & 7) == 0) {
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        if (j0 + u < topk) discard_line(y + (m * topk + j0 + u) * R + r);
+                    for (int u = 0; u < 8; ++u) {
+                        if (j0 + u >= topk) continue;
+                        discard_line(y + (m * topk + j0 + u) * R + r);
+                        if (LOW) discard_line(low + (m * topk + j0 + u) * R + r);
+                    }
                 }
             }
         }
-        if (VEC && F32) {
-            uint2 q;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.x) : "f"(s[1 % N]), "f"(s[0]));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.y) : "f"(s[3 % N]), "f"(s[2 % N]));
-            *reinterpret_cast<uint2*>(out + m * R + r) = q;
-        } else if (VEC) {
+        if (VEC) {
             uint4 q;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.x) : "f"(s[1 % N]), "f"(s[0]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.x) : "f"(s[1]), "f"(s[0]));
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.y) : "f"(s[3 % N]), "f"(s[2 % N]));
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.z) : "f"(s[5 % N]), "f"(s[4 % N]));
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q.w) : "f"(s[7 % N]), "f"(s[6 % N]));
@@ -174,12 +165,12 @@ __global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(Y* y, c
     }
 }
 
-template <class Y>
-cudaError_t launch_combine(const ExpertCall& c, Y* y, int sms, cudaStream_t st) {
+template <bool LOW>
+cudaError_t launch_combine(const ExpertCall& c, int sms, cudaStream_t st) {
     const auto* add = static_cast<const __nv_bfloat16*>(c.add);
     auto* out = static_cast<__nv_bfloat16*>(c.out);
     const bool vec = c.R % 8 == 0 && (reinterpret_cast<uintptr_t>(add) | reinterpret_cast<uintptr_t>(out)) % 16 == 0;
-    const int64_t work = (int64_t)c.M * (c.R / (vec ? 16 / (int)sizeof(Y) : 1));
+    const int64_t work = (int64_t)c.M * (c.R / (vec ? 8 : 1));
     int64_t ctas = (work + kCombineThreads - 1) / kCombineThreads;
     if (ctas > (int64_t)sms * 32) ctas = (int64_t)sms * 32;
     cudaLaunchConfig_t cfg = {};
@@ -192,8 +183,9 @@ cudaError_t launch_combine(const ExpertCall& c, Y* y, int sms, cudaStream_t st) 
     cfg.attrs = at;
     cfg.numAttrs = 1;
     const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, vec ? expert_combine_kernel<true, Y> : expert_combine_kernel<false, Y>, y, c.topk_ids,
-                           c.topk_weights, add, out, (int64_t)c.M, c.topk, c.R, c.E);
+        cudaLaunchKernelEx(&cfg, vec ? expert_combine_kernel<true, LOW> : expert_combine_kernel<false, LOW>,
+                           static_cast<const uint16_t*>(c.scratch), static_cast<const uint16_t*>(c.scratch_low),
+                           c.topk_ids, c.topk_weights, add, out, (int64_t)c.M, c.topk, c.R, c.E);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -317,7 +309,7 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
     a.x = c.x;
     a.ldx = c.ldx;
     a.kbytes = (int)kbytes;
-    if (c.op == kExDown) a.out = c.scratch;
+    if (c.op == kExDown) a.out = c.scratch, a.out_low = static_cast<uint16_t*>(c.scratch_low);
     const int grid = sms;
     a.slices = expert_slices(a.mk, c.E, s, sms, &a.slice_len);
     const bool pair = a.slices == 1 && expert_pair(a.mk, c.E);
@@ -326,8 +318,7 @@ int launch_expert(const ExpertCall& c, cudaStream_t st, cudaError_t* err) {
                     : c.op == kExGateUp ? launch_op<kExGateUp>(a, fp4, pair, grid, st)
                                         : launch_op<kExDown>(a, fp4, pair, grid, st);
     if (e == cudaSuccess && c.op == kExDown)
-        e = c.out_fmt == 3 ? launch_combine(c, static_cast<float*>(a.out), sms, st)
-                           : launch_combine(c, static_cast<__nv_bfloat16*>(a.out), sms, st);
+        e = c.scratch_low ? launch_combine<true>(c, sms, st) : launch_combine<false>(c, sms, st);
     *err = e;
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }

@@ -533,8 +533,8 @@ int mr_mx_pack_scales(const uint8_t *scale, int E, int R, int K, int format, int
 
 /*
  * Scratch bytes of mr_moe_down for up to M_max tokens of topk slots and R
- * output columns: the products of every slot on their way to the sum, in bf16
- * (for slots_fp32 ask for 2 * R columns).  The
+ * output columns: the products of every slot on their way to the sum (their
+ * upper halves; the optional buffer of the lower ones is as large).  The
  * buffer need not be zeroed and holds nothing between calls; calls that may
  * run concurrently (captured graphs among them) must not share it.  Returns 0
  * for out-of-range arguments.  Pure host function.
@@ -607,14 +607,15 @@ int mr_moe_gate_up(const mr_moe_gate_up_params *params, void *stream);
  * the sum over j ascending in fp32, so the result does not depend on the
  * order in which experts finish.  y's rounding adds up to 2^-8 * sum_j
  * |topk_weights[m, j] y[m * topk + j, r]| to a result's error, also where slots
- * (or add) cancel.  With slots_fp32 != 0 y is not rounded: the scratch and its
- * traffic are twice as large, the result has one rounding to bf16.  q, scale: the rows of act at their sorted
+ * (or add) cancel.  With scratch_low, a second buffer like scratch, y is not
+ * rounded: scratch holds the upper halves of the fp32 products and scratch_low
+ * the lower ones, and the result has one rounding to bf16.  q, scale: the rows of act at their sorted
  * positions (strides as mr_mx_gemm; padding rows are read but change
  * nothing); w2: [E, R, I].  Slots whose id in topk_ids is outside [0, E) add
  * nothing; a token without any gives add, or zero.  topk_ids, topk_weights:
  * [M, topk]; add: bf16 [M, R] or NULL; out: bf16 [M, R], may be add itself.
- * scratch: mr_expert_scratch_bytes(M, topk, R), with slots_fp32 of 2 * R,
- * 256-byte aligned.  Two launches.
+ * scratch: mr_expert_scratch_bytes(M, topk, R), 256-byte aligned;
+ * scratch_low: NULL, or as scratch.  Two launches.
  */
 typedef struct mr_moe_down_params {
     const uint8_t *q;
@@ -633,7 +634,8 @@ typedef struct mr_moe_down_params {
     void *out;
     void *scratch;
     size_t scratch_bytes;
-    int slots_fp32;
+    void *scratch_low;
+    size_t scratch_low_bytes;
 } mr_moe_down_params;
 int mr_moe_down(const mr_moe_down_params *params, void *stream);
 

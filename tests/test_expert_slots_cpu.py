@@ -1,5 +1,5 @@
 """The expert products' parameter blocks in C and in the binding, and the
-scratch of down's unrounded slots (no GPU)."""
+second scratch buffer of down (no GPU)."""
 
 import ctypes
 import subprocess
@@ -34,11 +34,8 @@ def test_parameter_blocks_match_the_header(tmp_path, name, cls):
 
 
 def test_scratch_of_unrounded_slots(lib):
-    """Twice the bytes: those of twice the columns."""
-    f = lib.mr_expert_scratch_bytes
-    need = f(DOWN["M"], DOWN["topk"], 2 * DOWN["R"])
-    assert need >= DOWN["M"] * DOWN["topk"] * DOWN["R"] * 4
-    short = dict(slots_fp32=1, scratch_bytes=need - 1)
-    assert call(lib, "down", short) == mr.MR_ERR_SCRATCH_TOO_SMALL
-    assert call(lib, "down", dict(slots_fp32=1, scratch_bytes=f(DOWN["M"], DOWN["topk"], DOWN["R"]))) \
-        == mr.MR_ERR_SCRATCH_TOO_SMALL
+    """The buffer of the lower halves is checked as the other one."""
+    need = lib.mr_expert_scratch_bytes(DOWN["M"], DOWN["topk"], DOWN["R"])
+    low = DOWN["scratch"]
+    assert call(lib, "down", dict(scratch_low=low, scratch_low_bytes=need - 1)) == mr.MR_ERR_SCRATCH_TOO_SMALL
+    assert call(lib, "down", dict(scratch_low=low + 16, scratch_low_bytes=need)) == mr.MR_ERR_INVALID_ARG

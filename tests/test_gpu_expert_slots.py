@@ -63,9 +63,11 @@ def test_unrounded_slots(mr, fmt, M, E, topk, R, I, block, invalid, skew):
         out = mr.moe_down(*a, W, ids, wts, st, ex, block, add=extra, scratch=scratch, slots_fp32=True)
         ref.assert_close(out, want, tol + HALF * (want.abs() + tol), "unrounded")
         assert torch.equal(out, mr.moe_down(*a, W, ids, wts, st, ex, block, add=extra, slots_fp32=True))
+        # what a call of this size does by itself
+        assert torch.equal(out, mr.moe_down(*a, W, ids, wts, st, ex, block, add=extra))
         # the rounded form: 2^-8 of every slot more
         tol = tol + HALF * (mag + tol)
-        out2 = mr.moe_down(*a, W, ids, wts, st, ex, block, add=extra, scratch=scratch)
+        out2 = mr.moe_down(*a, W, ids, wts, st, ex, block, add=extra, scratch=scratch, slots_fp32=False)
         ref.assert_close(out2, want, tol + HALF * (want.abs() + tol), "rounded")
     inplace = add.clone()
     mr.moe_down(*a, W, ids, wts, st, ex, block, add=inplace, out=inplace, scratch=scratch, slots_fp32=True)
@@ -104,7 +106,7 @@ def test_slots_that_cancel(mr, fmt):
     out = mr.moe_down(a, a_scale, W, ids, wts, st, ex, block, slots_fp32=True)
     # every sum here is of at most 64 terms in units of 2^-12 below 2^8: exact in fp32
     assert torch.equal(out, want.to(BF16))
-    rounded = mr.moe_down(a, a_scale, W, ids, wts, st, ex, block)
+    rounded = mr.moe_down(a, a_scale, W, ids, wts, st, ex, block, slots_fp32=False)
     ref.assert_close(rounded, want, HALF * mag + HALF * (want.abs() + HALF * mag))
     assert not torch.equal(rounded, out)
     # add takes the first slot away
@@ -123,19 +125,41 @@ def test_unrounded_slots_touch_their_own_scratch_only(mr):
         a, W = ref.random_mx((st.numel(), I), "mxfp4", 1), mr.MxWeight(*ref.random_mx((E, R, I), "mxfp4", 2), "mxfp4")
         want = mr.moe_down(*a, W, ids, wts, st, ex, block, slots_fp32=True)
         scratch = mr.ExpertScratch(2 * M, topk, R, slots_fp32=True)
-        rest = scratch.tensor[M * topk * R * 4:]
+        rest = [t[M * topk * R * 2:] for t in (scratch.tensor, scratch.low)]
         call = mr.PreparedDown(*a, W, ids, wts, st, ex, block, scratch=scratch, slots_fp32=True)
         for i in range(10):
-            rest.fill_(i)
+            for t in rest:
+                t.fill_(i)
             assert torch.equal(call(), want)
-            assert (rest == i).all()
+            assert all((t == i).all() for t in rest)
 
 
-def test_a_scratch_of_rounded_slots_is_refused(mr):
+def test_scratch_of_either_kind(mr, monkeypatch):
+    """A scratch without the lower halves' room, or with room for a few, is refused where it is needed; calls past the
+    limit round unless they are told not to."""
     M, E, topk, R, I, block = 19, 8, 3, 128, 64, 16
     ids, wts = routed(M, E, topk, 3)
     st, ex, _ = mr.moe_sort(ids, E, block)
     a, W = ref.random_mx((st.numel(), I), "mxfp8", 1), mr.MxWeight(*ref.random_mx((E, R, I), "mxfp8", 2))
+
+    def run(**kw):
+        return mr.moe_down(*a, W, ids, wts, st, ex, block, **kw)
+
+    whole, rounded = run(slots_fp32=True), run(slots_fp32=False)
+    assert not torch.equal(whole, rounded)
+    plain = mr.ExpertScratch(M, topk, R, slots_fp32=False)
+    assert plain.low is None and torch.equal(run(scratch=plain, slots_fp32=False), rounded)
+    for kw in (dict(), dict(slots_fp32=True)):
+        with pytest.raises(ValueError):
+            run(scratch=plain, **kw)
+    assert torch.equal(run(scratch=mr.ExpertScratch(M, topk, R)), whole)
+    monkeypatch.setattr(mr, "SLOTS_FP32_MAX", M * topk * R - 1)
+    assert torch.equal(run(), rounded) and torch.equal(run(scratch=mr.ExpertScratch(M, topk, R)), rounded)
+    assert torch.equal(run(slots_fp32=True), whole)
     with pytest.raises(mr.MoeRouteError) as e:
-        mr.moe_down(*a, W, ids, wts, st, ex, block, scratch=mr.ExpertScratch(M, topk, R), slots_fp32=True)
+        run(scratch=mr.ExpertScratch(M, topk, R), slots_fp32=True)
     assert e.value.status == mr.MR_ERR_SCRATCH_TOO_SMALL
+    # a scratch for more tokens than the limit serves the few that are kept whole
+    monkeypatch.setattr(mr, "SLOTS_FP32_MAX", M * topk * R)
+    big = mr.ExpertScratch(4 * M, topk, R)
+    assert big.low_nbytes == 2 * M * topk * R and torch.equal(run(scratch=big), whole)
