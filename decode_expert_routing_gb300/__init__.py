@@ -686,7 +686,7 @@ class _Prepared:
     scratch that an expert product's object makes itself are memory of the
     stream that is current then, and may be used on any."""
 
-    _home, _made, _weights, _ready, _captured, _streams = None, (), (), None, False, None
+    _home, _made, _weights, _ready, _streams = None, (), (), None, None
 
     def _own(self, made, weights, once):
         """made: the buffers that the object made itself, on the stream that
@@ -701,19 +701,28 @@ class _Prepared:
         self._made, self._weights, self._streams = [t for t in made if t is not None], weights, set()
         if self._made and not once:
             with _launch_ctx(self.device):
-                self._captured = torch.cuda.is_current_stream_capturing()
-                self._ready = torch.cuda.Event()
-                self._ready.record()
+                if torch.cuda.is_current_stream_capturing():
+                    self._ready = torch.cuda.current_stream()  # (an event of this capture is of no use to others)
+                else:
+                    self._ready = torch.cuda.Event()
+                    self._ready.record()
 
     def _first_on(self, sp):
         """The object's first call on the stream sp."""
         torch = _torch()
         if sp != self._home and self._made:
             own = _torch_stream(self.device, sp)
-            with torch.cuda.stream(own):
-                # (a capture takes no event from outside; what was queued before it has run when the graph does)
-                if self._ready is not None and torch.cuda.is_current_stream_capturing() == self._captured:
+
+            def capturing(stream):
+                with torch.cuda.stream(stream):
+                    return torch.cuda.is_current_stream_capturing()
+
+            # (a capture takes no event from outside; what was queued before it has run when the graph does)
+            if isinstance(self._ready, torch.cuda.Event):
+                if not capturing(own):
                     own.wait_event(self._ready)
+            elif self._ready is not None and capturing(self._ready) and capturing(own):
+                own.wait_stream(self._ready)
             for t in self._made:
                 t.record_stream(own)
         for w in self._weights:

@@ -247,11 +247,23 @@ def test_made_and_called_inside_a_capture(mr):
         a(side)
         c = down(mr, s, stream=side)
         main.wait_stream(side)
-    for _ in range(3):
-        g.replay()
+    # the same objects in another capture, on a third stream, and outside
+    third = torch.cuda.Stream()
+    g2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g2, stream=main):
+        third.wait_stream(main)
+        a(third)
+        b(third)
+        main.wait_stream(third)
+    for graph in (g, g2, g):
+        a.out.zero_()
+        graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(a.out, want[0]) and torch.equal(c, want[0]) and int(sums) == 3 * (4 << 20)
         assert all(torch.equal(o[rows], w[rows]) for o, w in zip(b.out, want[1]))
+    a.out.zero_()
+    a()
+    assert torch.equal(a.out, want[0])
 
 
 def test_streams_of_other_kinds(mr):
