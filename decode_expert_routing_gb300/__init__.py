@@ -960,8 +960,9 @@ class ExpertScratch:
     """A caller-owned scratch buffer of moe_down for up to M_max tokens of
     topk slots and R output columns: torch uint8 tensors whose contents do not
     matter between calls, tensor for the slots' rows (bf16, or the upper halves
-    of fp32) and low for the lower halves.  slots_fp32 as moe_down's: None is
-    for calls that leave it to the size, or give it as False."""
+    of fp32) and low for the lower halves.  slots_fp32: True for calls of any
+    size with slots_fp32; False for none (no low); None for those whose size
+    has them so."""
 
     def __init__(self, M_max: int, topk: int, R: int, device=None, slots_fp32: bool | None = None):
         torch = _torch()
@@ -1164,7 +1165,7 @@ class PreparedDown(_Prepared):
             made.append(out)
         _check_out(out, "out", (M, w2.R), torch.bfloat16, dev)
         if slots_fp32 is None:
-            slots_fp32 = M * topk * w2.R <= SLOTS_FP32_MAX
+            slots_fp32 = M * topk * w2.R <= SLOTS_FP32_MAX and (scratch is None or scratch.low is not None)
         if scratch is None:
             scratch = ExpertScratch(M, topk, w2.R, device=dev, slots_fp32=slots_fp32)
             made += [scratch.tensor, scratch.low]
@@ -1198,7 +1199,7 @@ def moe_down(q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, e
     [0, E) add nothing.  slots_fp32: True keeps the slots' rows in fp32 on
     their way to the sum; False rounds them to bf16, which adds up to 2^-8 of
     every weighted row to a result's error; None: in fp32 while M * topk * R is
-    at most SLOTS_FP32_MAX."""
+    at most SLOTS_FP32_MAX and a given scratch has room for it."""
     return _call_once(_one_device(q=q), stream,
                       lambda: PreparedDown(q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, block, add,
                                            out, scratch, slots_fp32, _once=True))

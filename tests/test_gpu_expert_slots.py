@@ -149,9 +149,9 @@ def test_scratch_of_either_kind(mr, monkeypatch):
     assert not torch.equal(whole, rounded)
     plain = mr.ExpertScratch(M, topk, R, slots_fp32=False)
     assert plain.low is None and torch.equal(run(scratch=plain, slots_fp32=False), rounded)
-    for kw in (dict(), dict(slots_fp32=True)):
-        with pytest.raises(ValueError):
-            run(scratch=plain, **kw)
+    assert torch.equal(run(scratch=plain), rounded)
+    with pytest.raises(ValueError):
+        run(scratch=plain, slots_fp32=True)
     assert torch.equal(run(scratch=mr.ExpertScratch(M, topk, R)), whole)
     monkeypatch.setattr(mr, "SLOTS_FP32_MAX", M * topk * R - 1)
     assert torch.equal(run(), rounded) and torch.equal(run(scratch=mr.ExpertScratch(M, topk, R)), rounded)
