@@ -22,11 +22,12 @@
 //
 // What bounds it (one GB300, weights of 128 experts, K = 6144, I = 768): few
 // rows, reading the weights of the experts hit: gate/up of 16 tokens x 8, E2M1,
-// 54.6 us, 6.4 TB/s.  One token's 77 MB take 16.5 us, of which some 5 are the
-// launch, the tables and the first stages' way from memory.  Many rows, loads
-// from memory and from L2 together: gate/up of 4096 tokens x 8, E4M3, 283 us,
-// 1.5 GB from memory (68 % of its peak), 5.3 GB from L2, the tensor cores at
-// 52 %; without the loads from memory it takes 225, without the products 256.
+// 54 us, 6.5 TB/s.  One token's 78 MB take 16.4 us: its 96 tiles give 96 of the
+// 152 CTAs work, and some 5 us are the launch, the tables and the first stages'
+// way from memory.  Many rows, loads from memory and from L2 together: gate/up
+// of 4096 tokens x 8, E4M3, 280 us, 1.5 GB from memory (67 % of its peak), 5.1 GB
+// from L2, the tensor cores at 51 %; without the loads from memory it took 225,
+// without the products 256.
 // A plain product of 4096 x 6144 x 6144, E2M1: 51 us, 6.1 PFLOP/s, tensor cores
 // at 62 %; 4.7 us of it are the last tiles' read-back.
 //
@@ -34,7 +35,7 @@
 // 128 and half of the activation rows (cta_group::2): a stage is 16 KB + 64 n
 // bytes instead of 16 KB + 128 n.  Loads from L2 (about 16 TB/s over all SMs)
 // bound tiles of many rows, so it takes them: gate/up of 32768 rows, E4M3, 280
-// us (314 alone), the E2M1 product 4096 x 6144 x 6144 50 us (60 alone).
+// us (315 alone), the E2M1 product 4096 x 6144 x 6144 51 us (60 alone).
 //
 // SPLIT: where there are too few tiles for the SMs, the CTAs of a cluster share
 // a tile's K range.  Each keeps its sums in its tensor memory; then every CTA

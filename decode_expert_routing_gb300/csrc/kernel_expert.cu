@@ -70,7 +70,7 @@ cudaError_t launch_mx_pack(const uint8_t* scale, int64_t E, int R, int K, int fp
 // CTAs are in place when the products end (the wait is for all of them, and
 // for the memory they wrote): CTAs of 64 threads find room for their registers
 // beside a CTA of the products; of 256 they did not, and started after them
-// (one token: 12.0 us for both launches, 12.7 with those).
+// (one token, rounded rows: 12.0 us for both launches, 12.7 with those).
 //
 // A launch of its own: added by the products' kernel, tokens finish when the
 // last of their experts does, and the CTA that sees it has all their sums to
@@ -79,7 +79,8 @@ cudaError_t launch_mx_pack(const uint8_t* scale, int64_t E, int R, int K, int fp
 //
 // Lines of y that have been read are given up (discard): nobody reads them
 // again, and those that still are in L2 need no way to memory.  Down of 64
-// tokens x 8, E2M1: 44.8 us (47.6 without); of 4096, E4M3: 260 (267).
+// tokens x 8, E2M1, rounded rows: 44.8 us (47.6 without); of 4096, E4M3: 260
+// (267).
 constexpr int kCombineThreads = 64;
 __device__ __forceinline__ void discard_line(const void* line) {
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
