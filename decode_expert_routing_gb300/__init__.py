@@ -1,4 +1,5 @@
-"""GB300-native MoE decode routing: router GEMV, top-k gate, sort, MXFP8 quant.
+"""GB300-native MoE decode routing: router GEMV, top-k gate, sort, MXFP8 quant,
+the experts' products, and the norm, rows and FP8 products around them.
 
 Thin Python binding over the C ABI of libmoe_route.so (include/moe_route.h):
 the functions below have the ABI's names without the ``mr_`` prefix, check
@@ -25,6 +26,9 @@ __all__ = [
     "PreparedRoute", "moe_sort_quant", "mxfp4_quant", "norm_apply", "moe_route_sort_quant_norm",
     "MxWeight", "ExpertScratch", "mx_gemm", "moe_gate_up", "moe_down", "PreparedMxGemm", "PreparedGateUp",
     "PreparedDown",
+    "add_rms_norm", "PreparedAddNorm", "fp8_quant", "fp8_gemm", "PreparedFp8Gemm", "moe_permute", "PreparedPermute",
+    "moe_permute_grad", "PreparedPermuteGrad", "moe_combine", "PreparedCombine", "moe_combine_grad",
+    "PreparedCombineGrad",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -95,6 +99,12 @@ SIGNATURES = {
     "mr_mx_gemm": (_I, [_P, _P]),
     "mr_moe_gate_up": (_I, [_P, _P]),
     "mr_moe_down": (_I, [_P, _P]),
+    "mr_add_rms_norm": (_I, [_P, _P]),
+    "mr_fp8_quant": (_I, [_P, _I64, _I, _I, _P, _P, _P]),
+    "mr_fp8_gemm": (_I, [_P, _P]),
+    "mr_moe_permute": (_I, [_P, _P]),
+    "mr_moe_combine": (_I, [_P, _P]),
+    "mr_moe_combine_grad": (_I, [_P, _P]),
 }
 
 
@@ -893,7 +903,8 @@ def _call_once(device, stream, make):
         call = make()
         call()
     if here != own:
-        for t in call.out if isinstance(call.out, tuple) else (call.out,):
+        outs = call.out
+        for t in outs.values() if isinstance(outs, dict) else outs if isinstance(outs, tuple) else (outs,):
             if any(t is m for m in call._made):
                 t.record_stream(here)
     return call.out
@@ -1203,3 +1214,375 @@ def moe_down(q, scale, w2: MxWeight, topk_ids, topk_weights, sorted_token_ids, e
     return _call_once(_one_device(q=q), stream,
                       lambda: PreparedDown(q, scale, w2, topk_ids, topk_weights, sorted_token_ids, expert_ids, block, add,
                                            out, scratch, slots_fp32, _once=True))
+
+
+# ---------------------------------------------------------------- residual norm, FP8 with scales per 128
+
+NORM_QUANT = {**QUANT_FORMAT, "fp8": 3}  # of add_rms_norm
+
+
+class AddNormParams(ctypes.Structure):
+    """mr_add_rms_norm_params of moe_route.h, field for field."""
+    _fields_ = [("x", _P), ("ldx", _I64), ("residual", _P), ("ldr", _I64), ("norm_weight", _P), ("norm_kind", _I),
+                ("eps", ctypes.c_float), ("M", _I), ("K", _I), ("quant_format", _I), ("sres", _P), ("lds", _I64),
+                ("rstd", _P), ("xn", _P), ("q", _P), ("scale", _P)]
+
+
+class Fp8GemmParams(ctypes.Structure):
+    """mr_fp8_gemm_params of moe_route.h, field for field."""
+    _fields_ = [("q", _P), ("ldq", _I64), ("x_scale", _P), ("ldxs", _I64), ("w", _P), ("ldw", _I64), ("w_scale", _P),
+                ("ldws", _I64), ("M", _I), ("R", _I), ("K", _I), ("out", _P), ("ldo", _I64), ("out_fp32", _I)]
+
+
+def _ld(t, multiple: int = 1):
+    """Row stride of a 2-D tensor; of a single row any will do."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // multiple) * multiple
+
+
+class PreparedAddNorm(_Prepared):
+    """add_rms_norm over fixed buffers; arguments as add_rms_norm."""
+
+    def __init__(self, x, residual, norm_weight, eps: float = 1e-6, norm: str = "gemma", quant=None, outputs=None,
+                 out=None, _once=False):
+        torch = _torch()
+        if quant not in NORM_QUANT:
+            raise ValueError(f"quant must be one of {list(NORM_QUANT)}")
+        if norm not in NORM_KIND:
+            raise ValueError(f"norm must be one of {list(NORM_KIND)}")
+        out = dict(out or {})
+        codes = {"q", "scale"} if quant is not None else set()
+        if outputs is None:
+            outputs = {"sres", "rstd"} | (codes or {"xn"})
+        wanted = set(outputs) | set(out) | codes
+        known = {"sres", "rstd", "xn"} | codes
+        if wanted - known or not wanted:
+            raise ValueError(f"outputs must be some of {sorted(known)}")
+        dev = _one_device(x=x, residual=residual, norm_weight=norm_weight, **out)
+        _row_major_2d(x, "x")
+        M, K = x.shape
+        if residual is not None:
+            _row_major_2d(residual, "residual")
+            if residual.shape != x.shape:
+                raise ValueError("residual must have the shape of x")
+        if norm_weight.dim() != 1 or norm_weight.shape[0] != K or not norm_weight.is_contiguous():
+            raise ValueError("norm_weight must be contiguous [K]")
+        if quant in ("mxfp8", "mxfp4") and K % 32:
+            raise ValueError("K must be a multiple of 32")
+        bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+        spec = {"sres": ((M, K), bf16), "rstd": ((M,), f32), "xn": ((M, K), bf16),
+                "q": ((M, K // 2 if quant == "mxfp4" else K), u8),
+                "scale": ((M, -(-K // 128)), f32) if quant == "fp8" else ((M, K // 32), u8)}
+        made = []
+        for name in ("sres", "rstd", "xn", "q", "scale"):
+            if name not in wanted:
+                continue
+            shape, dt = spec[name]
+            if name not in out:
+                out[name] = torch.empty(shape, dtype=dt, device=dev)
+                made.append(out[name])
+            elif name == "sres":  # (as x: any row stride)
+                if out[name].shape != x.shape or out[name].dtype != bf16:
+                    raise ValueError(f"sres must be bfloat16 {tuple(x.shape)}")
+                _row_major_2d(out[name], "sres")
+            else:
+                _check_out(out[name], name, shape, dt, dev)
+        p = self.p = AddNormParams()
+        p.x, p.ldx = _dev_ptr(x, "x", bf16), _ld(x, 8)
+        p.residual = _dev_ptr(residual, "residual", bf16, allow_none=True)
+        p.ldr = 0 if residual is None else _ld(residual, 8)
+        p.norm_weight, p.norm_kind = _dev_ptr(norm_weight, "norm_weight", bf16), NORM_KIND[norm]
+        p.eps, p.M, p.K, p.quant_format = float(eps), M, K, NORM_QUANT[quant]
+        for name in wanted:
+            setattr(p, name, out[name].data_ptr())
+        p.lds = _ld(out["sres"], 8) if "sres" in wanted else 0
+        self.out, self.device, self._keep = out, dev, (x, residual, norm_weight)
+        self._ref = ctypes.byref(p)
+        self._fn, self._name = _load().mr_add_rms_norm, "mr_add_rms_norm"
+        self._own(made, (), _once)
+
+
+def add_rms_norm(x, residual, norm_weight, eps: float = 1e-6, norm: str = "gemma", quant=None, outputs=None, out=None,
+                 stream=None):
+    """The residual's addition and the RMSNorm behind it (mr_add_rms_norm): a
+    dict of sres = bf16(x + residual) (residual None: x), rstd [M] fp32, xn
+    = bf16((sres * rstd) * s) with s = g ("rms") or 1 + g ("gemma"), and with
+    quant its codes q and scales: "mxfp8" / "mxfp4" (uint8 [M, K/32]) or "fp8"
+    (fp32 [M, ceil(K/128)], as fp8_quant).  outputs: which ones (default sres,
+    rstd and the codes, or xn without quant); out: a dict of given tensors
+    (sres may be x or residual itself)."""
+    return _call_once(_one_device(x=x), stream,
+                      lambda: PreparedAddNorm(x, residual, norm_weight, eps, norm, quant, outputs, out, _once=True))
+
+
+def fp8_quant(x, out=None, stream=None):
+    """(q uint8 [M, K] e4m3 codes, scale fp32 [M, ceil(K/128)]) of bf16 rows."""
+    torch = _torch()
+    dev = _one_device(x=x, **({} if out is None else dict(q=out[0], scale=out[1])))
+    _row_major_2d(x, "x")
+    M, K = x.shape
+    with torch.cuda.stream(_given_stream(dev, stream)):
+        if out is None:
+            out = (torch.empty((M, K), dtype=torch.uint8, device=dev),
+                   torch.empty((M, -(-K // 128)), dtype=torch.float32, device=dev))
+    q, s = out
+    _check_out(q, "q", (M, K), torch.uint8, dev)
+    _check_out(s, "scale", (M, -(-K // 128)), torch.float32, dev)
+    own = _given_stream(dev, stream) or torch.cuda.current_stream(dev)
+    with _launch_ctx(dev):
+        _check(_load().mr_fp8_quant(_dev_ptr(x, "x", torch.bfloat16), _ld(x, 8), M, K, _dev_ptr(q, "q", torch.uint8),
+                                    _dev_ptr(s, "scale", torch.float32), ctypes.c_void_p(own.cuda_stream)),
+               "mr_fp8_quant")
+        here = torch.cuda.current_stream(dev)
+        if own != here:  # (kept for the current stream too, whose results they are)
+            for t in out:
+                t.record_stream(here)
+    return q, s
+
+
+class PreparedFp8Gemm(_Prepared):
+    """fp8_gemm over fixed buffers; arguments as fp8_gemm."""
+
+    def __init__(self, q, scale, w, w_scale, out=None, out_dtype=None, _once=False):
+        torch = _torch()
+        dev = _one_device(q=q, scale=scale, w=w, w_scale=w_scale, out=out)
+        for t, name in ((q, "q"), (scale, "scale"), (w, "w"), (w_scale, "w_scale")):
+            if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+                raise ValueError(f"{name} must be 2-D with a contiguous last dimension")
+        M, K = q.shape
+        R, kb = w.shape[0], -(-K // 128)
+        if w.shape[1] != K:
+            raise ValueError(f"w must be [R, {K}]")
+        if tuple(scale.shape) != (M, kb):
+            raise ValueError(f"scale must be {(M, kb)}")
+        if tuple(w_scale.shape) != (-(-R // 128), kb):
+            raise ValueError(f"w_scale must be {(-(-R // 128), kb)}")
+        made = out is None
+        if made:
+            out = torch.empty((M, R), dtype=out_dtype or torch.bfloat16, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out must be {out_dtype}, got {out.dtype}")
+        if out.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("out must be bfloat16 or float32")
+        if tuple(out.shape) != (M, R) or (R > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < R):
+            raise ValueError(f"out must have shape {(M, R)} with a contiguous last dimension")
+        p = self.p = Fp8GemmParams()
+        p.q, p.ldq = _dev_ptr(q, "q", torch.uint8), _ld(q, 16)
+        p.x_scale, p.ldxs = _dev_ptr(scale, "scale", torch.float32), _ld(scale)
+        p.w, p.ldw = _dev_ptr(w, "w", torch.uint8), _ld(w, 16)
+        p.w_scale, p.ldws = _dev_ptr(w_scale, "w_scale", torch.float32), _ld(w_scale)
+        p.M, p.R, p.K = M, R, K
+        p.out, p.ldo, p.out_fp32 = out.data_ptr(), _ld(out), int(out.dtype == torch.float32)
+        self.out, self.device, self._keep = out, dev, (q, scale, w, w_scale)
+        self._ref = ctypes.byref(p)
+        self._fn, self._name = _load().mr_fp8_gemm, "mr_fp8_gemm"
+        self._own((out,) if made else (), (), _once)
+
+
+def fp8_gemm(q, scale, w, w_scale, out=None, out_dtype=None, stream=None):
+    """Product of E4M3 operands with fp32 scales per 128 (mr_fp8_gemm): [M, R]
+    (bf16, or out_dtype fp32) = x [M, K] @ w [R, K]^T with x given as the codes
+    q (uint8) and scales [M, ceil(K/128)] of fp8_quant, w as codes (uint8) and
+    scales [ceil(R/128), ceil(K/128)].  Rows start on 16 bytes."""
+    return _call_once(_one_device(q=q), stream,
+                      lambda: PreparedFp8Gemm(q, scale, w, w_scale, out, out_dtype, _once=True))
+
+
+# ---------------------------------------------------------------- rows to the experts and back
+
+class PermuteParams(ctypes.Structure):
+    """mr_moe_permute_params of moe_route.h, field for field."""
+    _fields_ = [("x", _P), ("ldx", _I64), ("row_type", _I), ("M", _I), ("K", _I), ("topk", _I), ("E", _I),
+                ("topk_ids", _P), ("sorted_token_ids", _P), ("num_tokens_post_padded", _P), ("capacity", _I64),
+                ("rows", _P), ("positions", _P)]
+
+
+class CombineParams(ctypes.Structure):
+    """mr_moe_combine_params of moe_route.h, field for field."""
+    _fields_ = [("y", _P), ("ldy", _I64), ("row_type", _I), ("capacity", _I64), ("M", _I), ("K", _I), ("topk", _I),
+                ("positions", _P), ("topk_weights", _P), ("add", _P), ("ldadd", _I64), ("out", _P)]
+
+
+class CombineGradParams(ctypes.Structure):
+    """mr_moe_combine_grad_params of moe_route.h, field for field."""
+    _fields_ = [("grad_out", _P), ("ldg", _I64), ("y", _P), ("ldy", _I64), ("row_type", _I), ("capacity", _I64),
+                ("M", _I), ("K", _I), ("topk", _I), ("positions", _P), ("topk_weights", _P), ("sorted_token_ids", _P),
+                ("num_tokens_post_padded", _P), ("grad_y", _P), ("grad_weights", _P)]
+
+
+def _row_type(t, name, codes=False):
+    torch = _torch()
+    types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, **({torch.uint8: 3} if codes else {})}
+    if t.dtype not in types:
+        raise ValueError(f"{name} must be one of {[str(d) for d in types]}, got {t.dtype}")
+    return types[t.dtype]
+
+
+def _rows_like(t, name, shape, dtype):
+    """An operand of rows: any row stride."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} with a contiguous last dimension")
+
+
+def _check_sorted_ids(st, nt, dev):
+    torch = _torch()
+    if st.dim() != 1 or st.numel() < 1:
+        raise ValueError("sorted_token_ids must be a vector")
+    _check_out(st, "sorted_token_ids", st.numel(), torch.int32, dev, min_numel=True)
+    _check_out(nt, "num_tokens_post_padded", 1, torch.int32, dev, min_numel=True)
+
+
+class PreparedPermute(_Prepared):
+    """moe_permute over fixed buffers; arguments as moe_permute."""
+
+    def __init__(self, x, topk_ids, num_experts: int, sorted_token_ids, num_tokens_post_padded, out=None,
+                 positions=None, _once=False):
+        torch = _torch()
+        dev = _one_device(x=x, topk_ids=topk_ids, sorted_token_ids=sorted_token_ids,
+                          num_tokens_post_padded=num_tokens_post_padded, out=out, positions=positions)
+        if x.dim() != 2 or topk_ids.dim() != 2:
+            raise ValueError("x must be [M, K] and topk_ids [M, k]")
+        (M, K), topk = x.shape, topk_ids.shape[1]
+        _rows_like(x, "x", (M, K), x.dtype)
+        _check_out(topk_ids, "topk_ids", (M, topk), torch.int32, dev)
+        _check_sorted_ids(sorted_token_ids, num_tokens_post_padded, dev)
+        cap, made = sorted_token_ids.numel(), []
+        if out is None:
+            out = torch.empty((cap, K), dtype=x.dtype, device=dev)
+            made.append(out)
+        _check_out(out, "out", (cap, K), x.dtype, dev)
+        if positions is None:
+            positions = torch.empty((M, topk), dtype=torch.int32, device=dev)
+            made.append(positions)
+        _check_out(positions, "positions", (M, topk), torch.int32, dev)
+        p = self.p = PermuteParams()
+        p.x, p.ldx, p.row_type = x.data_ptr(), _ld(x), _row_type(x, "x", codes=True)
+        p.M, p.K, p.topk, p.E = M, K, topk, num_experts
+        p.topk_ids, p.sorted_token_ids = topk_ids.data_ptr(), sorted_token_ids.data_ptr()
+        p.num_tokens_post_padded, p.capacity = num_tokens_post_padded.data_ptr(), cap
+        p.rows, p.positions = out.data_ptr(), positions.data_ptr()
+        self.out, self.device = (out, positions), dev
+        self._keep = (x, topk_ids, sorted_token_ids, num_tokens_post_padded)
+        self._ref = ctypes.byref(p)
+        self._fn, self._name = _load().mr_moe_permute, "mr_moe_permute"
+        self._own(made, (), _once)
+
+
+def moe_permute(x, topk_ids, num_experts: int, sorted_token_ids, num_tokens_post_padded, out=None, positions=None,
+                stream=None):
+    """Rows of tokens to the sorted positions of their assignments
+    (mr_moe_permute): (rows [capacity, K] in x's type, positions int32 [M, k]).
+    x: [M, K], bf16, fp16, fp32 or uint8 (codes, scale bytes).  Padding rows
+    are zero, rows behind num_tokens_post_padded are left as they were, and an
+    assignment that the sort left out has position -1."""
+    return _call_once(_one_device(x=x), stream,
+                      lambda: PreparedPermute(x, topk_ids, num_experts, sorted_token_ids, num_tokens_post_padded, out,
+                                              positions, _once=True))
+
+
+class PreparedCombine(_Prepared):
+    """moe_combine over fixed buffers; arguments as moe_combine."""
+
+    def __init__(self, y, positions, topk_weights=None, add=None, out=None, _once=False):
+        torch = _torch()
+        dev = _one_device(y=y, positions=positions, topk_weights=topk_weights, add=add, out=out)
+        if y.dim() != 2 or positions.dim() != 2:
+            raise ValueError("y must be [capacity, K] and positions [M, k]")
+        (cap, K), (M, topk) = y.shape, positions.shape
+        _rows_like(y, "y", (cap, K), y.dtype)
+        _check_out(positions, "positions", (M, topk), torch.int32, dev)
+        if topk_weights is not None:
+            _check_out(topk_weights, "topk_weights", (M, topk), torch.float32, dev)
+        if add is not None:
+            _rows_like(add, "add", (M, K), y.dtype)
+        made = out is None
+        if made:
+            out = torch.empty((M, K), dtype=y.dtype, device=dev)
+        _check_out(out, "out", (M, K), y.dtype, dev)
+        p = self.p = CombineParams()
+        p.y, p.ldy, p.row_type, p.capacity = y.data_ptr(), _ld(y), _row_type(y, "y"), cap
+        p.M, p.K, p.topk, p.positions = M, K, topk, positions.data_ptr()
+        p.topk_weights = None if topk_weights is None else topk_weights.data_ptr()
+        if add is not None:
+            p.add, p.ldadd = add.data_ptr(), _ld(add)
+        p.out = out.data_ptr()
+        self.out, self.device, self._keep = out, dev, (y, positions, topk_weights, add)
+        self._ref = ctypes.byref(p)
+        self._fn, self._name = _load().mr_moe_combine, "mr_moe_combine"
+        self._own((out,) if made else (), (), _once)
+
+
+def moe_combine(y, positions, topk_weights=None, add=None, out=None, stream=None):
+    """Rows at the sorted positions back to their tokens (mr_moe_combine):
+    [M, K] = add + sum over a token's slots of topk_weights (None: one) times
+    the row of y [capacity, K] at positions [M, k]; positions outside y add
+    nothing.  out may be add itself."""
+    return _call_once(_one_device(y=y), stream,
+                      lambda: PreparedCombine(y, positions, topk_weights, add, out, _once=True))
+
+
+class PreparedPermuteGrad(PreparedCombine):
+    """moe_permute_grad over fixed buffers; arguments as moe_permute_grad."""
+
+    def __init__(self, grad_rows, positions, out=None, _once=False):
+        super().__init__(grad_rows, positions, out=out, _once=_once)
+
+
+def moe_permute_grad(grad_rows, positions, out=None, stream=None):
+    """Gradient of moe_permute for x: [M, K] = the sum over a token's slots of
+    the rows of grad_rows [capacity, K] at positions [M, k] (those of padding
+    positions count for nothing)."""
+    return _call_once(_one_device(grad_rows=grad_rows), stream,
+                      lambda: PreparedPermuteGrad(grad_rows, positions, out, _once=True))
+
+
+class PreparedCombineGrad(_Prepared):
+    """moe_combine_grad over fixed buffers; arguments as moe_combine_grad."""
+
+    def __init__(self, grad_out, y, positions, topk_weights, sorted_token_ids, num_tokens_post_padded, out=None,
+                 grad_weights=None, _once=False):
+        torch = _torch()
+        dev = _one_device(grad_out=grad_out, y=y, positions=positions, topk_weights=topk_weights,
+                          sorted_token_ids=sorted_token_ids, num_tokens_post_padded=num_tokens_post_padded, out=out,
+                          grad_weights=grad_weights)
+        if grad_out.dim() != 2 or positions.dim() != 2:
+            raise ValueError("grad_out must be [M, K] and positions [M, k]")
+        (M, K), topk = grad_out.shape, positions.shape[1]
+        _rows_like(grad_out, "grad_out", (M, K), grad_out.dtype)
+        _check_out(positions, "positions", (M, topk), torch.int32, dev)
+        if topk_weights is not None:
+            _check_out(topk_weights, "topk_weights", (M, topk), torch.float32, dev)
+        _check_sorted_ids(sorted_token_ids, num_tokens_post_padded, dev)
+        cap, made = sorted_token_ids.numel(), []
+        _rows_like(y, "y", (cap, K), grad_out.dtype)
+        if out is None:
+            out = torch.empty((cap, K), dtype=y.dtype, device=dev)
+            made.append(out)
+        _check_out(out, "out", (cap, K), y.dtype, dev)
+        if grad_weights is None:
+            grad_weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
+            made.append(grad_weights)
+        _check_out(grad_weights, "grad_weights", (M, topk), torch.float32, dev)
+        p = self.p = CombineGradParams()
+        p.grad_out, p.ldg, p.y, p.ldy = grad_out.data_ptr(), _ld(grad_out), y.data_ptr(), _ld(y)
+        p.row_type, p.capacity = _row_type(y, "y"), cap
+        p.M, p.K, p.topk, p.positions = M, K, topk, positions.data_ptr()
+        p.topk_weights = None if topk_weights is None else topk_weights.data_ptr()
+        p.sorted_token_ids = sorted_token_ids.data_ptr()
+        p.num_tokens_post_padded = num_tokens_post_padded.data_ptr()
+        p.grad_y, p.grad_weights = out.data_ptr(), grad_weights.data_ptr()
+        self.out, self.device = (out, grad_weights), dev
+        self._keep = (grad_out, y, positions, topk_weights, sorted_token_ids, num_tokens_post_padded)
+        self._ref = ctypes.byref(p)
+        self._fn, self._name = _load().mr_moe_combine_grad, "mr_moe_combine_grad"
+        self._own(made, (), _once)
+
+
+def moe_combine_grad(grad_out, y, positions, topk_weights, sorted_token_ids, num_tokens_post_padded, out=None,
+                     grad_weights=None, stream=None):
+    """Gradients of moe_combine for its y and topk_weights (mr_moe_combine_grad):
+    (grad_y [capacity, K], grad_weights fp32 [M, k]).  grad_y has zeros at
+    padding positions and is left as it was behind num_tokens_post_padded;
+    out may be y itself.  (The gradient of add is grad_out.)"""
+    return _call_once(_one_device(grad_out=grad_out), stream,
+                      lambda: PreparedCombineGrad(grad_out, y, positions, topk_weights, sorted_token_ids,
+                                                  num_tokens_post_padded, out, grad_weights, _once=True))

@@ -6,8 +6,11 @@
 
 #include "../../include/moe_route.h"
 #include "expert_plan.h"
+#include "fp8_plan.h"
 #include "internal.h"
+#include "norm_plan.h"
 #include "route_plan.h"
+#include "rows_plan.h"
 #include "sort.cuh"
 
 namespace {
@@ -102,8 +105,8 @@ int mr_set_wait_limit_ns(uint64_t ns) {
 
 int mr_device_error(int clear) {
     const int v = mr::route_device_error(clear), t = mr::tc_gemv_device_error(clear);
-    const int x = mr::expert_device_error(clear);
-    return (v < 0 || t < 0 || x < 0) ? MR_ERR_CUDA : (v || t || x) ? MR_ERR_TIMEOUT : MR_OK;
+    const int x = mr::expert_device_error(clear), f = mr::fp8_device_error(clear);
+    return (v < 0 || t < 0 || x < 0 || f < 0) ? MR_ERR_CUDA : (v || t || x || f) ? MR_ERR_TIMEOUT : MR_OK;
 }
 
 #ifdef MR_TRACE
@@ -756,6 +759,192 @@ int mr_moe_down(const mr_moe_down_params* p, void* stream) {
     c.scratch = p->scratch;
     c.scratch_low = p->scratch_low;
     return run_expert(c, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ residual norm, FP8 with scales per 128
+
+// a bf16 operand or output of rows, 16-byte aligned
+static bool bad_rows(const void* p, int64_t ld, int K) { return p == nullptr || !aligned(p, 16) || ld < K || ld % 8 != 0; }
+
+extern "C" {
+
+int mr_add_rms_norm(const mr_add_rms_norm_params* p, void* stream) {
+    if (p == nullptr) return MR_ERR_INVALID_ARG;
+    int s = check_x(p->x, p->ldx, p->M, p->K);
+    if (s != MR_OK) return s;
+    if (p->residual != nullptr && bad_rows(p->residual, p->ldr, p->K)) return MR_ERR_INVALID_ARG;
+    if (p->norm_weight == nullptr || !aligned(p->norm_weight, 16)) return MR_ERR_INVALID_ARG;
+    if (p->norm_kind != MR_NORM_RMS && p->norm_kind != MR_NORM_GEMMA) return MR_ERR_INVALID_ARG;
+    if (!(p->eps >= 0.0f && p->eps <= 3.4e38f)) return MR_ERR_INVALID_ARG;
+    const int qf = p->quant_format;
+    if (qf < MR_QUANT_NONE || qf > MR_QUANT_FP8) return MR_ERR_INVALID_ARG;
+    const int multiple = qf == MR_QUANT_NONE ? 8 : qf == MR_QUANT_FP8 ? 16 : 32;
+    if (p->K % multiple != 0 || p->K > mr::kNormMaxK) return MR_ERR_UNSUPPORTED;
+    if (qf == MR_QUANT_NONE && (p->q != nullptr || p->scale != nullptr)) return MR_ERR_INVALID_ARG;
+    if (qf != MR_QUANT_NONE && (p->q == nullptr || !aligned(p->q, 8) || p->scale == nullptr ||
+                                (qf == MR_QUANT_FP8 && !aligned(p->scale, 4))))
+        return MR_ERR_INVALID_ARG;
+    if (p->sres == nullptr && p->rstd == nullptr && p->xn == nullptr && p->q == nullptr) return MR_ERR_INVALID_ARG;
+    if (p->sres != nullptr && bad_rows(p->sres, p->lds, p->K)) return MR_ERR_INVALID_ARG;
+    if ((p->rstd != nullptr && !aligned(p->rstd, 4)) || (p->xn != nullptr && !aligned(p->xn, 16)))
+        return MR_ERR_INVALID_ARG;
+    mr::NormArgs a{};
+    a.x = static_cast<const uint16_t*>(p->x);
+    a.residual = static_cast<const uint16_t*>(p->residual);
+    a.g = static_cast<const uint16_t*>(p->norm_weight);
+    a.sres = static_cast<uint16_t*>(p->sres);
+    a.xn = static_cast<uint16_t*>(p->xn);
+    a.rstd = p->rstd;
+    a.q = p->q;
+    a.scale = p->scale;
+    a.ldx = p->ldx;
+    a.ldr = p->ldr;
+    a.lds = p->lds;
+    a.M = p->M;
+    a.K = p->K;
+    a.gemma = p->norm_kind == MR_NORM_GEMMA ? 1 : 0;
+    a.fmt = qf;
+    a.eps = p->eps;
+    return cuda_status(mr::launch_add_norm(a, as_stream(stream)));
+}
+
+int mr_fp8_quant(const void* x, int64_t ldx, int M, int K, uint8_t* q, float* scale, void* stream) {
+    const int s = check_x(x, ldx, M, K);
+    if (s != MR_OK) return s;
+    if (q == nullptr || !aligned(q, 8) || scale == nullptr || !aligned(scale, 4)) return MR_ERR_INVALID_ARG;
+    if (K % 16 != 0) return MR_ERR_UNSUPPORTED;
+    return cuda_status(mr::launch_fp8_quant(x, ldx, M, K, q, scale, as_stream(stream)));
+}
+
+int mr_fp8_gemm(const mr_fp8_gemm_params* p, void* stream) {
+    if (p == nullptr || p->M < 1 || p->R < 1 || p->K < 1) return MR_ERR_INVALID_ARG;
+    const int64_t kb = ((int64_t)p->K + 127) / 128;
+    if (p->q == nullptr || !aligned(p->q, 16) || p->ldq < p->K || p->ldq % 16 != 0 || p->w == nullptr ||
+        !aligned(p->w, 16) || p->ldw < p->K || p->ldw % 16 != 0)
+        return MR_ERR_INVALID_ARG;
+    if (p->x_scale == nullptr || !aligned(p->x_scale, 4) || p->ldxs < kb || p->w_scale == nullptr ||
+        !aligned(p->w_scale, 4) || p->ldws < kb)
+        return MR_ERR_INVALID_ARG;
+    if (p->out == nullptr || !aligned(p->out, p->out_fp32 ? 4 : 2) || p->ldo < p->R) return MR_ERR_INVALID_ARG;
+    // (limits of the tensor maps and of 32-bit counts)
+    if (p->M > (1 << 30) || p->R > (1 << 24) || p->K > (1 << 24) || p->ldq >= ((int64_t)1 << 40) ||
+        p->ldw >= ((int64_t)1 << 40) || ((int64_t)p->M / 128 + 1) * ((int64_t)p->R / 16 + 1) >= ((int64_t)1 << 31))
+        return MR_ERR_UNSUPPORTED;
+    mr::Fp8GemmCall c{};
+    c.x = p->q;
+    c.w = p->w;
+    c.xs = p->x_scale;
+    c.ws = p->w_scale;
+    c.ldx = p->ldq;
+    c.ldw = p->ldw;
+    c.ldxs = p->ldxs;
+    c.ldws = p->ldws;
+    c.ldo = p->ldo;
+    c.M = p->M;
+    c.R = p->R;
+    c.K = p->K;
+    c.out = p->out;
+    c.out_fp32 = p->out_fp32 ? 1 : 0;
+    cudaError_t e = cudaSuccess;
+    const int s = mr::launch_fp8_gemm(c, as_stream(stream), &e);
+    return s == MR_ERR_CUDA ? cuda_status(e) : s;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ rows to the experts and back
+
+static int check_row_call(int type, bool bytes, int64_t cap, int M, int K, int topk) {
+    if (type < MR_ROW_BF16 || type > (bytes ? MR_ROW_U8 : MR_ROW_FP32)) return MR_ERR_INVALID_ARG;
+    if (M < 1 || K < 1 || topk < 1 || cap < 1) return MR_ERR_INVALID_ARG;
+    if (topk > MR_MAX_TOPK || (int64_t)M * topk >= ((int64_t)1 << 30) || cap >= ((int64_t)1 << 31) || K > (1 << 24))
+        return MR_ERR_UNSUPPORTED;
+    return MR_OK;
+}
+static bool bad_row(const void* p, int64_t ld, int K, int type) {
+    return p == nullptr || !aligned(p, (uintptr_t)mr::row_elem_bytes(type)) || ld < K || ld >= ((int64_t)1 << 40);
+}
+static bool bad_i32(const void* p) { return p == nullptr || !aligned(p, 4); }
+
+extern "C" {
+
+int mr_moe_permute(const mr_moe_permute_params* p, void* stream) {
+    if (p == nullptr) return MR_ERR_INVALID_ARG;
+    const int s = check_row_call(p->row_type, true, p->capacity, p->M, p->K, p->topk);
+    if (s != MR_OK) return s;
+    if (p->E < 1 || bad_row(p->x, p->ldx, p->K, p->row_type) || bad_row(p->rows, p->K, p->K, p->row_type) ||
+        bad_i32(p->topk_ids) || bad_i32(p->sorted_token_ids) || bad_i32(p->num_tokens_post_padded) ||
+        bad_i32(p->positions))
+        return MR_ERR_INVALID_ARG;
+    mr::ToExpertsArgs a{};
+    a.x = p->x;
+    a.ldx = p->ldx;
+    a.sorted = p->sorted_token_ids;
+    a.npost = p->num_tokens_post_padded;
+    a.ids = p->topk_ids;
+    a.positions = p->positions;
+    a.out = p->rows;
+    a.cap = p->capacity;
+    a.M = p->M;
+    a.K = p->K;
+    a.topk = p->topk;
+    a.E = p->E;
+    a.type = p->row_type;
+    return cuda_status(mr::launch_to_experts(a, as_stream(stream)));
+}
+
+int mr_moe_combine(const mr_moe_combine_params* p, void* stream) {
+    if (p == nullptr) return MR_ERR_INVALID_ARG;
+    const int s = check_row_call(p->row_type, false, p->capacity, p->M, p->K, p->topk);
+    if (s != MR_OK) return s;
+    if (bad_row(p->y, p->ldy, p->K, p->row_type) || bad_row(p->out, p->K, p->K, p->row_type) || bad_i32(p->positions) ||
+        (p->topk_weights != nullptr && !aligned(p->topk_weights, 4)) ||
+        (p->add != nullptr && bad_row(p->add, p->ldadd, p->K, p->row_type)))
+        return MR_ERR_INVALID_ARG;
+    mr::ToTokensArgs a{};
+    a.y = p->y;
+    a.add = p->add;
+    a.ldy = p->ldy;
+    a.ldadd = p->add != nullptr ? p->ldadd : 0;
+    a.cap = p->capacity;
+    a.positions = p->positions;
+    a.weights = p->topk_weights;
+    a.out = p->out;
+    a.M = p->M;
+    a.K = p->K;
+    a.topk = p->topk;
+    a.type = p->row_type;
+    return cuda_status(mr::launch_to_tokens(a, as_stream(stream)));
+}
+
+int mr_moe_combine_grad(const mr_moe_combine_grad_params* p, void* stream) {
+    if (p == nullptr) return MR_ERR_INVALID_ARG;
+    const int s = check_row_call(p->row_type, false, p->capacity, p->M, p->K, p->topk);
+    if (s != MR_OK) return s;
+    if (bad_row(p->grad_out, p->ldg, p->K, p->row_type) || bad_row(p->y, p->ldy, p->K, p->row_type) ||
+        bad_row(p->grad_y, p->K, p->K, p->row_type) || bad_i32(p->positions) || bad_i32(p->sorted_token_ids) ||
+        bad_i32(p->num_tokens_post_padded) || (p->topk_weights != nullptr && !aligned(p->topk_weights, 4)) ||
+        p->grad_weights == nullptr || !aligned(p->grad_weights, 4))
+        return MR_ERR_INVALID_ARG;
+    mr::ToExpertsArgs a{};
+    a.x = p->grad_out;
+    a.y = p->y;
+    a.ldx = p->ldg;
+    a.ldy = p->ldy;
+    a.weights = p->topk_weights;
+    a.sorted = p->sorted_token_ids;
+    a.npost = p->num_tokens_post_padded;
+    a.known = p->positions;
+    a.grad_w = p->grad_weights;
+    a.out = p->grad_y;
+    a.cap = p->capacity;
+    a.M = p->M;
+    a.K = p->K;
+    a.topk = p->topk;
+    a.type = p->row_type;
+    return cuda_status(mr::launch_to_experts(a, as_stream(stream)));
 }
 
 }  // extern "C"

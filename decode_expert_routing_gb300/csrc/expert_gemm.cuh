@@ -55,6 +55,7 @@
 #include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "tc_pipe.cuh"
 
 namespace mr {
 
@@ -104,58 +105,8 @@ struct ExpertArgs {
     int flags;
 };
 
-// Set when a bounded wait of the expert kernels ran out (read by the host).
-__device__ int g_ex_timeout;
-
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, unsigned parity) {
-    unsigned ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// The whole warp waits for the phase of this parity, at most limit_ns; a wait
-// that runs out sets the device's flag and *abort, which ends every other
-// wait of the CTA.
-__device__ __noinline__ bool ex_wait_slow(uint32_t bar, unsigned parity, unsigned long long limit_ns,
-                                          volatile int* abort) {
-    const unsigned long long t0 = global_ns();
-    for (int i = 1;; ++i) {
-        if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
-        if ((i & 15) != 0) continue;
-        const bool late = global_ns() - t0 >= limit_ns;
-        if (__any_sync(kFull, late)) {
-            *abort = 1;
-            atomicExch(&g_ex_timeout, 1);
-        }
-        if (__any_sync(kFull, *abort != 0)) return false;
-    }
-}
-__device__ __forceinline__ bool ex_wait(uint32_t bar, unsigned parity, unsigned long long limit_ns,
-                                        volatile int* abort) {
-    return __all_sync(kFull, mbar_try_wait(bar, parity)) || ex_wait_slow(bar, parity, limit_ns, abort);
-}
-// One lane of a converged warp, always the same one.
-__device__ __forceinline__ bool ex_elect() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-// Shared-memory matrix descriptors without their address field (address >> 4
-// in the low 14 bits).  Codes: K-major rows of 128 bytes in the 128-byte
-// swizzle (8-row groups 1024 bytes apart); a k-step starts 32 bytes further.
-constexpr unsigned long long kExDescCodes =
-    (1ull << 16) | ((unsigned long long)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 // Scale factors: 32 rows of 16 bytes without swizzle, 8-row groups 128 bytes apart.
 constexpr unsigned long long kExDescSf = ((unsigned long long)(128 >> 4) << 32) | (1ull << 46);
-__device__ __forceinline__ unsigned long long ex_desc(unsigned long long kind, uint32_t addr) {
-    return kind | (unsigned long long)((addr >> 4) & 0x3FFFu);
-}
 // 32 rows of 16 bytes to four tensor-memory columns, repeated in each of the
 // four 32-lane quarters: lane l, column c holds the four scales of row 32 c + l.
 // (PAIR: in both CTAs, each from its own shared memory.)
@@ -193,36 +144,6 @@ __device__ __forceinline__ void ex_mma(uint32_t d, unsigned long long a, unsigne
     else EX_MMA("1", "mxf8f6f4.block_scale.scale_vec::1X");
 }
 #undef EX_MMA
-// An arrival (PAIR: in both CTAs, at the same place) when the products issued so far are done.
-template <bool PAIR>
-__device__ __forceinline__ void ex_commit(uint32_t bar) {
-    if (PAIR)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                bar),
-            "h"((unsigned short)3)
-            : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                     : "memory");
-}
-// All threads of the cluster meet.  _meet: called from branches that a warp's
-// lanes may have left at different times.
-__device__ __forceinline__ void ex_cluster_meet() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ void ex_cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// 16 accumulator columns of this warp's 32 lanes.
-__device__ __forceinline__ void ex_ld16(uint32_t (&v)[16], uint32_t addr) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
 // L2 policies of the weights: those that one tile alone reads are the first to
 // go from L2, so that what is read again (activations, products on their way
 // to the sum) stays.  Gate/up of 16 tokens x 8 over 128 experts, E2M1: 54.5 us
@@ -254,19 +175,6 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* map, int x
 __device__ __forceinline__ void ex_cp_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// Barrier id of threads threads (whole warps); true when ok holds in all of them.
-__device__ __forceinline__ bool ex_sync(int id, int threads, bool ok) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
-        "barrier.cta.red.and.pred p, %1, %2, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(threads), "r"((uint32_t)ok)
-        : "memory");
-    return r != 0;
-}
-
 // a / b for a < 2^23 (a quotient rounded to within one, then put right): the
 // general division is several times longer, and the ones between the tables
 // and the first copy are in every call's way.

@@ -96,11 +96,11 @@ int check_counters(const void* scratch, cudaStream_t st);
 void* trace_buffer();
 
 // Launches kernel<<<grid, block, smem, st>>>(args...) through
-// cudaLaunchKernelEx, allowing programmatic dependent launch when the
-// MR_LAUNCH_PDL flag is set; returns the launch status.
+// cudaLaunchKernelEx, allowing programmatic dependent launch when overlap is
+// set; returns the launch status.
 template <class... KArgs, class... Args>
-cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                          cudaStream_t st, Args&&... args) {
+cudaError_t launch_with(bool overlap, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                        Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -108,11 +108,24 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = (launch_flags() & 1) ? 1 : 0;
+    attr[0].val.programmaticStreamSerializationAllowed = overlap ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+// The kernels that may touch memory before their wait: as the MR_LAUNCH_PDL flag says.
+template <class... KArgs, class... Args>
+cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                          Args&&... args) {
+    return launch_with((launch_flags() & 1) != 0, kernel, grid, block, smem, st, std::forward<Args>(args)...);
+}
+// Kernels that touch nothing before their wait for the kernel launched before
+// them: always.
+template <class... KArgs, class... Args>
+cudaError_t launch_overlapped(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                              Args&&... args) {
+    return launch_with(true, kernel, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
 // Opt a kernel into more than 48 KiB of dynamic shared memory, once per

@@ -1,0 +1,402 @@
+// Product of E4M3 operands with fp32 scales per 128 (mr_fp8_gemm).
+//
+//   out[m, r] = sum_b xs[m, b] ws[r / 128, b] P_b[m, r],   P_b[m, r] = sum_{k in b} q[m, k] w[r, k]
+//
+// The scales are any fp32 numbers, so the tensor core cannot apply them: it
+// computes one P_b (tcgen05.mma kind::f8f6f4, fp32) in tensor memory, and the
+// read-back warps add its scaled value to sums that they keep in registers
+// while it computes the next one in another buffer.  Rows of x are the
+// accumulator's lanes and rows of w its columns, so a thread has one row of x
+// and its scale is one number: a block costs a column one fused multiply-add
+// (two columns an instruction), and one product a scale block.
+//
+// Work: persistent CTAs (or pairs of two with cta_group::2) walk the tiles of
+// 128 (256) rows of x times n rows of w, row tiles fastest.  Warp 0 copies
+// (tensor maps, 128-byte swizzle, a block of 128 bytes a row per stage), warp 1
+// issues the products, warps 2-9 read back.
+#include "../../include/moe_route.h"
+#include "fp8_plan.h"
+#include "internal.h"
+#include "tc_pipe.cuh"
+#include "tensor_map.h"
+
+namespace mr {
+
+constexpr int kF8Threads = 320;
+constexpr int kF8Chunks = 8;  // of 16 columns, the most that a read-back thread keeps
+
+struct Fp8Args {
+    CUtensorMap tm_x, tm_w;  // boxes of xrows and n (pair: n / 2) rows x 128 bytes
+    const float *xs, *ws;
+    void* out;
+    int64_t ldxs, ldws, ldo, tiles;
+    unsigned long long wait_ns;
+    int M, R, KI, n, xrows, RT, nst, nbuf, out_fp32, vec, flags;
+};
+
+namespace {
+
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator, E4M3 operands, both K-major.
+__device__ __forceinline__ uint32_t f8_idesc(int m, int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+template <bool PAIR>
+__device__ __forceinline__ void f8_mma(uint32_t d, unsigned long long a, unsigned long long b, uint32_t idesc, bool acc) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"((uint32_t)acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"((uint32_t)acc)
+            : "memory");
+}
+__device__ __forceinline__ unsigned long long f8_pack(uint32_t lo, uint32_t hi) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+// acc += v * s on two fp32 numbers, each rounded once
+__device__ __forceinline__ void f8_fma2(unsigned long long& acc, unsigned long long v, unsigned long long s) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+}
+__device__ __forceinline__ float2 f8_unpack(unsigned long long v) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+// 16 columns (32 bytes of bf16 or 64 of fp32) of one row
+__device__ __forceinline__ void f8_store(const Fp8Args& a, int64_t m, int col, const unsigned long long* acc) {
+    const int left = a.R - col;
+    if (left <= 0) return;
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 t = f8_unpack(acc[i]);
+        f[2 * i] = t.x, f[2 * i + 1] = t.y;
+    }
+    if (a.out_fp32) {
+        float* o = static_cast<float*>(a.out) + m * a.ldo + col;
+        if (a.vec && left >= 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<float4*>(o)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < left) o[i] = f[i];
+        }
+    } else {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + m * a.ldo + col;
+        if (a.vec && left >= 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+            reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < left) o[i] = __float2bfloat16_rn(f[i]);
+        }
+    }
+}
+
+template <bool PAIR>
+__global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Args a) {
+    extern __shared__ __align__(16) unsigned char dsm[];
+    __shared__ __align__(8) unsigned long long s_full[kF8MaxStages], s_empty[kF8MaxStages], s_tfull[8], s_tempty[8], s_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
+    const int rank = PAIR ? (int)cluster_rank() : 0;
+    const uint32_t full0 = smem_u32(&s_full[0]), empty0 = smem_u32(&s_empty[0]);
+    const uint32_t tfull0 = smem_u32(&s_tfull[0]), tempty0 = smem_u32(&s_tempty[0]);
+    if (tid < kF8MaxStages) {
+        mbar_init(full0 + 8u * tid, PAIR && rank == 0 ? 2 : 1);  // (one from the peer)
+        mbar_init(empty0 + 8u * tid, 1);
+        if (tid < 8) {
+            mbar_init(tfull0 + 8u * tid, 1);
+            mbar_init(tempty0 + 8u * tid, PAIR ? 16 : 8);
+        }
+        if (tid == 8) mbar_init(smem_u32(&s_drain), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (tid == 9) s_abort = 0;
+    }
+    if (tid == 64) {
+        tma_prefetch_map(&a.tm_x);
+        tma_prefetch_map(&a.tm_w);
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    tc_fence_before();
+    if (PAIR) ex_cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    pdl_wait();
+
+    constexpr int of = PAIR ? 2 : 1;
+    const uint32_t tmem = __shfl_sync(kFull, s_tmem, 0);
+    const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
+    const uint32_t wbytes = (uint32_t)(a.n / of) * 128u, stage_bytes = wbytes + (uint32_t)a.xrows * 128u;
+    int st = 0;       // stage of the ring
+    unsigned ph = 0;  // its phase
+    int buf = 0;      // accumulator buffer
+    unsigned bph = 0;
+    const int64_t step = gridDim.x / of;
+
+    if (warp == 0) {
+        // ---- copies
+        int issued = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
+            const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT);
+            const int m0 = (rt * of + rank) * 128, w0 = ct * a.n + rank * (a.n / of);
+            for (int ki = 0; ki < a.KI; ++ki) {
+                if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
+                    ok = false;
+                    break;
+                }
+                if (ex_elect()) {
+                    const uint32_t full = full0 + 8u * st, at = base + (uint32_t)st * stage_bytes;
+                    mbar_expect_tx(full, stage_bytes + (((a.flags & 2) && issued == 0) ? 16u : 0u));
+                    tma_load_2d(at, &a.tm_w, ki * 128, w0, full);
+                    tma_load_2d(at + wbytes, &a.tm_x, ki * 128, m0, full);
+                }
+                __syncwarp();
+                ++issued;
+                if (++st == a.nst) st = 0, ph ^= 1u;
+            }
+        }
+        // after a wait that ran out: no copy stays in flight (bounded)
+        if (!ok && lane == 0) {
+            for (int i = 0; i < min(issued, a.nst); ++i) {
+                if (--st < 0) st = a.nst - 1, ph ^= 1u;
+                const unsigned long long t0 = global_ns();
+                while (!mbar_try_wait(full0 + 8u * st, ph) && global_ns() - t0 < a.wait_ns / 16 + 1000) {
+                }
+            }
+        }
+    } else if (warp == 1 && PAIR && rank == 1) {
+        // ---- a pair's products are issued by its first CTA: told when this CTA's operands are in place
+        bool ok = true;
+        const uint32_t peer = map_rank(full0, 0);
+        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
+            for (int ki = 0; ki < a.KI; ++ki) {
+                if (!ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
+                    ok = false;
+                    break;
+                }
+                if (ex_elect()) mbar_arrive_remote_shared(peer + 8u * st);
+                __syncwarp();
+                if (++st == a.nst) st = 0, ph ^= 1u;
+            }
+        }
+    } else if (warp == 1) {
+        // ---- products, a block into each buffer in turn
+        bool ok = true;
+        const uint32_t idesc = f8_idesc(128 * of, a.n);
+        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
+            for (int ki = 0; ki < a.KI; ++ki) {
+                if (!ex_wait(tempty0 + 8u * buf, bph ^ 1u, a.wait_ns, &s_abort) ||
+                    !ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (ex_elect()) {
+                    const uint32_t at = base + (uint32_t)st * stage_bytes, d = tmem + (uint32_t)(buf * a.n);
+                    const unsigned long long dw = ex_desc(kExDescCodes, at), dx = ex_desc(kExDescCodes, at + wbytes);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f8_mma<PAIR>(d, dx + 2 * j, dw + 2 * j, idesc, j > 0);
+                    ex_commit<PAIR>(empty0 + 8u * st);
+                    ex_commit<PAIR>(tfull0 + 8u * buf);
+                }
+                __syncwarp();
+                if (++st == a.nst) st = 0, ph ^= 1u;
+                if (++buf == a.nbuf) buf = 0, bph ^= 1u;
+            }
+        }
+    } else {
+        // ---- scaled sums: warps 2-5 take the first half of the columns, warps 6-9 the second
+        const int wq = warp & 3, grp = (warp - 2) >> 2, nch = a.n >> 4, half = (nch + 1) >> 1;
+        const int c0 = grp * half, mine = grp ? nch - half : half;  // chunks of 16 columns
+        const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+        const uint32_t tempty = PAIR ? map_rank(tempty0, 0) : tempty0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
+            const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT);
+            const int64_t m = (int64_t)(rt * of + rank) * 128 + wq * 32 + lane;
+            const int col0 = ct * a.n + c0 * 16;
+            // the scale block of the first columns, and the chunk from which on it is the next one
+            const int b0 = col0 >> 7, b1 = min(b0 + 1, (a.R - 1) >> 7), turn = 8 - ((col0 >> 4) & 7);
+            const float* xs = a.xs + (m < a.M ? m : a.M - 1) * a.ldxs;
+            const float* w0 = a.ws + (int64_t)min(b0, (a.R - 1) >> 7) * a.ldws;
+            const float* w1 = a.ws + (int64_t)b1 * a.ldws;
+            unsigned long long acc[kF8Chunks][8];
+#pragma unroll
+            for (int c = 0; c < kF8Chunks; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[c][i] = 0ull;
+            float nx = __ldg(xs), n0 = __ldg(w0), n1 = __ldg(w1);
+            for (int ki = 0; ki < a.KI; ++ki) {
+                const uint32_t u0 = __float_as_uint(__fmul_rn(nx, n0)), u1 = __float_as_uint(__fmul_rn(nx, n1));
+                const unsigned long long s0 = f8_pack(u0, u0), s1 = f8_pack(u1, u1);
+                if (ki + 1 < a.KI) nx = __ldg(xs + ki + 1), n0 = __ldg(w0 + ki + 1), n1 = __ldg(w1 + ki + 1);
+                if (!ex_wait(tfull0 + 8u * buf, bph, a.wait_ns, &s_abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + lanes + (uint32_t)(buf * a.n + c0 * 16);
+#pragma unroll
+                for (int c = 0; c < kF8Chunks; ++c) {
+                    if (c < mine) {
+                        uint32_t v[16];
+                        ex_ld16(v, d + 16u * c);
+                        const unsigned long long s = c < turn ? s0 : s1;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f8_fma2(acc[c][i], f8_pack(v[2 * i], v[2 * i + 1]), s);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_remote(tempty + 8u * buf);
+                    else mbar_arrive(tempty + 8u * buf);
+                }
+                if (++buf == a.nbuf) buf = 0, bph ^= 1u;
+            }
+            if (ok && m < a.M) {
+#pragma unroll
+                for (int c = 0; c < kF8Chunks; ++c)
+                    if (c < mine) f8_store(a, m, col0 + 16 * c, acc[c]);
+            }
+        }
+    }
+    __syncthreads();
+    if (PAIR) {
+        if (tid == 0 && s_abort)  // a wait that ran out here ends the peer's work too
+            asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(map_rank(smem_u32(&s_abort), (unsigned)rank ^ 1u)) : "memory");
+        __syncwarp();
+        ex_cluster_sync();  // (no CTA leaves while its peer may still use its memory)
+    }
+    if (warp == 1) {
+        if (s_abort) {
+            // products already issued are waited for before their tensor memory goes
+            if (rank == 0 && ex_elect()) ex_commit<PAIR>(smem_u32(&s_drain));
+            __syncwarp();
+            const unsigned long long t0 = global_ns();
+            while (!mbar_try_wait(smem_u32(&s_drain), 0) && global_ns() - t0 < a.wait_ns) {
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+        if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+bool encode_rows(CUtensorMap* map, const void* ptr, int K, int64_t rows, int64_t ld, int box_rows) {
+    const EncodeTiled fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool PAIR>
+cudaError_t launch_one(const Fp8Args& a, int grid, cudaStream_t st) {
+    static int prepared[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const auto kernel = fp8_gemm_kernel<PAIR>;
+    if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8Smem);
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&prepared[dev], 1, __ATOMIC_RELEASE);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kF8Threads);
+    cfg.dynamicSmemBytes = kF8Smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+int launch_fp8_gemm(const Fp8GemmCall& c, cudaStream_t st, cudaError_t* err) {
+    int dev = 0, sms = 0;
+    if ((*err = cudaGetDevice(&dev)) != cudaSuccess ||
+        (*err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return MR_ERR_CUDA;
+    const Fp8Plan p = fp8_plan(c.M, c.R, c.K, sms);
+    Fp8Args a{};
+    // (a row's stride matters only where there is another one)
+    if (!encode_rows(&a.tm_x, c.x, c.K, c.M, c.ldx, p.xrows) ||
+        !encode_rows(&a.tm_w, c.w, c.K, c.R, c.ldw, p.n / (p.pair ? 2 : 1)))
+        return MR_ERR_UNSUPPORTED;
+    a.xs = c.xs;
+    a.ws = c.ws;
+    a.out = c.out;
+    a.ldxs = c.ldxs;
+    a.ldws = c.ldws;
+    a.ldo = c.ldo;
+    a.tiles = (int64_t)p.RT * p.CT;
+    a.wait_ns = wait_limit_ns();
+    a.M = c.M;
+    a.R = c.R;
+    a.KI = (c.K + 127) / 128;
+    a.n = p.n;
+    a.xrows = p.xrows;
+    a.RT = p.RT;
+    a.nst = p.nst;
+    a.nbuf = p.nbuf;
+    a.out_fp32 = c.out_fp32;
+    a.vec = reinterpret_cast<uintptr_t>(c.out) % 16 == 0 && c.ldo % (c.out_fp32 ? 4 : 8) == 0;
+    a.flags = launch_flags();
+    const cudaError_t e = p.pair ? launch_one<true>(a, p.grid, st) : launch_one<false>(a, p.grid, st);
+    *err = e;
+    return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
+}
+
+int fp8_device_error(int clear) {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_ex_timeout, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && v) {
+        const int z = 0;
+        if (cudaMemcpyToSymbol(g_ex_timeout, &z, sizeof(int)) != cudaSuccess) return -1;
+    }
+    return v;
+}
+
+}  // namespace mr

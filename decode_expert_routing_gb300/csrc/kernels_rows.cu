@@ -1,0 +1,287 @@
+// Rows between the tokens and the sorted positions of their assignments, with
+// the weights applied on the way back, and the gradients of both.
+//
+//   mr_moe_permute        rows[p] = x[f / topk]                  f = sorted[p]
+//   mr_moe_permute_grad   gx[m]   = sum_j grows[pos[m, j]]
+//   mr_moe_combine        out[m]  = add[m] + sum_j w[m, j] y[pos[m, j]]
+//   mr_moe_combine_grad   gy[p]   = w[f] gout[f / topk],  gw[f] = <gout[f / topk], y[p]>
+//
+// The first and the last go by the position (one row is written for each),
+// the others by the token: no row has two writers, there are no atomics, and
+// every sum has one order.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "rows_plan.h"
+
+namespace mr {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+
+template <int BYTES>
+struct Vec;
+template <>
+struct Vec<16> { using T = uint4; };
+template <>
+struct Vec<8> { using T = uint2; };
+template <>
+struct Vec<4> { using T = uint32_t; };
+template <>
+struct Vec<2> { using T = uint16_t; };
+template <>
+struct Vec<1> { using T = uint8_t; };
+
+// N elements of one vector load as fp32, and back with one rounding.
+template <int TYPE, int BYTES>
+struct Elems {
+    static constexpr int N = BYTES / (TYPE == kRowFp32 ? 4 : 2);
+    using V = typename Vec<BYTES>::T;
+    static __device__ __forceinline__ void get(const V& v, float (&f)[N]) {
+        if constexpr (TYPE == kRowFp32) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = __uint_as_float(w[i]);
+        } else {
+            const uint16_t* w = reinterpret_cast<const uint16_t*>(&v);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                f[i] = TYPE == kRowBf16 ? __uint_as_float((uint32_t)w[i] << 16) : __half2float(__ushort_as_half(w[i]));
+        }
+    }
+    static __device__ __forceinline__ V put(const float (&f)[N]) {
+        V v;
+        if constexpr (TYPE == kRowFp32) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __float_as_uint(f[i]);
+        } else if constexpr (N == 1) {
+            uint16_t u;
+            if (TYPE == kRowBf16) asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(f[0]));
+            else u = __half_as_ushort(__float2half_rn(f[0]));
+            v = u;
+        } else {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (TYPE == kRowBf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+                else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+            }
+        }
+        return v;
+    }
+};
+
+// ------------------------------------------------------------------ to the experts
+
+// lanes threads to a row, kRowThreads / lanes rows to a CTA.  MODE 0: rows as
+// they are (any type); 1: weighted, with the weights' gradients.  Padding
+// positions give rows of zeros; those behind *npost are left as they are.
+template <int MODE, int TYPE, int BYTES>
+__global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExpertsArgs a, int lanes, int64_t row_vecs) {
+    using V = typename Vec<BYTES>::T;
+    __shared__ float s_dot[kRowThreads / 32];
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid % lanes, mk = a.M * a.topk;
+    const int64_t i0 = (int64_t)blockIdx.x * kRowThreads + tid;
+    // assignments that the sort left out
+    if (MODE == 0 && a.positions != nullptr && i0 < mk && (unsigned)a.ids[i0] >= (unsigned)a.E) a.positions[i0] = -1;
+    if (MODE == 1 && i0 < mk && (uint64_t)(int64_t)a.known[i0] >= (uint64_t)a.cap) a.grad_w[i0] = 0.0f;
+    const int64_t p = (int64_t)blockIdx.x * (kRowThreads / lanes) + tid / lanes;
+    const bool row = p < a.cap && p < *a.npost;
+    const int f = row ? a.sorted[p] : -1;
+    const bool real = (unsigned)f < (unsigned)mk;
+    if (row && !real) {
+        const V z{};
+        V* out = static_cast<V*>(a.out) + p * row_vecs;
+        for (int64_t c = lane; c < row_vecs; c += lanes) out[c] = z;
+    }
+    float dot = 0.0f;
+    if (real) {
+        const int m = f / a.topk;
+        V* out = static_cast<V*>(a.out) + p * row_vecs;
+        const V* x = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.x) + (int64_t)m * a.ldx);
+        if constexpr (MODE == 0) {
+            if (a.positions != nullptr && lane == 0) a.positions[f] = (int32_t)p;
+#pragma unroll 4
+            for (int64_t c = lane; c < row_vecs; c += lanes) out[c] = __ldg(x + c);
+        } else {
+            using E = Elems<TYPE, BYTES>;
+            const float w = a.weights == nullptr ? 1.0f : __ldg(a.weights + f);
+            const V* y = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + p * a.ldy);
+#pragma unroll 4
+            for (int64_t c = lane; c < row_vecs; c += lanes) {
+                const V gv = __ldg(x + c), yv = y[c];  // (out may be y itself)
+                float g[E::N], u[E::N];
+                E::get(gv, g);
+                E::get(yv, u);
+#pragma unroll
+                for (int i = 0; i < E::N; ++i) {
+                    dot = __fmaf_rn(g[i], u[i], dot);
+                    g[i] = __fmul_rn(w, g[i]);
+                }
+                out[c] = E::put(g);
+            }
+        }
+    }
+    if constexpr (MODE == 1) {
+        dot = warp_sum_fixed(dot);
+        const int warps = lanes / 32, warp = tid >> 5;
+        if ((tid & 31) == 0) s_dot[warp] = dot;
+        __syncthreads();
+        if (real && lane == 0) {
+            float s = 0.0f;
+            for (int i = 0; i < warps; ++i) s = __fadd_rn(s, s_dot[warp + i]);
+            a.grad_w[f] = s;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ back to the tokens
+
+// A thread takes N elements of a token's row; the rows of up to eight slots
+// are in flight at a time.  The sum goes over the slots in ascending order in
+// fp32, from add (or zero), and is rounded once.
+constexpr int kTokenThreads = 128;
+template <int TYPE, int BYTES>
+__global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokensArgs a, int row_vecs, int64_t total) {
+    using E = Elems<TYPE, BYTES>;
+    using V = typename Vec<BYTES>::T;
+    pdl_trigger();
+    pdl_wait();
+    for (int64_t i = (int64_t)blockIdx.x * kTokenThreads + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * kTokenThreads) {
+        const int64_t m = i / row_vecs;
+        const int c = (int)(i - m * row_vecs);
+        float s[E::N];
+#pragma unroll
+        for (int u = 0; u < E::N; ++u) s[u] = 0.0f;
+        if (a.add != nullptr)
+            // (a plain load: out may be add itself)
+            E::get(*(reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.add) + m * a.ldadd) + c), s);
+        for (int j0 = 0; j0 < a.topk; j0 += 8) {
+            V v[8];
+            int p[8];
+            float w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                p[u] = -1;
+                w[u] = 1.0f;
+                if (j0 + u >= a.topk) continue;
+                p[u] = __ldg(a.positions + m * a.topk + j0 + u);
+                if (a.weights != nullptr) w[u] = __ldg(a.weights + m * a.topk + j0 + u);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if ((uint64_t)(int64_t)p[u] >= (uint64_t)a.cap) continue;
+                v[u] = __ldg(reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + (int64_t)p[u] * a.ldy) + c);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if ((uint64_t)(int64_t)p[u] >= (uint64_t)a.cap) continue;
+                float f[E::N];
+                E::get(v[u], f);
+#pragma unroll
+                for (int q = 0; q < E::N; ++q) s[q] = __fmaf_rn(w[u], f[q], s[q]);
+            }
+        }
+        reinterpret_cast<V*>(a.out)[i] = E::put(s);
+    }
+}
+
+int vec_bytes(uintptr_t bits, int elem) {
+    for (int v = 16; v > elem; v >>= 1)
+        if ((bits & (uintptr_t)(v - 1)) == 0) return v;
+    return elem;
+}
+
+int device_sms(int* sms) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? (int)e : (int)cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+template <int MODE, int TYPE, int BYTES>
+cudaError_t launch_experts_v(const ToExpertsArgs& a, cudaStream_t st) {
+    const int64_t vecs = (int64_t)a.K * row_elem_bytes(a.type) / BYTES;
+    int lanes = 32;
+    while (lanes < kRowThreads && lanes < vecs) lanes *= 2;
+    const int64_t per = kRowThreads / lanes, mk = (int64_t)a.M * a.topk;
+    int64_t ctas = (a.cap + per - 1) / per;
+    if (ctas * kRowThreads < mk) ctas = (mk + kRowThreads - 1) / kRowThreads;  // (a thread for each assignment)
+    return launch_overlapped(to_experts_kernel<MODE, TYPE, BYTES>, dim3((unsigned)ctas), dim3(kRowThreads), 0, st, a,
+                             lanes, vecs);
+}
+
+template <int TYPE, int BYTES>
+cudaError_t launch_tokens_v(const ToTokensArgs& a, cudaStream_t st) {
+    int sms = 0;
+    const int e = device_sms(&sms);
+    if (e != 0) return (cudaError_t)e;
+    const int vecs = (int)((int64_t)a.K * row_elem_bytes(a.type) / BYTES);
+    const int64_t total = (int64_t)a.M * vecs;
+    int64_t ctas = (total + kTokenThreads - 1) / kTokenThreads;
+    if (ctas > (int64_t)sms * 16) ctas = (int64_t)sms * 16;
+    return launch_overlapped(to_tokens_kernel<TYPE, BYTES>, dim3((unsigned)ctas), dim3(kTokenThreads), 0, st, a, vecs,
+                             total);
+}
+
+}  // namespace
+
+cudaError_t launch_to_experts(const ToExpertsArgs& a0, cudaStream_t st) {
+    ToExpertsArgs a = a0;
+    const int eb = row_elem_bytes(a.type);
+    a.ldx *= eb;  // bytes from here on
+    a.ldy *= eb;
+    uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.ldx |
+                     (uintptr_t)((int64_t)a.K * eb);
+    if (a.y != nullptr) bits |= reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)a.ldy;
+    const int v = vec_bytes(bits, eb);
+    if (a.grad_w == nullptr) {
+        switch (v) {
+            case 16: return launch_experts_v<0, kRowU8, 16>(a, st);
+            case 8: return launch_experts_v<0, kRowU8, 8>(a, st);
+            case 4: return launch_experts_v<0, kRowU8, 4>(a, st);
+            case 2: return launch_experts_v<0, kRowU8, 2>(a, st);
+            default: return launch_experts_v<0, kRowU8, 1>(a, st);
+        }
+    }
+#define MR_EXPERTS(T)                                              \
+    switch (v) {                                                   \
+        case 16: return launch_experts_v<1, T, 16>(a, st);         \
+        case 8: return launch_experts_v<1, T, 8>(a, st);           \
+        case 4: return launch_experts_v<1, T, 4>(a, st);           \
+        default: return launch_experts_v<1, T, T == kRowFp32 ? 4 : 2>(a, st); \
+    }
+    if (a.type == kRowBf16) MR_EXPERTS(kRowBf16)
+    if (a.type == kRowFp16) MR_EXPERTS(kRowFp16)
+    MR_EXPERTS(kRowFp32)
+#undef MR_EXPERTS
+}
+
+cudaError_t launch_to_tokens(const ToTokensArgs& a0, cudaStream_t st) {
+    ToTokensArgs a = a0;
+    const int eb = row_elem_bytes(a.type);
+    a.ldy *= eb;
+    a.ldadd *= eb;
+    uintptr_t bits = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.ldy |
+                     (uintptr_t)((int64_t)a.K * eb);
+    if (a.add != nullptr) bits |= reinterpret_cast<uintptr_t>(a.add) | (uintptr_t)a.ldadd;
+    const int v = vec_bytes(bits, eb);
+#define MR_TOKENS(T)                                               \
+    switch (v) {                                                   \
+        case 16: return launch_tokens_v<T, 16>(a, st);             \
+        case 8: return launch_tokens_v<T, 8>(a, st);               \
+        case 4: return launch_tokens_v<T, 4>(a, st);               \
+        default: return launch_tokens_v<T, T == kRowFp32 ? 4 : 2>(a, st); \
+    }
+    if (a.type == kRowBf16) MR_TOKENS(kRowBf16)
+    if (a.type == kRowFp16) MR_TOKENS(kRowFp16)
+    MR_TOKENS(kRowFp32)
+#undef MR_TOKENS
+}
+
+}  // namespace mr

@@ -1,0 +1,28 @@
+// Host-side plan and launchers of the residual norm and the FP8 quantiser.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mr {
+
+constexpr int kNormMaxK = 65536;  // 1024 threads x 8 chunks of 8 elements
+
+struct NormArgs {
+    const uint16_t *x, *residual, *g;
+    uint16_t *sres, *xn;
+    float* rstd;
+    uint8_t* q;
+    void* scale;
+    int64_t ldx, ldr, lds;
+    int M, K, gemma, fmt;  // fmt: 0 none, 1 MXFP8, 2 MXFP4, 3 FP8 with scales per 128
+    float eps;
+};
+
+// Chunks of 8 elements that a thread holds, of rows of vpr chunks.
+inline int norm_chunks(int vpr) { return vpr <= 1024 ? 1 : vpr <= 2048 ? 2 : vpr <= 4096 ? 4 : 8; }
+
+cudaError_t launch_add_norm(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_fp8_quant(const void* x, int64_t ldx, int M, int K, uint8_t* q, float* scale, cudaStream_t st);
+
+}  // namespace mr

@@ -639,6 +639,181 @@ typedef struct mr_moe_down_params {
 } mr_moe_down_params;
 int mr_moe_down(const mr_moe_down_params *params, void *stream);
 
+/*
+ * The residual's addition and the RMSNorm behind it: what the route on the
+ * norm's scale (mr_route_params.rstd) and the products of 8-bit rows read.
+ *   sres[m, k] = bf16(x[m, k] + residual[m, k])       (residual NULL: x itself)
+ *   rstd[m]    = 1 / sqrt(mean_k(sres[m, k]^2) + eps)
+ *   xn[m, k]   = bf16((sres[m, k] * rstd[m]) * s[k])  (s and both products as
+ *                                                      mr_norm_apply has them)
+ *   q, scale   = xn in 8 or 4 bits: MR_QUANT_MXFP8 / MR_QUANT_MXFP4 as
+ *                mr_mxfp8_quant / mr_mxfp4_quant, MR_QUANT_FP8 as mr_fp8_quant
+ *                of the bf16 rows, bit for bit.
+ * The sum of squares is kept with its rounding errors and rstd is the
+ * formula's value rounded to nearest but for about one row in 10^5, so it
+ * depends on no order of summation.  Squares beyond fp32 (|sres| above 1.8e19)
+ * make rstd 0, a NaN or an infinity in a row makes the row NaN (an infinity:
+ * rstd 0, itself NaN and the others 0).
+ * x, residual: bf16 with row strides ldx, ldr in elements; norm_weight: bf16
+ * [K]; eps >= 0, finite.  Outputs, each optional (NULL) but one at least: sres
+ * bf16 with row stride lds (it may be x or residual itself, with that one's
+ * stride; it may not overlap them otherwise), rstd fp32 [M], xn bf16 [M, K], q
+ * and scale (both, with a quant_format; else both NULL).  bf16 pointers 16-byte
+ * aligned and strides multiples of 8; q 8-byte aligned, for MR_QUANT_FP8 scale
+ * 4-byte aligned.  K % 8 == 0 (MXFP8, MXFP4: % 32; MR_QUANT_FP8: % 16) and K <=
+ * 65536, else MR_ERR_UNSUPPORTED.  Any M >= 1.  One launch.
+ */
+#define MR_QUANT_FP8 3 /* E4M3 codes [M, K], fp32 scales [M, ceil(K / 128)]: mr_add_rms_norm only */
+typedef struct mr_add_rms_norm_params {
+    const void *x;
+    int64_t ldx;
+    const void *residual;
+    int64_t ldr;
+    const void *norm_weight;
+    int norm_kind;               /* MR_NORM_* */
+    float eps;
+    int M, K, quant_format;      /* MR_QUANT_NONE, _MXFP8, _MXFP4 or _FP8 */
+    void *sres;
+    int64_t lds;
+    float *rstd;
+    void *xn;
+    uint8_t *q;
+    void *scale;
+} mr_add_rms_norm_params;
+int mr_add_rms_norm(const mr_add_rms_norm_params *params, void *stream);
+
+/*
+ * E4M3 codes with one fp32 scale for every 128 elements of a row (the last
+ * group may be shorter):
+ *   scale[m, b] = max(amax / 448, 2^-126),  amax = the group's largest |x|
+ *   q[m, k]     = e4m3(x[m, k] * (1 / scale[m, k / 128]))
+ * each fp32 step and the codes rounded to nearest even, the codes saturating
+ * at 448.  A NaN or an infinity in a group makes what is read back of it (code
+ * times scale) NaN.  x: bf16 [M, ldx]; q: [M, K], 8-byte aligned; scale: fp32
+ * [M, ceil(K / 128)].  K % 16 == 0, else MR_ERR_UNSUPPORTED.  One launch.
+ */
+int mr_fp8_quant(const void *x, int64_t ldx, int M, int K, uint8_t *q, float *scale, void *stream);
+
+/*
+ * Product of E4M3 operands with fp32 scales, one for 128 elements of a row of
+ * x and one for 128 x 128 of w:
+ *   out[m, r] = sum_b x_scale[m, b] w_scale[r / 128, b] sum_{k in b} q[m, k] w[r, k]
+ * over the blocks b of 128 along K (the last of each kind may be shorter).
+ * The inner sums are those of the tensor core in fp32; the scaled sums are
+ * added in fp32 in ascending b, or, where the K range is shared between
+ * CTAs, ascending within each share and over the shares.
+ * q: [M, K] with row stride ldq in bytes; w: [R, K] with row stride ldw in
+ * bytes; both 16-byte aligned and their strides multiples of 16.  x_scale:
+ * fp32 [M, ceil(K / 128)] with row stride ldxs; w_scale: fp32 [ceil(R / 128),
+ * ceil(K / 128)] with row stride ldws.  out: bf16, or fp32 with out_fp32 != 0,
+ * row stride ldo in elements.  Any M, R, K >= 1 (K need not be a multiple of
+ * anything: bytes behind a row's K elements are not used).  One launch.
+ */
+typedef struct mr_fp8_gemm_params {
+    const uint8_t *q;
+    int64_t ldq;
+    const float *x_scale;
+    int64_t ldxs;
+    const uint8_t *w;
+    int64_t ldw;
+    const float *w_scale;
+    int64_t ldws;
+    int M, R, K;
+    void *out;
+    int64_t ldo;
+    int out_fp32;
+} mr_fp8_gemm_params;
+int mr_fp8_gemm(const mr_fp8_gemm_params *params, void *stream);
+
+/* Element types of the rows below. */
+typedef enum mr_row_type {
+    MR_ROW_BF16 = 0,
+    MR_ROW_FP16 = 1,
+    MR_ROW_FP32 = 2,
+    MR_ROW_U8 = 3                /* mr_moe_permute only: codes, scale bytes */
+} mr_row_type;
+
+/*
+ * Rows of tokens to the sorted positions of their assignments.  With f =
+ * sorted_token_ids[p], for every position p below num_tokens_post_padded[0]:
+ *   rows[p, k]   = x[f / topk, k]     (padding, f outside [0, M * topk): zeros)
+ *   positions[f] = p                  (f whose topk_ids[f] is outside [0, E): -1)
+ * Rows behind the last are left as they were.  x: row stride ldx in elements;
+ * topk_ids: the ids that were sorted, [M, topk]; rows: [capacity, K];
+ * positions: [M, topk].  sorted_token_ids: capacity entries, as mr_moe_sort or
+ * the route wrote them (each assignment at one position at most).  rows and
+ * positions overlap nothing that is read.  Any K >= 1 and alignment of the
+ * type (16-byte aligned rows are moved in 16-byte words).  topk <= 32, M *
+ * topk < 2^30, capacity < 2^31.  One launch.
+ */
+typedef struct mr_moe_permute_params {
+    const void *x;
+    int64_t ldx;
+    int row_type;                /* MR_ROW_* */
+    int M, K, topk, E;
+    const int32_t *topk_ids;
+    const int32_t *sorted_token_ids;
+    const int32_t *num_tokens_post_padded;
+    int64_t capacity;
+    void *rows;
+    int32_t *positions;
+} mr_moe_permute_params;
+int mr_moe_permute(const mr_moe_permute_params *params, void *stream);
+
+/*
+ * Rows at the sorted positions back to their tokens, weighted:
+ *   out[m, k] = add[m, k] + sum_j topk_weights[m, j] y[positions[m, j], k]
+ * summed in fp32 from add over ascending j and rounded once, so the result
+ * depends on nothing but the values.  Positions outside [0, capacity) add
+ * nothing; a token without any gives add, or zero.  topk_weights NULL: all
+ * one, which with add NULL is the gradient of mr_moe_permute (y the gradient
+ * of its rows).  y: [capacity, ldy] and add: [M, ldadd] (or NULL) of row_type
+ * (not MR_ROW_U8); out: [M, K], may be add itself when ldadd == K.
+ * Limits as mr_moe_permute.  One launch.
+ */
+typedef struct mr_moe_combine_params {
+    const void *y;
+    int64_t ldy;
+    int row_type;
+    int64_t capacity;
+    int M, K, topk;
+    const int32_t *positions;
+    const float *topk_weights;
+    const void *add;
+    int64_t ldadd;
+    void *out;
+} mr_moe_combine_params;
+int mr_moe_combine(const mr_moe_combine_params *params, void *stream);
+
+/*
+ * Gradients of mr_moe_combine for the gradient grad_out of its result (that
+ * of add is grad_out itself).  With f = sorted_token_ids[p], p below
+ * num_tokens_post_padded[0]:
+ *   grad_y[p, k]    = topk_weights[f] grad_out[f / topk, k]    (padding: zeros)
+ *   grad_weights[f] = sum_k grad_out[f / topk, k] y[p, k]      (fp32 sums)
+ * and grad_weights[f] = 0 where positions[f] is outside [0, capacity).  Rows
+ * of grad_y behind the last are left as they were.  topk_weights NULL: all
+ * one (grad_weights is written all the same).  grad_out: [M, ldg]; y:
+ * [capacity, ldy]; grad_y: [capacity, K], may be y itself when ldy == K;
+ * grad_weights: fp32 [M, topk].  Limits as mr_moe_permute.  One launch.
+ */
+typedef struct mr_moe_combine_grad_params {
+    const void *grad_out;
+    int64_t ldg;
+    const void *y;
+    int64_t ldy;
+    int row_type;
+    int64_t capacity;
+    int M, K, topk;
+    const int32_t *positions;
+    const float *topk_weights;
+    const int32_t *sorted_token_ids;
+    const int32_t *num_tokens_post_padded;
+    void *grad_y;
+    float *grad_weights;
+} mr_moe_combine_grad_params;
+int mr_moe_combine_grad(const mr_moe_combine_grad_params *params, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
