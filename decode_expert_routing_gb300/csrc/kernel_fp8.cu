@@ -7,13 +7,12 @@
 // read-back warps add its scaled value to sums that they keep in registers
 // while it computes the next one in another buffer.  Rows of x are the
 // accumulator's lanes and rows of w its columns, so a thread has one row of x
-// and its scale is one number: a block costs a column one fused multiply-add
-// (two columns an instruction), and one product a scale block.
+// and its scale is one number: a block costs a column one fused multiply-add.
 //
 // Work: persistent CTAs (or pairs of two with cta_group::2) walk the tiles of
 // 128 (256) rows of x times n rows of w, row tiles fastest.  Warp 0 copies
 // (tensor maps, 128-byte swizzle, a block of 128 bytes a row per stage), warp 1
-// issues the products, warps 2-9 read back.
+// issues the products, warps 2-3 prepare the scales, warps 4-15 read back.
 #include "../../include/moe_route.h"
 #include "fp8_plan.h"
 #include "internal.h"
@@ -22,8 +21,7 @@
 
 namespace mr {
 
-constexpr int kF8Threads = 320;
-constexpr int kF8Chunks = 8;  // of 16 columns, the most that a read-back thread keeps
+constexpr int kF8Threads = 512;
 
 struct Fp8Args {
     CUtensorMap tm_x, tm_w;  // boxes of xrows and n (pair: n / 2) rows x 128 bytes
@@ -40,46 +38,59 @@ namespace {
 __device__ __forceinline__ uint32_t f8_idesc(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+// What one lane of a warp issues (lead: 1 in that lane, 0 in the others) is
+// predicated in the instruction: in a branch of one lane the operands, which
+// these instructions take from uniform registers, are moved there one by one
+// (50 cycles a product).
 template <bool PAIR>
-__device__ __forceinline__ void f8_mma(uint32_t d, unsigned long long a, unsigned long long b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void f8_mma(uint32_t lead, uint32_t d, unsigned long long a, unsigned long long b,
+                                       uint32_t idesc, bool acc) {
     if (PAIR)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-            "r"((uint32_t)acc)
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"((uint32_t)acc), "r"(lead)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-            "r"((uint32_t)acc)
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"((uint32_t)acc), "r"(lead)
             : "memory");
 }
-__device__ __forceinline__ unsigned long long f8_pack(uint32_t lo, uint32_t hi) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
+template <bool PAIR>
+__device__ __forceinline__ void f8_commit(uint32_t lead, uint32_t bar) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::
+                "r"(bar),
+            "h"((unsigned short)3), "r"(lead)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
+            : "memory");
 }
-// acc += v * s on two fp32 numbers, each rounded once
-__device__ __forceinline__ void f8_fma2(unsigned long long& acc, unsigned long long v, unsigned long long s) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+__device__ __forceinline__ void f8_expect(uint32_t lead, uint32_t bar, unsigned bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(lead)
+        : "memory");
 }
-__device__ __forceinline__ float2 f8_unpack(unsigned long long v) {
-    uint32_t lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+__device__ __forceinline__ void f8_load(uint32_t lead, uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::
+            "r"(dst),
+        "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(y), "r"(bar), "r"(lead)
+        : "memory");
 }
-
 // 16 columns (32 bytes of bf16 or 64 of fp32) of one row
-__device__ __forceinline__ void f8_store(const Fp8Args& a, int64_t m, int col, const unsigned long long* acc) {
+__device__ __forceinline__ void f8_store(const Fp8Args& a, int64_t m, int col, const float (&f)[16]) {
     const int left = a.R - col;
     if (left <= 0) return;
-    float f[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 t = f8_unpack(acc[i]);
-        f[2 * i] = t.x, f[2 * i + 1] = t.y;
-    }
     if (a.out_fp32) {
         float* o = static_cast<float*>(a.out) + m * a.ldo + col;
         if (a.vec && left >= 16) {
@@ -107,10 +118,14 @@ __device__ __forceinline__ void f8_store(const Fp8Args& a, int64_t m, int col, c
     }
 }
 
-template <bool PAIR>
+// D: blocks of a stage and of a buffer (those behind K are zeros); MC: chunks
+// of 16 columns that a read-back warp takes, a third of them rounded up.
+template <bool PAIR, int D, int MC>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Args a) {
     extern __shared__ __align__(16) unsigned char dsm[];
-    __shared__ __align__(8) unsigned long long s_full[kF8MaxStages], s_empty[kF8MaxStages], s_tfull[8], s_tempty[8], s_drain;
+    __shared__ __align__(8) unsigned long long s_full[kF8MaxStages], s_empty[kF8MaxStages], s_tfull[8], s_tempty[8], s_mfree[8], s_drain;
+    // of the blocks in the accumulator buffers: a row's scale times that of each block of w's rows in the tile
+    __shared__ float s_scale[8][3][128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
@@ -121,8 +136,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         mbar_init(full0 + 8u * tid, PAIR && rank == 0 ? 2 : 1);  // (one from the peer)
         mbar_init(empty0 + 8u * tid, 1);
         if (tid < 8) {
-            mbar_init(tfull0 + 8u * tid, 1);
-            mbar_init(tempty0 + 8u * tid, PAIR ? 16 : 8);
+            mbar_init(tfull0 + 8u * tid, 3);  // the products, and two warps' scales
+            mbar_init(tempty0 + 8u * tid, 12);
+            mbar_init(smem_u32(&s_mfree[tid]), 24);  // (pair) both CTAs' buffers are free
         }
         if (tid == 8) mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -153,13 +169,19 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     constexpr int of = PAIR ? 2 : 1;
     const uint32_t tmem = __shfl_sync(kFull, s_tmem, 0);
     const uint32_t base = (smem_u32(dsm) + 1023u) & ~1023u;
-    const uint32_t wbytes = (uint32_t)(a.n / of) * 128u, stage_bytes = wbytes + (uint32_t)a.xrows * 128u;
+    // a stage: D blocks, each n (pair: n / 2) rows of w and xrows of x
+    const uint32_t wbytes = (uint32_t)(a.n / of) * 128u, block_bytes = wbytes + (uint32_t)a.xrows * 128u;
+    const uint32_t stage_bytes = D * block_bytes;
     int st = 0;       // stage of the ring
     unsigned ph = 0;  // its phase
     int buf = 0;      // accumulator buffer
     unsigned bph = 0;
     const int64_t step = gridDim.x / of;
+    const uint32_t lead = ex_elect() ? 1u : 0u;  // (whole warps up to here)
 
+    // registers of the warps that copy and issue for those that keep sums: 128 x 56 + 384 x 152 of the 512 x 128
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
         // ---- copies
         int issued = 0;
@@ -167,18 +189,18 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
             const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT);
             const int m0 = (rt * of + rank) * 128, w0 = ct * a.n + rank * (a.n / of);
-            for (int ki = 0; ki < a.KI; ++ki) {
-                if (!ex_wait(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
+            for (int ki = 0; ki < a.KI; ki += D) {
+                if (!ex_wait_cta(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
                 }
-                if (ex_elect()) {
-                    const uint32_t full = full0 + 8u * st, at = base + (uint32_t)st * stage_bytes;
-                    mbar_expect_tx(full, stage_bytes + (((a.flags & 2) && issued == 0) ? 16u : 0u));
-                    tma_load_2d(at, &a.tm_w, ki * 128, w0, full);
-                    tma_load_2d(at + wbytes, &a.tm_x, ki * 128, m0, full);
+                const uint32_t full = full0 + 8u * st, at = base + (uint32_t)st * stage_bytes;
+                f8_expect(lead, full, stage_bytes + (((a.flags & 2) && issued == 0) ? 16u : 0u));
+#pragma unroll
+                for (int b = 0; b < D; ++b) {
+                    f8_load(lead, at + b * block_bytes, &a.tm_w, (ki + b) * 128, w0, full);
+                    f8_load(lead, at + b * block_bytes + wbytes, &a.tm_x, (ki + b) * 128, m0, full);
                 }
-                __syncwarp();
                 ++issued;
                 if (++st == a.nst) st = 0, ph ^= 1u;
             }
@@ -197,8 +219,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         bool ok = true;
         const uint32_t peer = map_rank(full0, 0);
         for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
-            for (int ki = 0; ki < a.KI; ++ki) {
-                if (!ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
+            for (int ki = 0; ki < a.KI; ki += D) {
+                if (!ex_wait_cta(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
                 }
@@ -208,84 +230,143 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             }
         }
     } else if (warp == 1) {
-        // ---- products, a block into each buffer in turn
+        // ---- products, a stage's blocks side by side into each buffer in turn
         bool ok = true;
-        const uint32_t idesc = f8_idesc(128 * of, a.n);
+        const uint32_t idesc = f8_idesc(128 * of, a.n), mfree0 = PAIR ? smem_u32(&s_mfree[0]) : tempty0;
         for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
-            for (int ki = 0; ki < a.KI; ++ki) {
-                if (!ex_wait(tempty0 + 8u * buf, bph ^ 1u, a.wait_ns, &s_abort) ||
-                    !ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
+            for (int ki = 0; ki < a.KI; ki += D) {
+                // (a pair's stage is in the peer's memory too.  The buffer last: it is the one that is waited for)
+                if (!(PAIR ? ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)
+                           : ex_wait_cta(full0 + 8u * st, ph, a.wait_ns, &s_abort)) ||
+                    !ex_wait_cta(mfree0 + 8u * buf, bph ^ 1u, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (ex_elect()) {
-                    const uint32_t at = base + (uint32_t)st * stage_bytes, d = tmem + (uint32_t)(buf * a.n);
-                    const unsigned long long dw = ex_desc(kExDescCodes, at), dx = ex_desc(kExDescCodes, at + wbytes);
+                const uint32_t at = base + (uint32_t)st * stage_bytes, d = tmem + (uint32_t)(buf * D * a.n);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) f8_mma<PAIR>(d, dx + 2 * j, dw + 2 * j, idesc, j > 0);
-                    ex_commit<PAIR>(empty0 + 8u * st);
-                    ex_commit<PAIR>(tfull0 + 8u * buf);
+                for (int b = 0; b < D; ++b) {
+                    const unsigned long long dw = ex_desc(kExDescCodes, at + b * block_bytes);
+                    const unsigned long long dx = ex_desc(kExDescCodes, at + b * block_bytes + wbytes);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        f8_mma<PAIR>(lead, d + (uint32_t)(b * a.n), dx + 2 * j, dw + 2 * j, idesc, j > 0);
                 }
-                __syncwarp();
+                f8_commit<PAIR>(lead, empty0 + 8u * st);
+                f8_commit<PAIR>(lead, tfull0 + 8u * buf);
                 if (++st == a.nst) st = 0, ph ^= 1u;
                 if (++buf == a.nbuf) buf = 0, bph ^= 1u;
             }
         }
     } else {
-        // ---- scaled sums: warps 2-5 take the first half of the columns, warps 6-9 the second
-        const int wq = warp & 3, grp = (warp - 2) >> 2, nch = a.n >> 4, half = (nch + 1) >> 1;
-        const int c0 = grp * half, mine = grp ? nch - half : half;  // chunks of 16 columns
-        const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-        const uint32_t tempty = PAIR ? map_rank(tempty0, 0) : tempty0;
+        // ---- scales, a stage's at a time into the slots of the accumulator buffer: each warp those of 64 rows, a lane
+        // two of them
+        const int last = (a.R - 1) >> 7, row = (warp - 2) * 64 + lane;
+        bool ok = true;
+        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
+            const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT), bt = ct * a.n >> 7;
+            const int64_t m = (int64_t)(rt * of + rank) * 128 + row;
+            const float* xs[2] = {a.xs + min(m, (int64_t)a.M - 1) * a.ldxs, a.xs + min(m + 32, (int64_t)a.M - 1) * a.ldxs};
+            const float* ws[3];
+#pragma unroll
+            for (int j = 0; j < 3; ++j) ws[j] = a.ws + (int64_t)min(bt + j, last) * a.ldws;
+            float x[2][D], w[3][D];
+            auto fetch = [&](int ki) {
+#pragma unroll
+                for (int b = 0; b < D; ++b) {
+                    const int k = min(ki + b, a.KI - 1);  // (a block behind K is zeros, whatever its scale)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) x[i][b] = __ldg(xs[i] + k);
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) w[j][b] = __ldg(ws[j] + k);
+                }
+            };
+            fetch(0);
+            for (int ki = 0; ki < a.KI; ki += D) {
+                if (!ex_wait_cta(tempty0 + 8u * buf, bph ^ 1u, a.wait_ns, &s_abort)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int b = 0; b < D; ++b)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) s_scale[buf * D + b][j][row + 32 * i] = __fmul_rn(x[i][b], w[j][b]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tfull0 + 8u * buf);
+                if (++buf == a.nbuf) buf = 0, bph ^= 1u;
+                if (ki + D < a.KI) fetch(ki + D);
+            }
+        }
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        // ---- scaled sums: three groups of four warps, each a third of the columns
+        // (each takes MC chunks of 16 columns; where they are more than there are, the last ones twice, and stores
+        // its own: a read in a branch takes 130 cycles more)
+        const int wq = warp & 3, grp = (warp >> 2) - 1, nch = a.n >> 4;
+        const int c0 = min(grp * MC, nch - MC), own = grp * MC - c0;
+        const uint32_t lanes = (uint32_t)(wq * 32) << 16, mfree = PAIR ? map_rank(smem_u32(&s_mfree[0]), 0) : 0u;
         bool ok = true;
         for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
             const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT);
             const int64_t m = (int64_t)(rt * of + rank) * 128 + wq * 32 + lane;
             const int col0 = ct * a.n + c0 * 16;
-            // the scale block of the first columns, and the chunk from which on it is the next one
-            const int b0 = col0 >> 7, b1 = min(b0 + 1, (a.R - 1) >> 7), turn = 8 - ((col0 >> 4) & 7);
-            const float* xs = a.xs + (m < a.M ? m : a.M - 1) * a.ldxs;
-            const float* w0 = a.ws + (int64_t)min(b0, (a.R - 1) >> 7) * a.ldws;
-            const float* w1 = a.ws + (int64_t)b1 * a.ldws;
-            unsigned long long acc[kF8Chunks][8];
+            // the scale block of the first columns in the tile, and the chunk from which on it is the next one
+            const int j0 = (col0 >> 7) - (ct * a.n >> 7), j1 = min(j0 + 1, 2), turn = 8 - ((col0 >> 4) & 7);
+            const float *p0 = &s_scale[0][j0][wq * 32 + lane], *p1 = &s_scale[0][j1][wq * 32 + lane];
+            float acc[MC][16];
 #pragma unroll
-            for (int c = 0; c < kF8Chunks; ++c)
+            for (int c = 0; c < MC; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[c][i] = 0ull;
-            float nx = __ldg(xs), n0 = __ldg(w0), n1 = __ldg(w1);
-            for (int ki = 0; ki < a.KI; ++ki) {
-                const uint32_t u0 = __float_as_uint(__fmul_rn(nx, n0)), u1 = __float_as_uint(__fmul_rn(nx, n1));
-                const unsigned long long s0 = f8_pack(u0, u0), s1 = f8_pack(u1, u1);
-                if (ki + 1 < a.KI) nx = __ldg(xs + ki + 1), n0 = __ldg(w0 + ki + 1), n1 = __ldg(w1 + ki + 1);
-                if (!ex_wait(tfull0 + 8u * buf, bph, a.wait_ns, &s_abort)) {
+                for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
+            for (int ki = 0; ki < a.KI; ki += D) {
+                if (!ex_wait_cta(tfull0 + 8u * buf, bph, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem + lanes + (uint32_t)(buf * a.n + c0 * 16);
+                const uint32_t d = tmem + lanes + (uint32_t)(buf * D * a.n + c0 * 16);
+                float s0[D], s1[D];
+                // up to four chunks on their way at a time
+                constexpr int N = D * MC;
 #pragma unroll
-                for (int c = 0; c < kF8Chunks; ++c) {
-                    if (c < mine) {
-                        uint32_t v[16];
-                        ex_ld16(v, d + 16u * c);
-                        const unsigned long long s = c < turn ? s0 : s1;
+                for (int i0 = 0; i0 < N; i0 += 4) {
+                    uint32_t v[4][16];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) f8_fma2(acc[c][i], f8_pack(v[2 * i], v[2 * i + 1]), s);
+                    for (int i = i0; i < i0 + 4 && i < N; ++i)
+                        ex_ld16_async(v[i - i0], d + (uint32_t)(i / MC * a.n) + 16u * (i % MC));
+                    if (i0 == 0) {
+#pragma unroll
+                        for (int b = 0; b < D; ++b) s0[b] = p0[(buf * D + b) * 384], s1[b] = p1[(buf * D + b) * 384];
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_remote(tempty + 8u * buf);
-                    else mbar_arrive(tempty + 8u * buf);
+                    ex_ld_wait();
+                    if (i0 + 4 >= N) {  // (the last ones are in registers)
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            // (relaxed: the accumulators were read, nothing written is passed on)
+                            if (PAIR) mbar_arrive_remote(mfree + 8u * buf);
+                            mbar_arrive(tempty0 + 8u * buf);
+                        }
+                    }
+#pragma unroll
+                    for (int i = i0; i < i0 + 4 && i < N; ++i) {
+                        const int b = i / MC, c = i % MC;
+                        ex_ld_tie(v[i - i0]);
+                        const float s = c < turn ? s0[b] : s1[b];
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            acc[c][q] = __fmaf_rn(__uint_as_float(v[i - i0][q]), s, acc[c][q]);
+                    }
                 }
                 if (++buf == a.nbuf) buf = 0, bph ^= 1u;
             }
             if (ok && m < a.M) {
 #pragma unroll
-                for (int c = 0; c < kF8Chunks; ++c)
-                    if (c < mine) f8_store(a, m, col0 + 16 * c, acc[c]);
+                for (int c = 0; c < MC; ++c)
+                    if (c >= own) f8_store(a, m, col0 + 16 * c, acc[c]);
             }
         }
     }
@@ -322,14 +403,14 @@ bool encode_rows(CUtensorMap* map, const void* ptr, int K, int64_t rows, int64_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool PAIR>
+template <bool PAIR, int D, int MC>
 cudaError_t launch_one(const Fp8Args& a, int grid, cudaStream_t st) {
     static int prepared[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    const auto kernel = fp8_gemm_kernel<PAIR>;
+    const auto kernel = fp8_gemm_kernel<PAIR, D, MC>;
     if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8Smem);
         if (e != cudaSuccess) return e;
@@ -350,6 +431,20 @@ cudaError_t launch_one(const Fp8Args& a, int grid, cudaStream_t st) {
     cfg.numAttrs = PAIR ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kernel, a);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_plan(const Fp8Plan& p, const Fp8Args& a, cudaStream_t st) {
+    switch ((p.pair ? 100 : 0) + p.D * 10 + p.mc) {
+        case 41: return launch_one<false, 4, 1>(a, p.grid, st);
+        case 42: return launch_one<false, 4, 2>(a, p.grid, st);
+        case 21: return launch_one<false, 2, 1>(a, p.grid, st);
+        case 22: return launch_one<false, 2, 2>(a, p.grid, st);
+        case 23: return launch_one<false, 2, 3>(a, p.grid, st);
+        case 13: return launch_one<false, 1, 3>(a, p.grid, st);
+        case 14: return launch_one<false, 1, 4>(a, p.grid, st);
+        case 113: return launch_one<true, 1, 3>(a, p.grid, st);
+        default: return launch_one<true, 1, 4>(a, p.grid, st);
+    }
 }
 
 }  // namespace
@@ -384,7 +479,7 @@ int launch_fp8_gemm(const Fp8GemmCall& c, cudaStream_t st, cudaError_t* err) {
     a.out_fp32 = c.out_fp32;
     a.vec = reinterpret_cast<uintptr_t>(c.out) % 16 == 0 && c.ldo % (c.out_fp32 ? 4 : 8) == 0;
     a.flags = launch_flags();
-    const cudaError_t e = p.pair ? launch_one<true>(a, p.grid, st) : launch_one<false>(a, p.grid, st);
+    const cudaError_t e = launch_plan(p, a, st);
     *err = e;
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }

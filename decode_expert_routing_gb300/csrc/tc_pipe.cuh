@@ -44,6 +44,36 @@ __device__ __forceinline__ bool ex_wait(uint32_t bar, unsigned parity, unsigned 
                                         volatile int* abort) {
     return __all_sync(kFull, mbar_try_wait(bar, parity)) || ex_wait_slow(bar, parity, limit_ns, abort);
 }
+// The same where nothing of another CTA's memory is used after the wait (the
+// arrivals are this CTA's copies, or products and accumulator reads, whose
+// order tcgen05's own fences keep): acquired at the scope of the CTA.  No call:
+// the caller may hold more registers than a call leaves.
+__device__ __forceinline__ bool mbar_test_cta(uint32_t bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool ex_wait_cta(uint32_t bar, unsigned parity, unsigned long long limit_ns,
+                                            volatile int* abort) {
+    auto done = [&] { return __all_sync(kFull, mbar_test_cta(bar, parity)); };
+    if (done()) return true;
+    const unsigned long long t0 = global_ns();
+    for (int i = 1;; ++i) {
+        if (done()) return true;
+        if ((i & 15) != 0) continue;
+        if (__any_sync(kFull, global_ns() - t0 >= limit_ns)) {
+            *abort = 1;
+            atomicExch(&g_ex_timeout, 1);
+        }
+        if (__any_sync(kFull, *abort != 0)) return false;
+    }
+}
 // One lane of a converged warp, always the same one.
 __device__ __forceinline__ bool ex_elect() {
     uint32_t p;
@@ -80,14 +110,24 @@ __device__ __forceinline__ void ex_cluster_meet() {
 __device__ __forceinline__ void ex_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// 16 accumulator columns of this warp's 32 lanes.
-__device__ __forceinline__ void ex_ld16(uint32_t (&v)[16], uint32_t addr) {
+// 16 accumulator columns of this warp's 32 lanes: the read is under way until
+// ex_ld_wait; ex_ld_tie keeps later uses of a read's registers behind it.
+__device__ __forceinline__ void ex_ld16_async(uint32_t (&v)[16], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
           "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void ex_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void ex_ld_tie(uint32_t (&v)[16]) {
+    asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
+}
+__device__ __forceinline__ void ex_ld16(uint32_t (&v)[16], uint32_t addr) {
+    ex_ld16_async(v, addr);
+    ex_ld_wait();
+    ex_ld_tie(v);
 }
 // Barrier id of threads threads (whole warps); true when ok holds in all of them.
 __device__ __forceinline__ bool ex_sync(int id, int threads, bool ok) {
