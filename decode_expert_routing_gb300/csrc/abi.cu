@@ -106,7 +106,8 @@ int mr_set_wait_limit_ns(uint64_t ns) {
 int mr_device_error(int clear) {
     const int v = mr::route_device_error(clear), t = mr::tc_gemv_device_error(clear);
     const int x = mr::expert_device_error(clear), f = mr::fp8_device_error(clear);
-    return (v < 0 || t < 0 || x < 0 || f < 0) ? MR_ERR_CUDA : (v || t || x || f) ? MR_ERR_TIMEOUT : MR_OK;
+    const int w = mr::fp8_few_device_error(clear);
+    return (v < 0 || t < 0 || x < 0 || f < 0 || w < 0) ? MR_ERR_CUDA : (v || t || x || f || w) ? MR_ERR_TIMEOUT : MR_OK;
 }
 
 #ifdef MR_TRACE

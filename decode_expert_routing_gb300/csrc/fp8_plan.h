@@ -1,6 +1,7 @@
 // Host-side plan of the FP8 product with scales per 128.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -47,6 +48,35 @@ inline Fp8Plan fp8_plan(int M, int R, int K, int sms) {
     p.grid = of * (int)(tiles < slots ? tiles : slots);
     return p;
 }
+
+// Few rows of x: CTAs of 16 A rows of w and 8 B rows of x, gx x gy of them, nst
+// stages a warp.
+constexpr int kF8FewStages = 8;
+constexpr int kF8FewSmem = 220 * 1024;
+struct Fp8FewPlan {
+    int A, B, gx, gy, nst, smem;
+};
+inline bool fp8_few(int M) { return M <= 16; }
+inline Fp8FewPlan fp8_few_plan(int M, int R, int K, int sms) {
+    Fp8FewPlan p{};
+    p.B = M <= 8 ? 1 : 2;
+    p.A = (R + 31) / 32 >= sms ? 2 : 1;
+    p.gx = (R + 16 * p.A - 1) / (16 * p.A);
+    p.gy = (M + 8 * p.B - 1) / (8 * p.B);
+    const int KI = (K + 127) / 128, stage = (16 * p.A + 8 * p.B) * 128, per = (KI + 7) / 8;
+    // two CTAs on an SM where there are more than SMs
+    p.nst = ((int64_t)p.gx * p.gy > sms ? 110 * 1024 : kF8FewSmem - 1024) / (8 * stage);
+    if (p.nst > kF8FewStages) p.nst = kF8FewStages;
+    if (p.nst > per) p.nst = per;
+    const int ring = 8 * p.nst * stage, sums = 8 * 8 * p.B * (16 * p.A + 1) * 4;
+    p.smem = (ring > sums ? ring : sums) + 1024;
+    return p;
+}
+int launch_fp8_few(const Fp8GemmCall& c, int sms, cudaStream_t st, cudaError_t* err);
+int fp8_few_device_error(int clear);
+
+// Rows of K bytes, boxes of box_rows x 128 bytes in the 128-byte swizzle; behind K and the last row zeros are read.
+bool fp8_encode(CUtensorMap* map, const void* ptr, int K, int64_t rows, int64_t ld, int box_rows);
 
 int launch_fp8_gemm(const Fp8GemmCall& c, cudaStream_t st, cudaError_t* err);
 int fp8_device_error(int clear);

@@ -38,10 +38,6 @@ namespace {
 __device__ __forceinline__ uint32_t f8_idesc(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-// What one lane of a warp issues (lead: 1 in that lane, 0 in the others) is
-// predicated in the instruction: in a branch of one lane the operands, which
-// these instructions take from uniform registers, are moved there one by one
-// (50 cycles a product).
 template <bool PAIR>
 __device__ __forceinline__ void f8_mma(uint32_t lead, uint32_t d, unsigned long long a, unsigned long long b,
                                        uint32_t idesc, bool acc) {
@@ -72,20 +68,6 @@ __device__ __forceinline__ void f8_commit(uint32_t lead, uint32_t bar) {
             "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
             "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
             : "memory");
-}
-__device__ __forceinline__ void f8_expect(uint32_t lead, uint32_t bar, unsigned bytes) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(lead)
-        : "memory");
-}
-__device__ __forceinline__ void f8_load(uint32_t lead, uint32_t dst, const void* map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::
-            "r"(dst),
-        "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(y), "r"(bar), "r"(lead)
-        : "memory");
 }
 // 16 columns (32 bytes of bf16 or 64 of fp32) of one row
 __device__ __forceinline__ void f8_store(const Fp8Args& a, int64_t m, int col, const float (&f)[16]) {
@@ -195,11 +177,11 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                     break;
                 }
                 const uint32_t full = full0 + 8u * st, at = base + (uint32_t)st * stage_bytes;
-                f8_expect(lead, full, stage_bytes + (((a.flags & 2) && issued == 0) ? 16u : 0u));
+                ex_expect(lead, full, stage_bytes + (((a.flags & 2) && issued == 0) ? 16u : 0u));
 #pragma unroll
                 for (int b = 0; b < D; ++b) {
-                    f8_load(lead, at + b * block_bytes, &a.tm_w, (ki + b) * 128, w0, full);
-                    f8_load(lead, at + b * block_bytes + wbytes, &a.tm_x, (ki + b) * 128, m0, full);
+                    ex_load_2d(lead, at + b * block_bytes, &a.tm_w, (ki + b) * 128, w0, full);
+                    ex_load_2d(lead, at + b * block_bytes + wbytes, &a.tm_x, (ki + b) * 128, m0, full);
                 }
                 ++issued;
                 if (++st == a.nst) st = 0, ph ^= 1u;
@@ -393,16 +375,6 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     }
 }
 
-bool encode_rows(CUtensorMap* map, const void* ptr, int K, int64_t rows, int64_t ld, int box_rows) {
-    const EncodeTiled fn = encode_tiled();
-    if (fn == nullptr) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
-    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool PAIR, int D, int MC>
 cudaError_t launch_one(const Fp8Args& a, int grid, cudaStream_t st) {
     static int prepared[64];
@@ -449,16 +421,26 @@ cudaError_t launch_plan(const Fp8Plan& p, const Fp8Args& a, cudaStream_t st) {
 
 }  // namespace
 
+bool fp8_encode(CUtensorMap* map, const void* ptr, int K, int64_t rows, int64_t ld, int box_rows) {
+    const EncodeTiled fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int launch_fp8_gemm(const Fp8GemmCall& c, cudaStream_t st, cudaError_t* err) {
     int dev = 0, sms = 0;
     if ((*err = cudaGetDevice(&dev)) != cudaSuccess ||
         (*err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return MR_ERR_CUDA;
+    if (fp8_few(c.M)) return launch_fp8_few(c, sms, st, err);
     const Fp8Plan p = fp8_plan(c.M, c.R, c.K, sms);
     Fp8Args a{};
-    // (a row's stride matters only where there is another one)
-    if (!encode_rows(&a.tm_x, c.x, c.K, c.M, c.ldx, p.xrows) ||
-        !encode_rows(&a.tm_w, c.w, c.K, c.R, c.ldw, p.n / (p.pair ? 2 : 1)))
+    if (!fp8_encode(&a.tm_x, c.x, c.K, c.M, c.ldx, p.xrows) ||
+        !fp8_encode(&a.tm_w, c.w, c.K, c.R, c.ldw, p.n / (p.pair ? 2 : 1)))
         return MR_ERR_UNSUPPORTED;
     a.xs = c.xs;
     a.ws = c.ws;

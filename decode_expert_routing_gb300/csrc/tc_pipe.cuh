@@ -142,4 +142,23 @@ __device__ __forceinline__ bool ex_sync(int id, int threads, bool ok) {
     return r != 0;
 }
 
+// What one lane of a warp issues (lead: 1 in that lane, 0 in the others) is
+// predicated in the instruction: in a branch of one lane the operands, which
+// these instructions take from uniform registers, are moved there one by one
+// (50 cycles a product).
+__device__ __forceinline__ void ex_expect(uint32_t lead, uint32_t bar, unsigned bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void ex_load_2d(uint32_t lead, uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::
+            "r"(dst),
+        "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(y), "r"(bar), "r"(lead)
+        : "memory");
+}
+
 }  // namespace mr

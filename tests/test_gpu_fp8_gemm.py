@@ -170,7 +170,7 @@ def test_a_wait_that_runs_out(mr):
     the next call is right."""
     mr.set_wait_limit_ns(2_000_000)
     try:
-        for M, R, K in ((3, 500, 512), (700, 6144, 512)):
+        for M, R, K in ((3, 500, 512), (200, 500, 512), (700, 6144, 512)):
             a = operands(M, R, K)
             mr.set_launch_flags(mr.LAUNCH_TEST_STALL)
             mr.fp8_gemm(*a)
