@@ -18,34 +18,68 @@ struct Fp8GemmCall {
 constexpr int kF8Smem = 208 * 1024;  // dynamic shared memory of a CTA
 constexpr int kF8MaxStages = 24;
 
-// Tiles: rows of x are the accumulator's lanes (128 a CTA, 256 a pair), n
-// rows of w its columns.
+// Tiles: rows of x are the accumulator's lanes (128 a CTA, of up to 64 rows 64;
+// 256 a pair), n rows of w its columns.  slices > 1: CTAs of a cluster share
+// a tile's blocks of K, slice_len each; every cluster has one tile.
 struct Fp8Plan {
     int pair, n, xrows, RT, CT, D, mc, nst, nbuf, grid;  // mc: chunks of 16 columns of a read-back warp
+    int slices, slice_len;
 };
+inline int fp8_room(int xrows) { return kF8Smem - 1024 - (128 - xrows) * 128; }  // for stages
+// Blocks of a stage: as many as leave two buffers of accumulators and four stages.
+inline int fp8_depth(bool pair, int xrows, int n) {
+    const int block = (xrows + n) * 128, room = fp8_room(xrows);
+    return pair ? 1 : n <= 64 && room / (4 * block) >= 4 ? 4 : n <= 128 && room / (2 * block) >= 4 ? 2 : 1;
+}
+inline int fp8_chunks(int n, int D) {  // of 16 columns, of a read-back warp (three groups)
+    const int mc = (n / 16 + 2) / 3;
+    return D == 1 && mc < 3 ? 3 : mc;
+}
+// Cycles of a block of K in one CTA, as measured: the read-back, by its chunks
+// and by how many blocks share its waits (48 columns, four blocks: 264; 96, two:
+// 650; 192, one: 1140; 192 of a pair: 850, fewer columns no less), or the
+// bytes' way from L2 (48 columns of 128 rows: 450).
+inline int fp8_block_cycles(bool pair, int xrows, int n) {
+    if (pair) return 850;
+    const int D = fp8_depth(false, xrows, n), read = 30 + 230 * fp8_chunks(n, D) + 60 * (4 / D - 1);
+    const int l2 = (xrows + n) * 128 / 50;
+    return read > l2 ? read : l2;
+}
+// The tile and slices whose rounds cost least.  Handing the sums over costs
+// 2000 cycles and 12 a column.  40 x 1536 x 6144: 48 columns in 4 slices 6.9 us,
+// 16 in one 8.8; 64 x 6144 x 6144: 48 in one 12.7, 96 in two 12.6, 64 in one
+// 14.4; 200 x 6144 x 6144: 176 in two 16.5, 96 in one 21.3; 300 x 2000 x 2976:
+// 48 in one 8.4, 96 in two 9.1.
 inline Fp8Plan fp8_plan(int M, int R, int K, int sms) {
     Fp8Plan p{};
-    p.pair = sms >= 2 && M > 128 && (int64_t)((M + 255) / 256) * ((R + 255) / 256) * 2 >= sms;
-    const int of = p.pair ? 2 : 1, slots = sms / of;
-    p.RT = p.pair ? (M + 255) / 256 : (M + 127) / 128;
-    p.xrows = p.pair || M >= 128 ? 128 : (M + 7) / 8 * 8;
+    const int KI = (K + 127) / 128;
     int64_t least = INT64_MAX;
-    for (int n = 192; n >= (p.pair ? 64 : 16); n -= 16 * of) {
-        const int ct = (R + n - 1) / n;
-        const int64_t rounds = ((int64_t)p.RT * ct + slots - 1) / slots;
-        const int64_t cost = rounds * (p.pair ? n + 8 : n + p.xrows / 2 + 16);
-        if (cost < least) least = cost, p.n = n, p.CT = ct;
+    for (int pair = 0; pair <= (M > 128 && sms >= 2 ? 1 : 0); ++pair) {
+        const int of = 1 + pair, slots = sms / of, rt = (M + 128 * of - 1) / (128 * of);
+        const int xrows = M >= 128 ? 128 : (M + 7) / 8 * 8;
+        for (int n = 192; n >= (pair ? 128 : 16); n -= 16 * of) {
+            const int ct = (R + n - 1) / n;
+            const int64_t tiles = (int64_t)rt * ct;
+            for (int s = 1; s <= (pair ? 1 : 8); s *= 2) {
+                // (a slice is whole stages of up to four blocks, and every slice has one)
+                const int len = s == 1 ? KI : ((KI + s - 1) / s + 3) / 4 * 4;
+                if (s > 1 && (tiles * s > sms || len * (s - 1) >= KI)) break;
+                const int64_t rounds = (tiles * s + slots - 1) / slots;
+                const int64_t cost = rounds * len * fp8_block_cycles(pair != 0, xrows, n) + (s > 1 ? 2000 + 12 * n : 0);
+                if (cost >= least) continue;
+                least = cost;
+                p.pair = pair, p.n = n, p.xrows = xrows, p.RT = rt, p.CT = ct, p.slices = s, p.slice_len = len;
+            }
+        }
     }
-    // blocks of a stage: as many as leave two buffers of accumulators and four stages
-    const int block = (p.xrows + p.n / of) * 128, room = kF8Smem - 1024 - (128 - p.xrows) * 128;
-    p.D = p.pair ? 1 : p.n <= 64 && room / (4 * block) >= 4 ? 4 : p.n <= 128 && room / (2 * block) >= 4 ? 2 : 1;
-    p.mc = (p.n / 16 + 2) / 3;
-    if (p.D == 1 && p.mc < 3) p.mc = 3;  // (n is 96 or more)
+    const int of = 1 + p.pair, block = (p.xrows + p.n / of) * 128, slots = sms / of;
+    p.D = fp8_depth(p.pair != 0, p.xrows, p.n);
+    p.mc = fp8_chunks(p.n, p.D);
     p.nbuf = 512 / (p.D * p.n) < 8 / p.D ? 512 / (p.D * p.n) : 8 / p.D;
-    p.nst = room / (p.D * block);
+    p.nst = fp8_room(p.xrows) / (p.D * block);
     if (p.nst > kF8MaxStages) p.nst = kF8MaxStages;
     const int64_t tiles = (int64_t)p.RT * p.CT;
-    p.grid = of * (int)(tiles < slots ? tiles : slots);
+    p.grid = p.slices > 1 ? (int)tiles * p.slices : of * (int)(tiles < slots ? tiles : slots);
     return p;
 }
 

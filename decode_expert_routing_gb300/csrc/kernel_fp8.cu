@@ -30,6 +30,7 @@ struct Fp8Args {
     int64_t ldxs, ldws, ldo, tiles;
     unsigned long long wait_ns;
     int M, R, KI, n, xrows, RT, nst, nbuf, out_fp32, vec, flags;
+    int slices, slice_len;  // SPLIT: CTAs of a cluster, blocks of each
 };
 
 namespace {
@@ -102,7 +103,9 @@ __device__ __forceinline__ void f8_store(const Fp8Args& a, int64_t m, int col, c
 
 // D: blocks of a stage and of a buffer (those behind K are zeros); MC: chunks
 // of 16 columns that a read-back warp takes, a third of them rounded up.
-template <bool PAIR, int D, int MC>
+// SPLIT: the CTAs of a cluster (one tile each cluster) share its K range, and
+// add their sums in K order, every CTA those of the chunks that it owns.
+template <bool PAIR, int D, int MC, bool SPLIT>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Args a) {
     extern __shared__ __align__(16) unsigned char dsm[];
     __shared__ __align__(8) unsigned long long s_full[kF8MaxStages], s_empty[kF8MaxStages], s_tfull[8], s_tempty[8], s_mfree[8], s_drain;
@@ -158,9 +161,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     unsigned ph = 0;  // its phase
     int buf = 0;      // accumulator buffer
     unsigned bph = 0;
-    const int64_t step = gridDim.x / of;
+    const int64_t first = SPLIT ? blockIdx.x / a.slices : blockIdx.x / of, step = SPLIT ? gridDim.x / a.slices : gridDim.x / of;
+    const int slice = SPLIT ? (int)cluster_rank() : 0;
+    const int k0 = SPLIT ? slice * a.slice_len : 0, k1 = SPLIT ? min(a.KI, k0 + a.slice_len) : a.KI;
+    const bool half = !PAIR && a.xrows <= 64;  // products of 64 rows: four times 16 lanes
     const uint32_t lead = ex_elect() ? 1u : 0u;  // (whole warps up to here)
 
+    bool met = false;
     // registers of the warps that copy and issue for those that keep sums: 128 x 56 + 384 x 152 of the 512 x 128
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -168,10 +175,10 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         // ---- copies
         int issued = 0;
         bool ok = true;
-        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
+        for (int64_t t = first; ok && t < a.tiles; t += step) {
             const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT);
             const int m0 = (rt * of + rank) * 128, w0 = ct * a.n + rank * (a.n / of);
-            for (int ki = 0; ki < a.KI; ki += D) {
+            for (int ki = k0; ki < k1; ki += D) {
                 if (!ex_wait_cta(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
@@ -200,8 +207,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         // ---- a pair's products are issued by its first CTA: told when this CTA's operands are in place
         bool ok = true;
         const uint32_t peer = map_rank(full0, 0);
-        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
-            for (int ki = 0; ki < a.KI; ki += D) {
+        for (int64_t t = first; ok && t < a.tiles; t += step) {
+            for (int ki = k0; ki < k1; ki += D) {
                 if (!ex_wait_cta(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
@@ -214,9 +221,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     } else if (warp == 1) {
         // ---- products, a stage's blocks side by side into each buffer in turn
         bool ok = true;
-        const uint32_t idesc = f8_idesc(128 * of, a.n), mfree0 = PAIR ? smem_u32(&s_mfree[0]) : tempty0;
-        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
-            for (int ki = 0; ki < a.KI; ki += D) {
+        const uint32_t idesc = f8_idesc(half ? 64 : 128 * of, a.n), mfree0 = PAIR ? smem_u32(&s_mfree[0]) : tempty0;
+        for (int64_t t = first; ok && t < a.tiles; t += step) {
+            for (int ki = k0; ki < k1; ki += D) {
                 // (a pair's stage is in the peer's memory too.  The buffer last: it is the one that is waited for)
                 if (!(PAIR ? ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)
                            : ex_wait_cta(full0 + 8u * st, ph, a.wait_ns, &s_abort)) ||
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         // two of them
         const int last = (a.R - 1) >> 7, row = (warp - 2) * 64 + lane;
         bool ok = true;
-        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
+        for (int64_t t = first; ok && t < a.tiles; t += step) {
             const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT), bt = ct * a.n >> 7;
             const int64_t m = (int64_t)(rt * of + rank) * 128 + row;
             const float* xs[2] = {a.xs + min(m, (int64_t)a.M - 1) * a.ldxs, a.xs + min(m + 32, (int64_t)a.M - 1) * a.ldxs};
@@ -256,15 +263,15 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             auto fetch = [&](int ki) {
 #pragma unroll
                 for (int b = 0; b < D; ++b) {
-                    const int k = min(ki + b, a.KI - 1);  // (a block behind K is zeros, whatever its scale)
+                    const bool in = D == 1 || ki + b < a.KI;  // (behind K: no scale either)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) x[i][b] = __ldg(xs[i] + k);
+                    for (int i = 0; i < 2; ++i) x[i][b] = in ? __ldg(xs[i] + ki + b) : 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) w[j][b] = __ldg(ws[j] + k);
+                    for (int j = 0; j < 3; ++j) w[j][b] = in ? __ldg(ws[j] + ki + b) : 0.0f;
                 }
             };
-            fetch(0);
-            for (int ki = 0; ki < a.KI; ki += D) {
+            fetch(k0);
+            for (int ki = k0; ki < k1; ki += D) {
                 if (!ex_wait_cta(tempty0 + 8u * buf, bph ^ 1u, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(tfull0 + 8u * buf);
                 if (++buf == a.nbuf) buf = 0, bph ^= 1u;
-                if (ki + D < a.KI) fetch(ki + D);
+                if (ki + D < k1) fetch(ki + D);
             }
         }
     }
@@ -291,19 +298,20 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         const int c0 = min(grp * MC, nch - MC), own = grp * MC - c0;
         const uint32_t lanes = (uint32_t)(wq * 32) << 16, mfree = PAIR ? map_rank(smem_u32(&s_mfree[0]), 0) : 0u;
         bool ok = true;
-        for (int64_t t = blockIdx.x / of; ok && t < a.tiles; t += step) {
+        for (int64_t t = first; ok && t < a.tiles; t += step) {
             const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT);
-            const int64_t m = (int64_t)(rt * of + rank) * 128 + wq * 32 + lane;
+            const int row = half ? wq * 16 + (lane & 15) : wq * 32 + lane;
+            const int64_t m = half && lane >= 16 ? a.M : (int64_t)(rt * of + rank) * 128 + row;
             const int col0 = ct * a.n + c0 * 16;
             // the scale block of the first columns in the tile, and the chunk from which on it is the next one
             const int j0 = (col0 >> 7) - (ct * a.n >> 7), j1 = min(j0 + 1, 2), turn = 8 - ((col0 >> 4) & 7);
-            const float *p0 = &s_scale[0][j0][wq * 32 + lane], *p1 = &s_scale[0][j1][wq * 32 + lane];
+            const float *p0 = &s_scale[0][j0][row], *p1 = &s_scale[0][j1][row];
             float acc[MC][16];
 #pragma unroll
             for (int c = 0; c < MC; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
-            for (int ki = 0; ki < a.KI; ki += D) {
+            for (int ki = k0; ki < k1; ki += D) {
                 if (!ex_wait_cta(tfull0 + 8u * buf, bph, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
@@ -345,12 +353,50 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 }
                 if (++buf == a.nbuf) buf = 0, bph ^= 1u;
             }
-            if (ok && m < a.M) {
+            if (SPLIT) {
+                // every CTA's products are done, so its ring's room is free: [sender][its chunks of mine][16][128]
+                ex_cluster_meet();
+                const int most = (nch + a.slices - 1) / a.slices, at = wq * 32 + lane;
+#pragma unroll
+                for (int c = 0; c < MC; ++c) {
+                    const int i = c0 + c, owner = i % a.slices;
+                    if (c < own || owner == slice) continue;
+                    const uint32_t to = map_rank(base, (unsigned)owner) + (uint32_t)((slice * most + i / a.slices) * 2048 + at) * 4u;
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 512u * q), "f"(acc[c][q]) : "memory");
+                }
+                ex_cluster_meet();
+                met = true;
+#pragma unroll
+                for (int c = 0; c < MC; ++c) {
+                    const int i = c0 + c;
+                    if (c < own || i % a.slices != slice || !ok || m >= a.M) continue;
+                    float sum[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) sum[q] = 0.0f;
+                    for (int z = 0; z < a.slices; ++z) {
+                        const uint32_t from = base + (uint32_t)((z * most + i / a.slices) * 2048 + at) * 4u;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            float x = acc[c][q];
+                            if (z != slice) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(from + 512u * q) : "memory");
+                            sum[q] = __fadd_rn(sum[q], x);
+                        }
+                    }
+                    f8_store(a, m, col0 + 16 * c, sum);
+                }
+            } else if (ok && m < a.M) {
 #pragma unroll
                 for (int c = 0; c < MC; ++c)
                     if (c >= own) f8_store(a, m, col0 + 16 * c, acc[c]);
             }
         }
+    }
+    if (SPLIT && !met) {  // the two meetings of the CTAs that hand sums over
+        __syncwarp();
+        ex_cluster_meet();
+        ex_cluster_meet();
     }
     __syncthreads();
     if (PAIR) {
@@ -375,14 +421,14 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     }
 }
 
-template <bool PAIR, int D, int MC>
+template <bool PAIR, int D, int MC, bool SPLIT>
 cudaError_t launch_one(const Fp8Args& a, int grid, cudaStream_t st) {
     static int prepared[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    const auto kernel = fp8_gemm_kernel<PAIR, D, MC>;
+    const auto kernel = fp8_gemm_kernel<PAIR, D, MC, SPLIT>;
     if (!__atomic_load_n(&prepared[dev], __ATOMIC_ACQUIRE)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8Smem);
         if (e != cudaSuccess) return e;
@@ -397,26 +443,30 @@ cudaError_t launch_one(const Fp8Args& a, int grid, cudaStream_t st) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.x = SPLIT ? (unsigned)a.slices : 2;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = PAIR ? 2 : 1;
+    cfg.numAttrs = PAIR || SPLIT ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kernel, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_plan(const Fp8Plan& p, const Fp8Args& a, cudaStream_t st) {
-    switch ((p.pair ? 100 : 0) + p.D * 10 + p.mc) {
-        case 41: return launch_one<false, 4, 1>(a, p.grid, st);
-        case 42: return launch_one<false, 4, 2>(a, p.grid, st);
-        case 21: return launch_one<false, 2, 1>(a, p.grid, st);
-        case 22: return launch_one<false, 2, 2>(a, p.grid, st);
-        case 23: return launch_one<false, 2, 3>(a, p.grid, st);
-        case 13: return launch_one<false, 1, 3>(a, p.grid, st);
-        case 14: return launch_one<false, 1, 4>(a, p.grid, st);
-        case 113: return launch_one<true, 1, 3>(a, p.grid, st);
-        default: return launch_one<true, 1, 4>(a, p.grid, st);
+template <bool SPLIT>
+cudaError_t launch_single(const Fp8Plan& p, const Fp8Args& a, cudaStream_t st) {
+    switch (p.D * 10 + p.mc) {
+        case 41: return launch_one<false, 4, 1, SPLIT>(a, p.grid, st);
+        case 42: return launch_one<false, 4, 2, SPLIT>(a, p.grid, st);
+        case 21: return launch_one<false, 2, 1, SPLIT>(a, p.grid, st);
+        case 22: return launch_one<false, 2, 2, SPLIT>(a, p.grid, st);
+        case 23: return launch_one<false, 2, 3, SPLIT>(a, p.grid, st);
+        case 13: return launch_one<false, 1, 3, SPLIT>(a, p.grid, st);
+        default: return launch_one<false, 1, 4, SPLIT>(a, p.grid, st);
     }
+}
+cudaError_t launch_plan(const Fp8Plan& p, const Fp8Args& a, cudaStream_t st) {
+    if (p.slices > 1) return launch_single<true>(p, a, st);
+    if (!p.pair) return launch_single<false>(p, a, st);
+    return p.mc == 3 ? launch_one<true, 1, 3, false>(a, p.grid, st) : launch_one<true, 1, 4, false>(a, p.grid, st);
 }
 
 }  // namespace
@@ -461,6 +511,8 @@ int launch_fp8_gemm(const Fp8GemmCall& c, cudaStream_t st, cudaError_t* err) {
     a.out_fp32 = c.out_fp32;
     a.vec = reinterpret_cast<uintptr_t>(c.out) % 16 == 0 && c.ldo % (c.out_fp32 ? 4 : 8) == 0;
     a.flags = launch_flags();
+    a.slices = p.slices;
+    a.slice_len = p.slice_len;
     const cudaError_t e = launch_plan(p, a, st);
     *err = e;
     return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;

@@ -39,7 +39,8 @@ SHAPES = [  # M, R, K
     (1, 1, 1), (1, 16, 16), (1, 200, 300), (2, 129, 128), (7, 33, 129), (8, 6144, 768), (1, 1536, 6144), (9, 500, 100),
     (16, 17, 2976), (17, 128, 256), (33, 2000, 512), (64, 1000, 1024), (65, 15, 640), (100, 255, 2048), (127, 256, 384),
     (128, 257, 400), (129, 300, 1000), (200, 2500, 528), (255, 700, 127), (256, 6144, 256), (257, 6100, 144),
-    (300, 2000, 2976), (500, 9000, 272), (1001, 4100, 640), (1300, 1536, 6144)]
+    (300, 2000, 2976), (500, 9000, 272), (1001, 4100, 640), (1300, 1536, 6144),
+    (17, 1536, 6144), (40, 1536, 5000), (64, 500, 6144), (100, 1536, 3000), (60, 6144, 1100)]
 
 
 @pytest.mark.parametrize("M,R,K", SHAPES)

@@ -133,8 +133,8 @@ int main() {
     const int sms[] = {1, 2, 100, 148, 152};
     for (int M : Ms) for (int R : Rs) for (int K : Ks) for (int s : sms) {
         const mr::Fp8Plan p = mr::fp8_plan(M, R, K, s);
-        printf("%d %d %d %d %d %d %d %d %d %d %d %d %d %d\n", M, R, K, s, p.pair, p.n, p.xrows, p.RT, p.CT, p.D, p.mc, p.nst,
-               p.nbuf, p.grid);
+        printf("%d %d %d %d %d %d %d %d %d %d %d %d %d %d %d %d\n", M, R, K, s, p.pair, p.n, p.xrows, p.RT, p.CT, p.D, p.mc, p.nst,
+               p.nbuf, p.grid, p.slices, p.slice_len);
     }
 }
 '''
@@ -148,7 +148,7 @@ def test_plans_keep_what_the_kernel_relies_on(tmp_path):
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines()
     assert len(out) == 20 * 16 * 9 * 5
     for line in out:
-        M, R, K, sms, pair, n, xrows, RT, CT, D, mc, nst, nbuf, grid = map(int, line.split())
+        M, R, K, sms, pair, n, xrows, RT, CT, D, mc, nst, nbuf, grid, slices, len_ = map(int, line.split())
         of = 2 if pair else 1
         assert n % (16 * of) == 0 and 16 * of <= n <= 192 and (D, n <= {1: 192, 2: 128, 4: 64}[D]) in {(1, True), (2, True), (4, True)}
         # copies: whole groups of 8 rows, no more than the operand's 128, and every row of x has one
@@ -160,5 +160,11 @@ def test_plans_keep_what_the_kernel_relies_on(tmp_path):
         # accumulators and stages (the product reads 128 rows of x whatever was copied)
         assert 2 <= nbuf and nbuf * D <= 8 and nbuf * D * n <= 512
         assert 3 <= nst <= 24 and nst * D * (xrows + n // of) * 128 + (128 - xrows) * 128 + 1024 <= 208 * 1024
-        assert grid % of == 0 and grid >= of and grid // of <= RT * CT
-        assert grid <= sms or (pair == 0 and grid == 1)
+        KI = -(-K // 128)
+        if slices == 1:
+            assert grid % of == 0 and grid >= of and grid // of <= RT * CT
+            assert grid <= sms or (pair == 0 and grid == 1)
+        else:  # one tile a cluster, blocks for every slice in whole stages, and room for the sums where the stages were
+            assert not pair and slices in (2, 4, 8) and grid == RT * CT * slices <= sms
+            assert len_ % D == 0 and len_ * (slices - 1) < KI <= len_ * slices
+            assert slices * -(-(n // 16) // slices) * 16 * 128 * 4 + 1024 <= 208 * 1024
