@@ -11,23 +11,29 @@ namespace mr {
 constexpr int kFp8Group = 128;
 
 // Codes and scale of 8 consecutive bf16 values (one lane of the 16 lanes that
-// hold a group of 128; all 32 lanes of the warp call it together):
+// hold a group of 128; all 32 lanes of the warp call these together):
 //   scale = max(amax / 448, 2^-126),  code = e4m3(x * (1 / scale)),
 // every fp32 step rounded to nearest.  At the lower bound 1 / scale is finite
 // and the smallest bf16, 2^-133, is 2^-7: no value is lost, and a group of
-// zeros needs no case of its own.  A NaN makes the scale NaN (the comparison
-// keeps it), an infinity makes it infinite: either way the group's products
-// are NaN.
-__device__ __forceinline__ uint2 fp8_quant_16th(uint4 v, float* scale) {
+// zeros needs no case of its own.  A NaN or an infinity makes the scale NaN
+// (the comparison keeps it), and with it every code and product of the group.
+__device__ __forceinline__ float fp8_amax_16th(uint4 v) {
     unsigned m = vmax_u16x2(vmax_u16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                             vmax_u16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) m = vmax_u16x2(m, __shfl_xor_sync(kFull, m, o));
-    const float amax = __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
-    float s = __fdiv_rn(amax, 448.0f);
-    s = s < 0x1p-126f ? 0x1p-126f : s;
-    *scale = s;
-    const float inv = __frcp_rn(s);
+    return __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
+}
+// amax / 448 rounded to nearest: a first quotient with the rounded reciprocal,
+// put right by its remainder, which is exact (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).
+__device__ __forceinline__ float fp8_scale(float amax) {
+    constexpr float y = 1.0f / 448.0f;
+    const float q = __fmul_rn(amax, y);
+    const float s = __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), y, q);
+    return s < 0x1p-126f ? 0x1p-126f : s;
+}
+__device__ __forceinline__ uint2 fp8_codes(uint4 v, float inv) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t out[2] = {0u, 0u};
 #pragma unroll
@@ -38,6 +44,23 @@ __device__ __forceinline__ uint2 fp8_quant_16th(uint4 v, float* scale) {
         out[i >> 1] |= (uint32_t)p << (16 * (i & 1));
     }
     return make_uint2(out[0], out[1]);
+}
+// The scales of C chunks (two groups of 128 each in a warp) and their
+// reciprocals: lane 16 h + i has that of half h of chunk i, so that the
+// reciprocal is computed once for all of them.
+template <int C>
+__device__ __forceinline__ void fp8_scales(const float (&amax)[C], float (&scale)[C], float (&inv)[C]) {
+    static_assert(C <= 16, "a lane of each half for every chunk");
+    const int lane = threadIdx.x & 31;
+    float mine = amax[0];
+#pragma unroll
+    for (int i = 1; i < C; ++i) mine = (lane & 15) == i ? amax[i] : mine;
+    const float s = fp8_scale(mine), r = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        scale[i] = __shfl_sync(kFull, s, (lane & 16) + i);
+        inv[i] = __shfl_sync(kFull, r, (lane & 16) + i);
+    }
 }
 
 // One warp per 128 chunks of 8 elements (8 groups) of a row, four loads in
@@ -59,14 +82,17 @@ __global__ void __launch_bounds__(kFp8Threads) fp8_quant_kernel(const uint16_t* 
             const int c = c0 + u * 32;
             v[u] = c < vpr ? ld_stream_v4(x + r * ldx + c * 8) : make_uint4(0u, 0u, 0u, 0u);
         }
+        float amax[kFp8Unroll], s[kFp8Unroll], inv[kFp8Unroll];
+#pragma unroll
+        for (int u = 0; u < kFp8Unroll; ++u) amax[u] = fp8_amax_16th(v[u]);
+        fp8_scales(amax, s, inv);
 #pragma unroll
         for (int u = 0; u < kFp8Unroll; ++u) {
             const int c = c0 + u * 32;
-            float s;
-            const uint2 q8 = fp8_quant_16th(v[u], &s);
+            const uint2 q8 = fp8_codes(v[u], inv[u]);
             if (c >= vpr) continue;
             *reinterpret_cast<uint2*>(q + r * K + c * 8) = q8;
-            if ((lane & 15) == 0) scale[r * KB + c / 16] = s;
+            if ((lane & 15) == 0) scale[r * KB + c / 16] = s[u];
         }
     }
 }
@@ -106,10 +132,42 @@ __device__ __forceinline__ Two two_add(Two a, Two b) {  // (lo parts: rounding e
     const ffloat s = ff_two_sum(a.hi, b.hi);
     return {s.hi, __fadd_rn(__fadd_rn(a.lo, b.lo), s.lo)};
 }
-__device__ __forceinline__ void two_add_to(Two& a, float b) {
-    const ffloat s = ff_two_sum(a.hi, b);
-    a.hi = s.hi;
-    a.lo = __fadd_rn(a.lo, s.lo);
+// Two fp32 numbers in one register pair: one instruction for both, each rounded
+// by itself.  (At 4096 x 6144 the kernel issued 46 instructions an element, 78 %
+// of what the SMs can, and took 38 us.)
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair_of(uint32_t lo, uint32_t hi) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ void pair_split(Pair p, float& lo, float& hi) {
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(p));
+    lo = __uint_as_float(a), hi = __uint_as_float(b);
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair pair_sub(Pair a, Pair b) {
+    Pair r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair pair_bf16(uint32_t two) { return pair_of(two << 16, two & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pair_to_bf16(Pair p) {
+    float lo, hi;
+    pair_split(p, lo, hi);
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
 }
 
 // 1 / sqrt((hi + lo) / K + eps)
@@ -130,9 +188,9 @@ __device__ __forceinline__ float norm_rstd(Two sum, int K, float eps) {
     return __fmaf_rn(__fmul_rn(r, 0.5f), e, r);
 }
 
-template <int C, int FMT>
-__global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
-    __shared__ float s_hi[32], s_lo[32];
+template <int C, int FMT, int T>
+__global__ void __launch_bounds__(T) add_norm_kernel(const NormArgs a) {
+    __shared__ float s_hi[32], s_lo[32], s_rstd;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
     const int vpr = a.K / 8;
     const int64_t m = blockIdx.x;
@@ -151,86 +209,125 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const NormArgs a) {
         const int c = tid + i * nthr;
         g[i] = c < vpr ? ld_ro_v4(a.g + c * 8) : zero;
     }
-    Two sum = {0.0f, 0.0f};
+    Pair hi = 0ull, lo = 0ull;  // sums of the even and of the odd elements' squares, and their rounding errors
 #pragma unroll
     for (int i = 0; i < C; ++i) {
+        uint32_t* p = &v[i].x;
+        const uint32_t* q = &r[i].x;
         if (a.residual != nullptr) {
-            uint32_t* p = &v[i].x;
-            const uint32_t* q = &r[i].x;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float lo = __fadd_rn(__uint_as_float(p[j] << 16), __uint_as_float(q[j] << 16));
-                const float hi = __fadd_rn(__uint_as_float(p[j] & 0xFFFF0000u), __uint_as_float(q[j] & 0xFFFF0000u));
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[j]) : "f"(hi), "f"(lo));
-            }
+            for (int j = 0; j < 4; ++j) p[j] = pair_to_bf16(pair_add(pair_bf16(p[j]), pair_bf16(q[j])));
         }
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xFFFF0000u);
-            two_add_to(sum, __fmul_rn(lo, lo));
-            two_add_to(sum, __fmul_rn(hi, hi));
+            const Pair x = pair_bf16(p[j]), x2 = pair_mul(x, x), s = pair_add(hi, x2), b = pair_sub(s, hi);
+            lo = pair_add(lo, pair_add(pair_sub(hi, pair_sub(s, b)), pair_sub(x2, b)));
+            hi = s;
         }
         const int c = tid + i * nthr;
         if (a.sres != nullptr && c < vpr) *reinterpret_cast<uint4*>(a.sres + m * a.lds + c * 8) = v[i];
     }
+    Two sum, odd;
+    pair_split(hi, sum.hi, odd.hi);
+    pair_split(lo, sum.lo, odd.lo);
+    sum = two_add(sum, odd);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         sum = two_add(sum, Two{__shfl_xor_sync(kFull, sum.hi, o), __shfl_xor_sync(kFull, sum.lo, o)});
-    if (nw > 1) {
-        if (lane == 0) s_hi[warp] = sum.hi, s_lo[warp] = sum.lo;
-        __syncthreads();
+    // (of many rows one warp finishes the sum; of few, where a barrier's latency counts, every warp for itself)
+    if (lane == 0) s_hi[warp] = sum.hi, s_lo[warp] = sum.lo;
+    __syncthreads();
+    float rstd;
+    if (T > 256 || warp == 0) {
         sum = lane < nw ? Two{s_hi[lane], s_lo[lane]} : Two{0.0f, 0.0f};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = T > 256 ? 16 : 4; o > 0; o >>= 1)
             sum = two_add(sum, Two{__shfl_xor_sync(kFull, sum.hi, o), __shfl_xor_sync(kFull, sum.lo, o)});
+        rstd = norm_rstd(sum, a.K, a.eps);
+        if (tid == 0) {
+            s_rstd = rstd;
+            if (a.rstd != nullptr) a.rstd[m] = rstd;
+        }
     }
-    const float rstd = norm_rstd(sum, a.K, a.eps);
-    if (a.rstd != nullptr && tid == 0) a.rstd[m] = rstd;
+    if (T <= 256) {
+        __syncthreads();
+        rstd = s_rstd;
+    }
     if (FMT == 0 && a.xn == nullptr) return;
+    const Pair rr = pair_of(__float_as_uint(rstd), __float_as_uint(rstd)), ones = pair_of(0x3F800000u, 0x3F800000u);
+    uint4 n[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
+        // norm_pair's steps (a row's end: zeros, whatever rstd is)
         const int c = tid + i * nthr;
-        const bool in = c < vpr;
-        const uint4 n = in ? norm_chunk(v[i], g[i], rstd, a.gemma != 0) : zero;
-        if (a.xn != nullptr && in) *reinterpret_cast<uint4*>(a.xn + m * a.K + c * 8) = n;
-        if (FMT == 1) {
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, w[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+        uint32_t* o = &n[i].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Pair k = a.gemma ? pair_add(ones, pair_bf16(w[j])) : pair_bf16(w[j]);
+            o[j] = pair_to_bf16(pair_mul(pair_mul(pair_bf16(x[j]), rr), k));
+        }
+        if (c >= vpr) n[i] = zero;
+        if (a.xn != nullptr && c < vpr) *reinterpret_cast<uint4*>(a.xn + m * a.K + c * 8) = n[i];
+    }
+    if constexpr (FMT == 3) {
+        float amax[C], s[C], inv[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) amax[i] = fp8_amax_16th(n[i]);
+        fp8_scales(amax, s, inv);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = tid + i * nthr;
+            const uint2 q = fp8_codes(n[i], inv[i]);
+            if (c >= vpr) continue;
+            *reinterpret_cast<uint2*>(a.q + m * a.K + c * 8) = q;
+            if ((lane & 15) == 0) static_cast<float*>(a.scale)[m * ((a.K + kFp8Group - 1) / kFp8Group) + c / 16] = s[i];
+        }
+    }
+    if constexpr (FMT == 1 || FMT == 2) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = tid + i * nthr;
             unsigned sb;
-            const uint2 q = mx_quant_quad(n, &sb);
-            if (in) *reinterpret_cast<uint2*>(a.q + m * a.K + c * 8) = q;
-            if (in && (lane & 3) == 0) static_cast<uint8_t*>(a.scale)[m * (a.K / 32) + c / 4] = (uint8_t)sb;
-        } else if (FMT == 2) {
-            unsigned sb;
-            const uint32_t q = mx4_quant_quad(n, &sb);
-            if (in) *reinterpret_cast<uint32_t*>(a.q + m * (a.K / 2) + c * 4) = q;
-            if (in && (lane & 3) == 0) static_cast<uint8_t*>(a.scale)[m * (a.K / 32) + c / 4] = (uint8_t)sb;
-        } else if (FMT == 3) {
-            float s;
-            const uint2 q = fp8_quant_16th(n, &s);
-            if (in) *reinterpret_cast<uint2*>(a.q + m * a.K + c * 8) = q;
-            if (in && (lane & 15) == 0)
-                static_cast<float*>(a.scale)[m * ((a.K + kFp8Group - 1) / kFp8Group) + c / 16] = s;
+            if (FMT == 1) {
+                const uint2 q = mx_quant_quad(n[i], &sb);
+                if (c < vpr) *reinterpret_cast<uint2*>(a.q + m * a.K + c * 8) = q;
+            } else {
+                const uint32_t q = mx4_quant_quad(n[i], &sb);
+                if (c < vpr) *reinterpret_cast<uint32_t*>(a.q + m * (a.K / 2) + c * 4) = q;
+            }
+            if (c < vpr && (lane & 3) == 0) static_cast<uint8_t*>(a.scale)[m * (a.K / 32) + c / 4] = (uint8_t)sb;
         }
     }
 }
 
-template <int C>
-cudaError_t launch_norm_c(const NormArgs& a, int threads, cudaStream_t st) {
-    void (*kernel)(const NormArgs) = a.fmt == 0   ? add_norm_kernel<C, 0>
-                                     : a.fmt == 1 ? add_norm_kernel<C, 1>
-                                     : a.fmt == 2 ? add_norm_kernel<C, 2>
-                                                  : add_norm_kernel<C, 3>;
+template <int C, int T>
+cudaError_t launch_norm_c(const NormArgs& a, cudaStream_t st) {
+    void (*kernel)(const NormArgs) = a.fmt == 0   ? add_norm_kernel<C, 0, T>
+                                     : a.fmt == 1 ? add_norm_kernel<C, 1, T>
+                                     : a.fmt == 2 ? add_norm_kernel<C, 2, T>
+                                                  : add_norm_kernel<C, 3, T>;
+    const int threads = ((a.K / 8 + C - 1) / C + 31) / 32 * 32;
     return launch_overlapped(kernel, dim3((unsigned)a.M), dim3((unsigned)threads), 0, st, a);
 }
 
 cudaError_t launch_add_norm(const NormArgs& a, cudaStream_t st) {
-    const int vpr = a.K / 8;
-    const int c = norm_chunks(vpr), threads = ((vpr + c - 1) / c + 31) / 32 * 32;
-    switch (c) {
-        case 1: return launch_norm_c<1>(a, threads, st);
-        case 2: return launch_norm_c<2>(a, threads, st);
-        case 4: return launch_norm_c<4>(a, threads, st);
-        default: return launch_norm_c<8>(a, threads, st);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const NormPlan p = norm_plan(a.M, a.K, sms);
+    switch (p.small * 10 + p.chunks) {
+        case 11: return launch_norm_c<1, 256>(a, st);
+        case 12: return launch_norm_c<2, 256>(a, st);
+        case 13: return launch_norm_c<3, 256>(a, st);
+        case 14: return launch_norm_c<4, 256>(a, st);
+        case 16: return launch_norm_c<6, 256>(a, st);
+        case 18: return launch_norm_c<8, 256>(a, st);
+        case 1: return launch_norm_c<1, 1024>(a, st);
+        case 2: return launch_norm_c<2, 1024>(a, st);
+        case 4: return launch_norm_c<4, 1024>(a, st);
+        default: return launch_norm_c<8, 1024>(a, st);
     }
 }
 

@@ -79,53 +79,71 @@ struct Elems {
 // lanes threads to a row, kRowThreads / lanes rows to a CTA.  MODE 0: rows as
 // they are (any type); 1: weighted, with the weights' gradients.  Padding
 // positions give rows of zeros; those behind *npost are left as they are.
+// A thread's loads of up to kRowUnroll words are under way together.
+constexpr int kRowUnroll = 4;
 template <int MODE, int TYPE, int BYTES>
-__global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExpertsArgs a, int lanes, int64_t row_vecs) {
+__global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExpertsArgs a, int lanes, int shift, int vecs) {
     using V = typename Vec<BYTES>::T;
     __shared__ float s_dot[kRowThreads / 32];
     pdl_trigger();
     pdl_wait();
-    const int tid = threadIdx.x, lane = tid % lanes, mk = a.M * a.topk;
-    const int64_t i0 = (int64_t)blockIdx.x * kRowThreads + tid;
-    // assignments that the sort left out
-    if (MODE == 0 && a.positions != nullptr && i0 < mk && (unsigned)a.ids[i0] >= (unsigned)a.E) a.positions[i0] = -1;
-    if (MODE == 1 && i0 < mk && (uint64_t)(int64_t)a.known[i0] >= (uint64_t)a.cap) a.grad_w[i0] = 0.0f;
-    const int64_t p = (int64_t)blockIdx.x * (kRowThreads / lanes) + tid / lanes;
-    const bool row = p < a.cap && p < *a.npost;
-    const int f = row ? a.sorted[p] : -1;
-    const bool real = (unsigned)f < (unsigned)mk;
-    if (row && !real) {
-        const V z{};
-        V* out = static_cast<V*>(a.out) + p * row_vecs;
-        for (int64_t c = lane; c < row_vecs; c += lanes) out[c] = z;
+    const int tid = threadIdx.x, lane = tid & (lanes - 1), mk = a.M * a.topk;
+    const int64_t p = ((int64_t)blockIdx.x << (__ffs(kRowThreads) - 1 - shift)) + (tid >> shift);
+    int f = -1;
+    bool row = false;
+    if (p < a.cap) {
+        f = __ldg(a.sorted + p);
+        row = p < __ldg(a.npost);
     }
+    {
+        // assignments that the sort left out
+        const int64_t i0 = (int64_t)blockIdx.x * kRowThreads + tid;
+        if (MODE == 0 && i0 < mk && (unsigned)a.ids[i0] >= (unsigned)a.E) a.positions[i0] = -1;
+        if (MODE == 1 && i0 < mk && (uint64_t)(int64_t)a.known[i0] >= (uint64_t)a.cap) a.grad_w[i0] = 0.0f;
+    }
+    const bool real = row && (unsigned)f < (unsigned)mk;
+    V* out = static_cast<V*>(a.out) + p * vecs;
     float dot = 0.0f;
     if (real) {
-        const int m = f / a.topk;
-        V* out = static_cast<V*>(a.out) + p * row_vecs;
-        const V* x = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.x) + (int64_t)m * a.ldx);
+        const V* x = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.x) + (int64_t)((unsigned)f / (unsigned)a.topk) * a.ldx);
         if constexpr (MODE == 0) {
-            if (a.positions != nullptr && lane == 0) a.positions[f] = (int32_t)p;
-#pragma unroll 4
-            for (int64_t c = lane; c < row_vecs; c += lanes) out[c] = __ldg(x + c);
+            if (lane == 0) a.positions[f] = (int32_t)p;
+            for (int c = lane; c < vecs; c += lanes * kRowUnroll) {
+                V v[kRowUnroll];
+#pragma unroll
+                for (int u = 0; u < kRowUnroll; ++u)
+                    if (c + u * lanes < vecs) v[u] = __ldg(x + c + u * lanes);
+#pragma unroll
+                for (int u = 0; u < kRowUnroll; ++u)
+                    if (c + u * lanes < vecs) __stcs(out + c + u * lanes, v[u]);
+            }
         } else {
             using E = Elems<TYPE, BYTES>;
             const float w = a.weights == nullptr ? 1.0f : __ldg(a.weights + f);
             const V* y = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + p * a.ldy);
-#pragma unroll 4
-            for (int64_t c = lane; c < row_vecs; c += lanes) {
-                const V gv = __ldg(x + c), yv = y[c];  // (out may be y itself)
-                float g[E::N], u[E::N];
-                E::get(gv, g);
-                E::get(yv, u);
+            for (int c = lane; c < vecs; c += lanes * kRowUnroll) {
+                V gv[kRowUnroll], yv[kRowUnroll];
 #pragma unroll
-                for (int i = 0; i < E::N; ++i) {
-                    dot = __fmaf_rn(g[i], u[i], dot);
-                    g[i] = __fmul_rn(w, g[i]);
+                for (int u = 0; u < kRowUnroll; ++u)
+                    if (c + u * lanes < vecs) gv[u] = __ldg(x + c + u * lanes), yv[u] = __ldcs(y + c + u * lanes);
+#pragma unroll
+                for (int u = 0; u < kRowUnroll; ++u) {
+                    if (c + u * lanes >= vecs) continue;
+                    float g[E::N], z[E::N];
+                    E::get(gv[u], g);
+                    E::get(yv[u], z);
+#pragma unroll
+                    for (int i = 0; i < E::N; ++i) {
+                        dot = __fmaf_rn(g[i], z[i], dot);
+                        g[i] = __fmul_rn(w, g[i]);
+                    }
+                    __stcs(out + c + u * lanes, E::put(g));  // (out may be y itself: its words have been read)
                 }
-                out[c] = E::put(g);
             }
         }
+    } else if (row) {
+        const V z{};
+        for (int c = lane; c < vecs; c += lanes) __stcs(out + c, z);
     }
     if constexpr (MODE == 1) {
         dot = warp_sum_fixed(dot);
@@ -142,53 +160,70 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExperts
 
 // ------------------------------------------------------------------ back to the tokens
 
-// A thread takes N elements of a token's row; the rows of up to eight slots
-// are in flight at a time.  The sum goes over the slots in ascending order in
-// fp32, from add (or zero), and is rounded once.
+// lanes threads to a token's row and kTokenVecs words to a thread, whose rows of
+// up to eight slots are under way together.  The sum goes over the slots in
+// ascending order in fp32, from add (or zero), and is rounded once.
 constexpr int kTokenThreads = 128;
-template <int TYPE, int BYTES>
-__global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokensArgs a, int row_vecs, int64_t total) {
+template <int TYPE, int BYTES, int VECS>
+__global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokensArgs a, int lanes, int shift, int vecs,
+                                                                  int blocks, int64_t total) {
     using E = Elems<TYPE, BYTES>;
     using V = typename Vec<BYTES>::T;
     pdl_trigger();
     pdl_wait();
-    for (int64_t i = (int64_t)blockIdx.x * kTokenThreads + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * kTokenThreads) {
-        const int64_t m = i / row_vecs;
-        const int c = (int)(i - m * row_vecs);
-        float s[E::N];
+    const int tid = threadIdx.x, lane = tid & (lanes - 1), per = kTokenThreads >> shift;
+    for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+        const int64_t mb = blocks == 1 ? b : b / blocks, m = mb * per + (tid >> shift);
+        const int c0 = (int)(b - mb * blocks) * lanes * VECS + lane;
+        if (m >= a.M || c0 >= vecs) continue;
+        float s[VECS][E::N];
 #pragma unroll
-        for (int u = 0; u < E::N; ++u) s[u] = 0.0f;
-        if (a.add != nullptr)
-            // (a plain load: out may be add itself)
-            E::get(*(reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.add) + m * a.ldadd) + c), s);
+        for (int k = 0; k < VECS; ++k)
+#pragma unroll
+            for (int q = 0; q < E::N; ++q) s[k][q] = 0.0f;
+        if (a.add != nullptr) {
+            // (plain loads: out may be add itself)
+            const V* add = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.add) + m * a.ldadd) + c0;
+#pragma unroll
+            for (int k = 0; k < VECS; ++k)
+                if (c0 + k * lanes < vecs) E::get(add[k * lanes], s[k]);
+        }
+        const int32_t* pos = a.positions + m * a.topk;
+        const float* wts = a.weights + (a.weights != nullptr ? m * a.topk : 0);
         for (int j0 = 0; j0 < a.topk; j0 += 8) {
-            V v[8];
-            int p[8];
+            V v[8][VECS];
             float w[8];
+            unsigned in = 0u;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                p[u] = -1;
                 w[u] = 1.0f;
                 if (j0 + u >= a.topk) continue;
-                p[u] = __ldg(a.positions + m * a.topk + j0 + u);
-                if (a.weights != nullptr) w[u] = __ldg(a.weights + m * a.topk + j0 + u);
+                const int p = __ldg(pos + j0 + u);
+                if (a.weights != nullptr) w[u] = __ldg(wts + j0 + u);
+                if ((uint64_t)(int64_t)p >= (uint64_t)a.cap) continue;
+                in |= 1u << u;
+                const V* y = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + (int64_t)p * a.ldy) + c0;
+#pragma unroll
+                for (int k = 0; k < VECS; ++k)
+                    if (c0 + k * lanes < vecs) v[u][k] = __ldcs(y + k * lanes);
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                if ((uint64_t)(int64_t)p[u] >= (uint64_t)a.cap) continue;
-                v[u] = __ldg(reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + (int64_t)p[u] * a.ldy) + c);
-            }
+                if (!(in >> u & 1u)) continue;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if ((uint64_t)(int64_t)p[u] >= (uint64_t)a.cap) continue;
-                float f[E::N];
-                E::get(v[u], f);
+                for (int k = 0; k < VECS; ++k) {
+                    if (c0 + k * lanes >= vecs) continue;
+                    float f[E::N];
+                    E::get(v[u][k], f);
 #pragma unroll
-                for (int q = 0; q < E::N; ++q) s[q] = __fmaf_rn(w[u], f[q], s[q]);
+                    for (int q = 0; q < E::N; ++q) s[k][q] = __fmaf_rn(w[u], f[q], s[k][q]);
+                }
             }
         }
-        reinterpret_cast<V*>(a.out)[i] = E::put(s);
+        V* out = static_cast<V*>(a.out) + m * vecs + c0;
+#pragma unroll
+        for (int k = 0; k < VECS; ++k)
+            if (c0 + k * lanes < vecs) out[k * lanes] = E::put(s[k]);
     }
 }
 
@@ -198,35 +233,40 @@ int vec_bytes(uintptr_t bits, int elem) {
     return elem;
 }
 
-int device_sms(int* sms) {
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    return e != cudaSuccess ? (int)e : (int)cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+int log2_of(int v) {
+    int s = 0;
+    while ((1 << s) < v) ++s;
+    return s;
 }
 
 template <int MODE, int TYPE, int BYTES>
 cudaError_t launch_experts_v(const ToExpertsArgs& a, cudaStream_t st) {
-    const int64_t vecs = (int64_t)a.K * row_elem_bytes(a.type) / BYTES;
+    const int vecs = (int)((int64_t)a.K * row_elem_bytes(a.type) / BYTES);
     int lanes = 32;
     while (lanes < kRowThreads && lanes < vecs) lanes *= 2;
     const int64_t per = kRowThreads / lanes, mk = (int64_t)a.M * a.topk;
     int64_t ctas = (a.cap + per - 1) / per;
     if (ctas * kRowThreads < mk) ctas = (mk + kRowThreads - 1) / kRowThreads;  // (a thread for each assignment)
     return launch_overlapped(to_experts_kernel<MODE, TYPE, BYTES>, dim3((unsigned)ctas), dim3(kRowThreads), 0, st, a,
-                             lanes, vecs);
+                             lanes, log2_of(lanes), vecs);
 }
 
+template <int TYPE, int BYTES, int VECS>
+cudaError_t launch_tokens_n(const ToTokensArgs& a, int vecs, cudaStream_t st) {
+    int lanes = 32;
+    while (lanes < kTokenThreads && lanes * VECS < vecs) lanes *= 2;
+    const int per = kTokenThreads / lanes, blocks = (vecs + lanes * VECS - 1) / (lanes * VECS);
+    const int64_t total = ((int64_t)a.M + per - 1) / per * blocks;
+    const int64_t ctas = total < ((int64_t)1 << 30) ? total : ((int64_t)1 << 30);
+    return launch_overlapped(to_tokens_kernel<TYPE, BYTES, VECS>, dim3((unsigned)ctas), dim3(kTokenThreads), 0, st, a,
+                             lanes, log2_of(lanes), vecs, blocks, total);
+}
 template <int TYPE, int BYTES>
 cudaError_t launch_tokens_v(const ToTokensArgs& a, cudaStream_t st) {
-    int sms = 0;
-    const int e = device_sms(&sms);
-    if (e != 0) return (cudaError_t)e;
     const int vecs = (int)((int64_t)a.K * row_elem_bytes(a.type) / BYTES);
-    const int64_t total = (int64_t)a.M * vecs;
-    int64_t ctas = (total + kTokenThreads - 1) / kTokenThreads;
-    if (ctas > (int64_t)sms * 16) ctas = (int64_t)sms * 16;
-    return launch_overlapped(to_tokens_kernel<TYPE, BYTES>, dim3((unsigned)ctas), dim3(kTokenThreads), 0, st, a, vecs,
-                             total);
+    // two words a thread where that leaves enough CTAs
+    return (int64_t)a.M * vecs >= (1 << 18) ? launch_tokens_n<TYPE, BYTES, 2>(a, vecs, st)
+                                           : launch_tokens_n<TYPE, BYTES, 1>(a, vecs, st);
 }
 
 }  // namespace

@@ -19,8 +19,18 @@ struct NormArgs {
     float eps;
 };
 
-// Chunks of 8 elements that a thread holds, of rows of vpr chunks.
-inline int norm_chunks(int vpr) { return vpr <= 1024 ? 1 : vpr <= 2048 ? 2 : vpr <= 4096 ? 4 : 8; }
+// Chunks of 8 elements that a thread holds; small: CTAs of at most 256 threads.
+struct NormPlan {
+    int small, chunks;
+};
+inline NormPlan norm_plan(int M, int K, int sms) {
+    const int vpr = K / 8;
+    if (M > 2 * sms && vpr <= 2048) {
+        const int c = (vpr + 255) / 256;
+        return {1, c <= 4 ? c : c <= 6 ? 6 : 8};
+    }
+    return {0, vpr <= 1024 ? 1 : vpr <= 2048 ? 2 : vpr <= 4096 ? 4 : 8};
+}
 
 cudaError_t launch_add_norm(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_fp8_quant(const void* x, int64_t ldx, int M, int K, uint8_t* q, float* scale, cudaStream_t st);
