@@ -79,11 +79,18 @@ struct Elems {
 // lanes threads to a row, kRowThreads / lanes rows to a CTA.  MODE 0: rows as
 // they are (any type); 1: weighted, with the weights' gradients.  Padding
 // positions give rows of zeros; those behind *npost are left as they are.
-// A thread's loads of up to kRowUnroll words are under way together.
-constexpr int kRowUnroll = 4;
+// A thread's loads of up to U words are under way together.
+//
+// MODE 0 goes through the rows in slabs, one slab of every row after the other
+// (blockIdx.y): a slab of x stays in L2 for all of its topk reads.  4096 x 8
+// rows of 6144, in slabs of 4 KB: 77 us (6.5 TB/s), whole rows 92.  MODE 1 takes
+// whole rows, for their sums.
+__host__ __device__ constexpr int row_unroll(int bytes) { return bytes >= 8 ? 4 : 6; }
 template <int MODE, int TYPE, int BYTES>
-__global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExpertsArgs a, int lanes, int shift, int vecs) {
+__global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExpertsArgs a, int lanes, int shift, int vecs,
+                                                                  int slab) {
     using V = typename Vec<BYTES>::T;
+    constexpr int U = row_unroll(BYTES);
     __shared__ float s_dot[kRowThreads / 32];
     pdl_trigger();
     pdl_wait();
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExperts
     {
         // assignments that the sort left out
         const int64_t i0 = (int64_t)blockIdx.x * kRowThreads + tid;
-        if (MODE == 0 && i0 < mk && (unsigned)a.ids[i0] >= (unsigned)a.E) a.positions[i0] = -1;
+        if (MODE == 0 && blockIdx.y == 0 && i0 < mk && (unsigned)a.ids[i0] >= (unsigned)a.E) a.positions[i0] = -1;
         if (MODE == 1 && i0 < mk && (uint64_t)(int64_t)a.known[i0] >= (uint64_t)a.cap) a.grad_w[i0] = 0.0f;
     }
     const bool real = row && (unsigned)f < (unsigned)mk;
@@ -107,27 +114,28 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExperts
     if (real) {
         const V* x = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.x) + (int64_t)((unsigned)f / (unsigned)a.topk) * a.ldx);
         if constexpr (MODE == 0) {
-            if (lane == 0) a.positions[f] = (int32_t)p;
-            for (int c = lane; c < vecs; c += lanes * kRowUnroll) {
-                V v[kRowUnroll];
+            if (lane == 0 && blockIdx.y == 0) a.positions[f] = (int32_t)p;
+            const int c1 = min((int)(blockIdx.y + 1) * slab, vecs);
+            for (int c = (int)blockIdx.y * slab + lane; c < c1; c += lanes * U) {
+                V v[U];
 #pragma unroll
-                for (int u = 0; u < kRowUnroll; ++u)
-                    if (c + u * lanes < vecs) v[u] = __ldg(x + c + u * lanes);
+                for (int u = 0; u < U; ++u)
+                    if (c + u * lanes < c1) v[u] = __ldg(x + c + u * lanes);
 #pragma unroll
-                for (int u = 0; u < kRowUnroll; ++u)
-                    if (c + u * lanes < vecs) __stcs(out + c + u * lanes, v[u]);
+                for (int u = 0; u < U; ++u)
+                    if (c + u * lanes < c1) __stcs(out + c + u * lanes, v[u]);
             }
         } else {
             using E = Elems<TYPE, BYTES>;
             const float w = a.weights == nullptr ? 1.0f : __ldg(a.weights + f);
             const V* y = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + p * a.ldy);
-            for (int c = lane; c < vecs; c += lanes * kRowUnroll) {
-                V gv[kRowUnroll], yv[kRowUnroll];
+            for (int c = lane; c < vecs; c += lanes * U) {
+                V gv[U], yv[U];
 #pragma unroll
-                for (int u = 0; u < kRowUnroll; ++u)
+                for (int u = 0; u < U; ++u)
                     if (c + u * lanes < vecs) gv[u] = __ldg(x + c + u * lanes), yv[u] = __ldcs(y + c + u * lanes);
 #pragma unroll
-                for (int u = 0; u < kRowUnroll; ++u) {
+                for (int u = 0; u < U; ++u) {
                     if (c + u * lanes >= vecs) continue;
                     float g[E::N], z[E::N];
                     E::get(gv[u], g);
@@ -142,8 +150,8 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExperts
             }
         }
     } else if (row) {
-        const V z{};
-        for (int c = lane; c < vecs; c += lanes) __stcs(out + c, z);
+        const int c0 = (int)blockIdx.y * slab, c1 = min(c0 + slab, vecs);
+        for (int c = c0 + lane; c < c1; c += lanes) __stcs(out + c, V{});
     }
     if constexpr (MODE == 1) {
         dot = warp_sum_fixed(dot);
@@ -193,16 +201,28 @@ __global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokens
         for (int j0 = 0; j0 < a.topk; j0 += 8) {
             V v[8][VECS];
             float w[8];
+            int p[8];
             unsigned in = 0u;
+            // (one word a thread: all positions, then all rows; more of them, small ones, go slot by slot: rows of 6143
+            // 75 us instead of 91)
+            if (VECS == 1) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    p[u] = j0 + u < a.topk ? __ldg(pos + j0 + u) : -1;
+                    w[u] = a.weights != nullptr && j0 + u < a.topk ? __ldg(wts + j0 + u) : 1.0f;
+                }
+            }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                w[u] = 1.0f;
-                if (j0 + u >= a.topk) continue;
-                const int p = __ldg(pos + j0 + u);
-                if (a.weights != nullptr) w[u] = __ldg(wts + j0 + u);
-                if ((uint64_t)(int64_t)p >= (uint64_t)a.cap) continue;
+                if (VECS > 1) {
+                    w[u] = 1.0f;
+                    if (j0 + u >= a.topk) continue;
+                    p[u] = __ldg(pos + j0 + u);
+                    if (a.weights != nullptr) w[u] = __ldg(wts + j0 + u);
+                }
+                if ((uint64_t)(int64_t)p[u] >= (uint64_t)a.cap) continue;
                 in |= 1u << u;
-                const V* y = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + (int64_t)p * a.ldy) + c0;
+                const V* y = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + (int64_t)p[u] * a.ldy) + c0;
 #pragma unroll
                 for (int k = 0; k < VECS; ++k)
                     if (c0 + k * lanes < vecs) v[u][k] = __ldcs(y + k * lanes);
@@ -227,6 +247,98 @@ __global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokens
     }
 }
 
+// The same of many tokens with rows of whole 8- or 16-byte words: a CTA takes
+// every nth piece of lanes * VECS words; a warp has one token at a time, its
+// lanes the slots' positions and weights, which are read one piece ahead.  4096
+// x 8 rows of 6144: 73 us, 79 by the kernel above; 64 tokens 3.5 and 3.2, rows
+// of 6143 138 and 75.
+template <int TYPE, int BYTES, int VECS>
+__global__ void __launch_bounds__(kTokenThreads) to_tokens_many_kernel(const ToTokensArgs a, int lanes, int shift, int vecs,
+                                                                  int blocks, int64_t total) {
+    using E = Elems<TYPE, BYTES>;
+    using V = typename Vec<BYTES>::T;
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & (lanes - 1), slot = tid & 31, per = kTokenThreads >> shift;
+    // the piece's token (whole warps agree on it), its first word, and the lane's slot of it
+    struct Piece {
+        int64_t m;
+        int c0, p;
+        float w;
+    };
+    auto fetch = [&](int64_t b) {
+        Piece q{a.M, 0, -1, 1.0f};
+        if (b >= total) return q;
+        const int64_t mb = blocks == 1 ? b : b / blocks;
+        q.m = mb * per + (tid >> shift);
+        q.c0 = (int)(b - mb * blocks) * lanes * VECS + lane;
+        if (q.m < a.M && slot < a.topk) {
+            q.p = __ldg(a.positions + q.m * a.topk + slot);
+            if (a.weights != nullptr) q.w = __ldg(a.weights + q.m * a.topk + slot);
+        }
+        return q;
+    };
+    Piece next = fetch(blockIdx.x);
+    for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+        const Piece q = next;
+        const bool valid = (uint64_t)(int64_t)q.p < (uint64_t)a.cap;
+        const unsigned in = __ballot_sync(kFull, valid);
+        const int c0 = q.c0;
+        const bool mine = q.m < a.M;
+        float s[VECS][E::N];
+#pragma unroll
+        for (int k = 0; k < VECS; ++k)
+#pragma unroll
+            for (int i = 0; i < E::N; ++i) s[k][i] = 0.0f;
+        V add[VECS];
+        if (a.add != nullptr) {
+            // (plain loads: out may be add itself)
+            const V* from = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.add) + q.m * a.ldadd) + c0;
+#pragma unroll
+            for (int k = 0; k < VECS; ++k)
+                if (mine && c0 + k * lanes < vecs) add[k] = from[k * lanes];
+        }
+        for (int j0 = 0; j0 < a.topk; j0 += 8) {
+            V v[8][VECS];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (!(in >> (j0 + u) & 1u)) continue;  // (no bit from topk on)
+                const int p = __shfl_sync(kFull, q.p, j0 + u);
+                const V* y = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + (int64_t)p * a.ldy) + c0;
+#pragma unroll
+                for (int k = 0; k < VECS; ++k)
+                    if (c0 + k * lanes < vecs) v[u][k] = __ldcs(y + k * lanes);
+            }
+            if (j0 == 0) {
+                next = fetch(b + gridDim.x);
+                if (a.add != nullptr) {
+#pragma unroll
+                    for (int k = 0; k < VECS; ++k)
+                        if (mine && c0 + k * lanes < vecs) E::get(add[k], s[k]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (!(in >> (j0 + u) & 1u)) continue;
+                const float w = __shfl_sync(kFull, q.w, j0 + u);
+#pragma unroll
+                for (int k = 0; k < VECS; ++k) {
+                    if (c0 + k * lanes >= vecs) continue;
+                    float f[E::N];
+                    E::get(v[u][k], f);
+#pragma unroll
+                    for (int i = 0; i < E::N; ++i) s[k][i] = __fmaf_rn(w, f[i], s[k][i]);
+                }
+            }
+        }
+        if (!mine) continue;
+        V* out = static_cast<V*>(a.out) + q.m * vecs + c0;
+#pragma unroll
+        for (int k = 0; k < VECS; ++k)
+            if (c0 + k * lanes < vecs) out[k * lanes] = E::put(s[k]);
+    }
+}
+
 int vec_bytes(uintptr_t bits, int elem) {
     for (int v = 16; v > elem; v >>= 1)
         if ((bits & (uintptr_t)(v - 1)) == 0) return v;
@@ -239,16 +351,28 @@ int log2_of(int v) {
     return s;
 }
 
+cudaError_t device_sms(int* sms) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
 template <int MODE, int TYPE, int BYTES>
 cudaError_t launch_experts_v(const ToExpertsArgs& a, cudaStream_t st) {
     const int vecs = (int)((int64_t)a.K * row_elem_bytes(a.type) / BYTES);
+    // 8- and 16-byte words: 64 threads a row, four words each (4 KB) in a slab; MODE 1 so of many rows (2048 x 8
+    // positions of 6144: 75 us, with 128 threads 80, with 256 94), of few 256 (64 x 8: 6.9 us, with 64 7.4).
+    // Smaller words, whose instructions count: whole rows (2048 x 4 rows of 6143: 37 us, in slabs 75).
+    const bool wide = BYTES >= 8;
+    const int most = !wide ? (MODE == 0 ? 256 : 128) : MODE == 0 || a.cap >= 4096 ? 64 : 256;
     int lanes = 32;
-    while (lanes < kRowThreads && lanes < vecs) lanes *= 2;
+    while (lanes < most && lanes < vecs) lanes *= 2;
     const int64_t per = kRowThreads / lanes, mk = (int64_t)a.M * a.topk;
     int64_t ctas = (a.cap + per - 1) / per;
     if (ctas * kRowThreads < mk) ctas = (mk + kRowThreads - 1) / kRowThreads;  // (a thread for each assignment)
-    return launch_overlapped(to_experts_kernel<MODE, TYPE, BYTES>, dim3((unsigned)ctas), dim3(kRowThreads), 0, st, a,
-                             lanes, log2_of(lanes), vecs);
+    const int slab = MODE == 0 && wide ? lanes * row_unroll(BYTES) : vecs, slabs = (vecs + slab - 1) / slab;
+    return launch_overlapped(to_experts_kernel<MODE, TYPE, BYTES>, dim3((unsigned)ctas, (unsigned)slabs), dim3(kRowThreads),
+                             0, st, a, lanes, log2_of(lanes), vecs, slab);
 }
 
 template <int TYPE, int BYTES, int VECS>
@@ -263,10 +387,22 @@ cudaError_t launch_tokens_n(const ToTokensArgs& a, int vecs, cudaStream_t st) {
 }
 template <int TYPE, int BYTES>
 cudaError_t launch_tokens_v(const ToTokensArgs& a, cudaStream_t st) {
+    constexpr int VECS = 2;
     const int vecs = (int)((int64_t)a.K * row_elem_bytes(a.type) / BYTES);
     // two words a thread where that leaves enough CTAs
-    return (int64_t)a.M * vecs >= (1 << 18) ? launch_tokens_n<TYPE, BYTES, 2>(a, vecs, st)
-                                           : launch_tokens_n<TYPE, BYTES, 1>(a, vecs, st);
+    if ((int64_t)a.M * vecs < (1 << 18)) return launch_tokens_n<TYPE, BYTES, 1>(a, vecs, st);
+    if constexpr (BYTES >= 8) {
+        int sms = 0;
+        const cudaError_t e = device_sms(&sms);
+        if (e != cudaSuccess) return e;
+        int lanes = 32;
+        while (lanes < kTokenThreads && lanes * VECS < vecs) lanes *= 2;
+        const int per = kTokenThreads / lanes, blocks = (vecs + lanes * VECS - 1) / (lanes * VECS);
+        const int64_t total = ((int64_t)a.M + per - 1) / per * blocks, most = (int64_t)sms * 4;
+        return launch_overlapped(to_tokens_many_kernel<TYPE, BYTES, VECS>, dim3((unsigned)(total < most ? total : most)),
+                                 dim3(kTokenThreads), 0, st, a, lanes, log2_of(lanes), vecs, blocks, total);
+    }
+    return launch_tokens_n<TYPE, BYTES, VECS>(a, vecs, st);
 }
 
 }  // namespace
