@@ -311,48 +311,65 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             for (int c = 0; c < MC; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
+            // batches of two chunks: one is read while the one before is added, the last of a buffer (which is given
+            // back once it is in registers) while the next buffer is asked for
+            constexpr int N = D * MC, NB = (N + 1) / 2;
+            uint32_t v[2][2][16];
+            float s0[D], s1[D];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) v[0][i][q] = v[1][i][q] = 0u;
+#pragma unroll
+            for (int b = 0; b < D; ++b) s0[b] = s1[b] = 0.0f;
+            auto add = [&](int i) {
+#pragma unroll
+                for (int j = 2 * i; j < 2 * i + 2 && j < N; ++j) {
+                    const int b = j / MC, c = j % MC;
+                    const float s = c < turn ? s0[b] : s1[b];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        acc[c][q] = __fmaf_rn(__uint_as_float(v[i & 1][j & 1][q]), s, acc[c][q]);
+                }
+            };
             for (int ki = k0; ki < k1; ki += D) {
-                if (!ex_wait_cta(tfull0 + 8u * buf, bph, a.wait_ns, &s_abort)) {
+                const bool ready = mbar_peek_cta(tfull0 + 8u * buf, bph);
+                add(NB - 1);  // of the buffer before (of none: zeros)
+                if (!__all_sync(kFull, ready) && !ex_wait_cta(tfull0 + 8u * buf, bph, a.wait_ns, &s_abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + lanes + (uint32_t)(buf * D * a.n + c0 * 16);
-                float s0[D], s1[D];
-                // up to four chunks on their way at a time
-                constexpr int N = D * MC;
+                auto read = [&](int i) {
 #pragma unroll
-                for (int i0 = 0; i0 < N; i0 += 4) {
-                    uint32_t v[4][16];
+                    for (int j = 2 * i; j < 2 * i + 2 && j < N; ++j)
+                        ex_ld16_async(v[i & 1][j & 1], d + (uint32_t)(j / MC * a.n) + 16u * (j % MC));
+                };
+                read(0);
 #pragma unroll
-                    for (int i = i0; i < i0 + 4 && i < N; ++i)
-                        ex_ld16_async(v[i - i0], d + (uint32_t)(i / MC * a.n) + 16u * (i % MC));
-                    if (i0 == 0) {
+                for (int b = 0; b < D; ++b) s0[b] = p0[(buf * D + b) * 384], s1[b] = p1[(buf * D + b) * 384];
 #pragma unroll
-                        for (int b = 0; b < D; ++b) s0[b] = p0[(buf * D + b) * 384], s1[b] = p1[(buf * D + b) * 384];
-                    }
+                for (int i = 0; i < NB; ++i) {
                     ex_ld_wait();
-                    if (i0 + 4 >= N) {  // (the last ones are in registers)
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            // (relaxed: the accumulators were read, nothing written is passed on)
-                            if (PAIR) mbar_arrive_remote(mfree + 8u * buf);
-                            mbar_arrive(tempty0 + 8u * buf);
-                        }
+                    ex_ld_tie(v[i & 1][0]);
+                    if (2 * i + 1 < N) ex_ld_tie(v[i & 1][1]);
+                    if (i + 1 < NB) {
+                        read(i + 1);
+                        add(i);
+                        continue;
                     }
-#pragma unroll
-                    for (int i = i0; i < i0 + 4 && i < N; ++i) {
-                        const int b = i / MC, c = i % MC;
-                        ex_ld_tie(v[i - i0]);
-                        const float s = c < turn ? s0[b] : s1[b];
-#pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            acc[c][q] = __fmaf_rn(__uint_as_float(v[i - i0][q]), s, acc[c][q]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        // (relaxed: the accumulators were read, nothing written is passed on)
+                        if (PAIR) mbar_arrive_remote(mfree + 8u * buf);
+                        mbar_arrive(tempty0 + 8u * buf);
                     }
                 }
                 if (++buf == a.nbuf) buf = 0, bph ^= 1u;
             }
+            if (ok) add(NB - 1);
             if (SPLIT) {
                 // every CTA's products are done, so its ring's room is free: [sender][its chunks of mine][16][128]
                 ex_cluster_meet();

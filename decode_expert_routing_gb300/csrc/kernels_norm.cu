@@ -189,7 +189,7 @@ __device__ __forceinline__ float norm_rstd(Two sum, int K, float eps) {
 }
 
 template <int C, int FMT, int T>
-__global__ void __launch_bounds__(T, T == 256 && C == 3 ? 5 : 1) add_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(T, T == 256 && C == 3 && FMT == 3 ? 5 : 1) add_norm_kernel(const NormArgs a) {
     __shared__ float s_hi[32], s_lo[32], s_rstd;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
     const int vpr = a.K / 8;

@@ -74,6 +74,19 @@ __device__ __forceinline__ bool ex_wait_cta(uint32_t bar, unsigned parity, unsig
         if (__any_sync(kFull, *abort != 0)) return false;
     }
 }
+// The phase's state now, as a lane sees it, without waiting for it.  (Nothing that
+// the phase publishes may be read before the answer has been looked at.)
+__device__ __forceinline__ bool mbar_peek_cta(uint32_t bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // One lane of a converged warp, always the same one.
 __device__ __forceinline__ bool ex_elect() {
     uint32_t p;
