@@ -133,6 +133,12 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         tma_prefetch_map(&a.tm_x);
         tma_prefetch_map(&a.tm_w);
     }
+    if (warp == 3) {
+        // the weight's way to L2 while the kernel before ends: the first stages
+        const int t0 = (int)(blockIdx.x / (SPLIT ? a.slices : PAIR ? 2 : 1)) / a.RT;
+        const int k = (SPLIT ? (int)cluster_rank() * a.slice_len : 0) + lane;
+        if (lane < a.nst * D && k < a.KI) ex_prefetch_2d(&a.tm_w, k * 128, t0 * a.n + rank * (a.n / 2));
+    }
     if (warp == 1) {
         if (PAIR) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))

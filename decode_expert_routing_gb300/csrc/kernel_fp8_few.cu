@@ -68,12 +68,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) fp8_few_kernel(const __grid
         tma_prefetch_map(&a.tm_x);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // this warp's blocks: warp, warp + 8, ...; its i-th is in stage i % nst
+    const int mine = (a.KI - warp + kFewWarps - 1) / kFewWarps;  // (may be negative or 0: none)
+    // the weight's way to L2 while the kernel before ends
+    if (lane < min(mine, a.nst)) ex_prefetch_2d(&a.tm_w, (warp + lane * kFewWarps) * 128, r0);
     __syncthreads();
     pdl_trigger();
     pdl_wait();
 
-    // this warp's blocks: warp, warp + 8, ...; its i-th is in stage i % nst
-    const int mine = (a.KI - warp + kFewWarps - 1) / kFewWarps;  // (may be negative or 0: none)
     const uint32_t lead = ex_elect() ? 1u : 0u;
     auto copy = [&](int i, int st) {
         const uint32_t at = base + (uint32_t)st * stage, bar = full + 8u * st;

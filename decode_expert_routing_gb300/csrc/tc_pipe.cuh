@@ -174,4 +174,13 @@ __device__ __forceinline__ void ex_load_2d(uint32_t lead, uint32_t dst, const vo
         : "memory");
 }
 
+// The same tile into L2 alone, by the calling lane.  Nothing is read by the kernel: it may
+// come before the wait for the kernel launched before, whatever that one writes.
+__device__ __forceinline__ void ex_prefetch_2d(const void* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<unsigned long long>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 }  // namespace mr
