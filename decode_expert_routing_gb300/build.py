@@ -20,8 +20,8 @@ LIB = os.path.join(HERE, "libmoe_route.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["abi.cu", "kernels_gemv.cu", "kernels_aux.cu", "kernel_route.cu", "kernel_route_spw6.cu",
-           "kernel_route_spw7.cu", "kernel_tc_gemv.cu", "kernel_expert.cu", "kernel_fp8.cu", "kernel_fp8_few.cu", "kernels_norm.cu",
-           "kernels_rows.cu", "noalloc.cu"]
+           "kernel_route_spw7.cu", "kernel_tc_gemv.cu", "kernel_expert.cu", "kernel_fp8.cu",
+           "kernel_fp8_few.cu", "kernels_norm.cu", "kernels_rows.cu", "noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # No --use_fast_math: the quantiser and the sigmoid recipe need IEEE rounding
 # and subnormals (no flush to zero).

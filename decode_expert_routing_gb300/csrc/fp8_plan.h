@@ -31,25 +31,30 @@ inline int fp8_depth(bool pair, int xrows, int n) {
     const int block = (xrows + n) * 128, room = fp8_room(xrows);
     return pair ? 1 : n <= 64 && room / (4 * block) >= 4 ? 4 : n <= 128 && room / (2 * block) >= 4 ? 2 : 1;
 }
-inline int fp8_chunks(int n, int D) {  // of 16 columns, of a read-back warp (three groups)
-    const int mc = (n / 16 + 2) / 3;
-    return D == 1 && mc < 3 ? 3 : mc;
+inline int fp8_chunks(int n, int D) {  // of 16 columns, of a read-back warp (two groups)
+    const int mc = (n / 16 + 1) / 2;
+    return D > 1 ? mc : mc <= 4 ? 4 : mc <= 6 ? 6 : 7;
 }
-// Cycles of a block of K in one CTA, as measured: the read-back, by its chunks
-// and by how many blocks share its waits (48 columns, four blocks: 264; 96, two:
-// 650; 192, one: 1140; 192 of a pair: 850, fewer columns no less), or the
-// bytes' way from L2 (48 columns of 128 rows: 450).
+// Cycles of a block of K in one CTA, fitted to the times of every tile and
+// number of slices at 12 sizes: the read-back, by its chunks and by how many
+// blocks share its waits (four blocks of 48 columns 305, two of 96 460, one of
+// 128 570, of 192 810; pairs of 176 750, of 224 820), or the bytes' way from L2,
+// 51 a cycle (128 rows and 48 columns: 440).
 inline int fp8_block_cycles(bool pair, int xrows, int n) {
-    if (pair) return 850;
-    const int D = fp8_depth(false, xrows, n), read = 30 + 230 * fp8_chunks(n, D) + 60 * (4 / D - 1);
-    const int l2 = (xrows + n) * 128 / 50;
+    if (pair) return 400 + 2 * n;
+    const int D = fp8_depth(false, xrows, n), mc = fp8_chunks(n, D), l2 = (xrows + n) * 5 / 2;
+    const int read = D == 4 ? 125 + 90 * mc : D == 2 ? 220 + 80 * mc : 90 + 120 * mc;
     return read > l2 ? read : l2;
 }
-// The tile and slices whose rounds cost least.  Handing the sums over costs
-// 2000 cycles and 12 a column.  40 x 1536 x 6144: 48 columns in 4 slices 6.9 us,
-// 16 in one 8.8; 64 x 6144 x 6144: 48 in one 12.7, 96 in two 12.6, 64 in one
-// 14.4; 200 x 6144 x 6144: 176 in two 16.5, 96 in one 21.3; 300 x 2000 x 2976:
-// 48 in one 8.4, 96 in two 9.1.
+// What a call costs besides: a pair's start, and handing the slices' sums over.
+inline int fp8_call_cycles(bool pair, int n, int slices) {
+    return pair ? 1500 : slices > 1 ? 37 * n + 520 * slices : 0;
+}
+// The tile and slices whose rounds cost least.  40 x 1536 x 6144: 32 columns in
+// two slices 6.7 us, 48 in four 7.0, 16 in one 8.3; 40 x 6144 x 6144: 48 in one
+// 10.9, 96 in two 12.0; 64 x 6144 x 6144: 96 in two 11.9, 64 in one 12.6; 200 x
+// 6144 x 6144: 176 in two 16.1, 112 in one 18.1; 4096 x 6144 x 6144 by pairs: 224
+// columns 125 us, 192 135.
 inline Fp8Plan fp8_plan(int M, int R, int K, int sms) {
     Fp8Plan p{};
     const int KI = (K + 127) / 128;
@@ -57,7 +62,7 @@ inline Fp8Plan fp8_plan(int M, int R, int K, int sms) {
     for (int pair = 0; pair <= (M > 128 && sms >= 2 ? 1 : 0); ++pair) {
         const int of = 1 + pair, slots = sms / of, rt = (M + 128 * of - 1) / (128 * of);
         const int xrows = M >= 128 ? 128 : (M + 7) / 8 * 8;
-        for (int n = 192; n >= (pair ? 128 : 16); n -= 16 * of) {
+        for (int n = 224; n >= (pair ? 128 : 16); n -= 16 * of) {
             const int ct = (R + n - 1) / n;
             const int64_t tiles = (int64_t)rt * ct;
             for (int s = 1; s <= (pair ? 1 : 8); s *= 2) {
@@ -65,7 +70,8 @@ inline Fp8Plan fp8_plan(int M, int R, int K, int sms) {
                 const int len = s == 1 ? KI : ((KI + s - 1) / s + 3) / 4 * 4;
                 if (s > 1 && (tiles * s > sms || len * (s - 1) >= KI)) break;
                 const int64_t rounds = (tiles * s + slots - 1) / slots;
-                const int64_t cost = rounds * len * fp8_block_cycles(pair != 0, xrows, n) + (s > 1 ? 2000 + 12 * n : 0);
+                const int64_t cost =
+                    rounds * len * fp8_block_cycles(pair != 0, xrows, n) + fp8_call_cycles(pair != 0, n, s);
                 if (cost >= least) continue;
                 least = cost;
                 p.pair = pair, p.n = n, p.xrows = xrows, p.RT = rt, p.CT = ct, p.slices = s, p.slice_len = len;

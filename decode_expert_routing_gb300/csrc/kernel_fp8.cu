@@ -12,7 +12,21 @@
 // Work: persistent CTAs (or pairs of two with cta_group::2) walk the tiles of
 // 128 (256) rows of x times n rows of w, row tiles fastest.  Warp 0 copies
 // (tensor maps, 128-byte swizzle, a block of 128 bytes a row per stage), warp 1
-// issues the products, warps 2-3 prepare the scales, warps 4-15 read back.
+// issues the products, warps 2-3 prepare the scales, warps 4-11 read back, each
+// group of four half of the columns.  (Three groups of a third: 134.7 -> 136.5
+// us at 4096 x 6144 x 6144 with 192 columns, and 224 have no registers, four:
+// 142.  One group that reads what another adds later: 153.)  Few rows leave
+// most of this idle, so tiles become narrow, stages and buffers take up to four
+// blocks (one wait for all of them), products up to 64 rows are of 64, and
+// where tiles are still fewer than SMs a cluster shares their K range.
+//
+// What bounds it: of 4096 x 6144 x 6144 (125 us, 2480 TFLOP/s, 1.25 of the
+// bf16 rate measured here) a pair's block of K of 224 columns takes 820 cycles:
+// 448 for the products, 600 for its bytes' way from L2, 224 each to read tensor
+// memory and to add; the read-back's waits at both ends of a buffer join them.
+// Below 128 rows it is the weight: 64 x 6144 x 6144 11.8 us (3.3 TB/s), 40 x
+// 1536 x 6144 6.7 us, most of it start, first bytes and the sums' way through
+// the cluster.
 #include "../../include/moe_route.h"
 #include "fp8_plan.h"
 #include "internal.h"
@@ -21,7 +35,7 @@
 
 namespace mr {
 
-constexpr int kF8Threads = 512;
+constexpr int kF8Threads = 384;
 
 struct Fp8Args {
     CUtensorMap tm_x, tm_w;  // boxes of xrows and n (pair: n / 2) rows x 128 bytes
@@ -102,13 +116,14 @@ __device__ __forceinline__ void f8_store(const Fp8Args& a, int64_t m, int col, c
 }
 
 // D: blocks of a stage and of a buffer (those behind K are zeros); MC: chunks
-// of 16 columns that a read-back warp takes, a third of them rounded up.
+// of 16 columns that a read-back warp takes, half of them rounded up.
 // SPLIT: the CTAs of a cluster (one tile each cluster) share its K range, and
 // add their sums in K order, every CTA those of the chunks that it owns.
 template <bool PAIR, int D, int MC, bool SPLIT>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Args a) {
     extern __shared__ __align__(16) unsigned char dsm[];
-    __shared__ __align__(8) unsigned long long s_full[kF8MaxStages], s_empty[kF8MaxStages], s_tfull[8], s_tempty[8], s_mfree[8], s_drain;
+    __shared__ __align__(8) unsigned long long s_full[kF8MaxStages], s_empty[kF8MaxStages];
+    __shared__ __align__(8) unsigned long long s_tfull[8], s_tempty[8], s_mfree[8], s_drain;
     // of the blocks in the accumulator buffers: a row's scale times that of each block of w's rows in the tile
     __shared__ float s_scale[8][3][128];
     __shared__ uint32_t s_tmem;
@@ -122,8 +137,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         mbar_init(empty0 + 8u * tid, 1);
         if (tid < 8) {
             mbar_init(tfull0 + 8u * tid, 3);  // the products, and two warps' scales
-            mbar_init(tempty0 + 8u * tid, 12);
-            mbar_init(smem_u32(&s_mfree[tid]), 24);  // (pair) both CTAs' buffers are free
+            mbar_init(tempty0 + 8u * tid, 8);
+            mbar_init(smem_u32(&s_mfree[tid]), 16);  // (pair) both CTAs' buffers are free
         }
         if (tid == 8) mbar_init(smem_u32(&s_drain), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -167,137 +182,139 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     unsigned ph = 0;  // its phase
     int buf = 0;      // accumulator buffer
     unsigned bph = 0;
-    const int64_t first = SPLIT ? blockIdx.x / a.slices : blockIdx.x / of, step = SPLIT ? gridDim.x / a.slices : gridDim.x / of;
+    const int64_t first = blockIdx.x / (SPLIT ? a.slices : of), step = gridDim.x / (SPLIT ? a.slices : of);
     const int slice = SPLIT ? (int)cluster_rank() : 0;
     const int k0 = SPLIT ? slice * a.slice_len : 0, k1 = SPLIT ? min(a.KI, k0 + a.slice_len) : a.KI;
     const bool half = !PAIR && a.xrows <= 64;  // products of 64 rows: four times 16 lanes
     const uint32_t lead = ex_elect() ? 1u : 0u;  // (whole warps up to here)
 
     bool met = false;
-    // registers of the warps that copy and issue for those that keep sums: 128 x 56 + 384 x 152 of the 512 x 128
+    // registers of the warps that copy and issue for those that keep sums: 128 x 56 + 256 x 216 of the 384 x 168
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0) {
-        // ---- copies
-        int issued = 0;
-        bool ok = true;
-        for (int64_t t = first; ok && t < a.tiles; t += step) {
-            const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT);
-            const int m0 = (rt * of + rank) * 128, w0 = ct * a.n + rank * (a.n / of);
-            for (int ki = k0; ki < k1; ki += D) {
-                if (!ex_wait_cta(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t full = full0 + 8u * st, at = base + (uint32_t)st * stage_bytes;
-                ex_expect(lead, full, stage_bytes + (((a.flags & 2) && issued == 0) ? 16u : 0u));
-#pragma unroll
-                for (int b = 0; b < D; ++b) {
-                    ex_load_2d(lead, at + b * block_bytes, &a.tm_w, (ki + b) * 128, w0, full);
-                    ex_load_2d(lead, at + b * block_bytes + wbytes, &a.tm_x, (ki + b) * 128, m0, full);
-                }
-                ++issued;
-                if (++st == a.nst) st = 0, ph ^= 1u;
-            }
-        }
-        // after a wait that ran out: no copy stays in flight (bounded)
-        if (!ok && lane == 0) {
-            for (int i = 0; i < min(issued, a.nst); ++i) {
-                if (--st < 0) st = a.nst - 1, ph ^= 1u;
-                const unsigned long long t0 = global_ns();
-                while (!mbar_try_wait(full0 + 8u * st, ph) && global_ns() - t0 < a.wait_ns / 16 + 1000) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            // ---- copies
+            int issued = 0;
+            bool ok = true;
+            for (int64_t t = first; ok && t < a.tiles; t += step) {
+                const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT);
+                const int m0 = (rt * of + rank) * 128, w0 = ct * a.n + rank * (a.n / of);
+                for (int ki = k0; ki < k1; ki += D) {
+                    if (!ex_wait_cta(empty0 + 8u * st, ph ^ 1u, a.wait_ns, &s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = full0 + 8u * st, at = base + (uint32_t)st * stage_bytes;
+                    ex_expect(lead, full, stage_bytes + (((a.flags & 2) && issued == 0) ? 16u : 0u));
+    #pragma unroll
+                    for (int b = 0; b < D; ++b) {
+                        ex_load_2d(lead, at + b * block_bytes, &a.tm_w, (ki + b) * 128, w0, full);
+                        ex_load_2d(lead, at + b * block_bytes + wbytes, &a.tm_x, (ki + b) * 128, m0, full);
+                    }
+                    ++issued;
+                    if (++st == a.nst) st = 0, ph ^= 1u;
                 }
             }
-        }
-    } else if (warp == 1 && PAIR && rank == 1) {
-        // ---- a pair's products are issued by its first CTA: told when this CTA's operands are in place
-        bool ok = true;
-        const uint32_t peer = map_rank(full0, 0);
-        for (int64_t t = first; ok && t < a.tiles; t += step) {
-            for (int ki = k0; ki < k1; ki += D) {
-                if (!ex_wait_cta(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
-                    ok = false;
-                    break;
+            // after a wait that ran out: no copy stays in flight (bounded)
+            if (!ok && lane == 0) {
+                for (int i = 0; i < min(issued, a.nst); ++i) {
+                    if (--st < 0) st = a.nst - 1, ph ^= 1u;
+                    const unsigned long long t0 = global_ns();
+                    while (!mbar_try_wait(full0 + 8u * st, ph) && global_ns() - t0 < a.wait_ns / 16 + 1000) {
+                    }
                 }
-                if (ex_elect()) mbar_arrive_remote_shared(peer + 8u * st);
-                __syncwarp();
-                if (++st == a.nst) st = 0, ph ^= 1u;
             }
-        }
-    } else if (warp == 1) {
-        // ---- products, a stage's blocks side by side into each buffer in turn
-        bool ok = true;
-        const uint32_t idesc = f8_idesc(half ? 64 : 128 * of, a.n), mfree0 = PAIR ? smem_u32(&s_mfree[0]) : tempty0;
-        for (int64_t t = first; ok && t < a.tiles; t += step) {
-            for (int ki = k0; ki < k1; ki += D) {
-                // (a pair's stage is in the peer's memory too.  The buffer last: it is the one that is waited for)
-                if (!(PAIR ? ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)
-                           : ex_wait_cta(full0 + 8u * st, ph, a.wait_ns, &s_abort)) ||
-                    !ex_wait_cta(mfree0 + 8u * buf, bph ^ 1u, a.wait_ns, &s_abort)) {
-                    ok = false;
-                    break;
+        } else if (warp == 1 && PAIR && rank == 1) {
+            // ---- a pair's products are issued by its first CTA: told when this CTA's operands are in place
+            bool ok = true;
+            const uint32_t peer = map_rank(full0, 0);
+            for (int64_t t = first; ok && t < a.tiles; t += step) {
+                for (int ki = k0; ki < k1; ki += D) {
+                    if (!ex_wait_cta(full0 + 8u * st, ph, a.wait_ns, &s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (ex_elect()) mbar_arrive_remote_shared(peer + 8u * st);
+                    __syncwarp();
+                    if (++st == a.nst) st = 0, ph ^= 1u;
                 }
-                tc_fence_after();
-                const uint32_t at = base + (uint32_t)st * stage_bytes, d = tmem + (uint32_t)(buf * D * a.n);
-#pragma unroll
-                for (int b = 0; b < D; ++b) {
-                    const unsigned long long dw = ex_desc(kExDescCodes, at + b * block_bytes);
-                    const unsigned long long dx = ex_desc(kExDescCodes, at + b * block_bytes + wbytes);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        f8_mma<PAIR>(lead, d + (uint32_t)(b * a.n), dx + 2 * j, dw + 2 * j, idesc, j > 0);
+            }
+        } else if (warp == 1) {
+            // ---- products, a stage's blocks side by side into each buffer in turn
+            bool ok = true;
+            const uint32_t idesc = f8_idesc(half ? 64 : 128 * of, a.n), mfree0 = PAIR ? smem_u32(&s_mfree[0]) : tempty0;
+            for (int64_t t = first; ok && t < a.tiles; t += step) {
+                for (int ki = k0; ki < k1; ki += D) {
+                    // (a pair's stage is in the peer's memory too.  The buffer last: it is the one that is waited for)
+                    if (!(PAIR ? ex_wait(full0 + 8u * st, ph, a.wait_ns, &s_abort)
+                               : ex_wait_cta(full0 + 8u * st, ph, a.wait_ns, &s_abort)) ||
+                        !ex_wait_cta(mfree0 + 8u * buf, bph ^ 1u, a.wait_ns, &s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = base + (uint32_t)st * stage_bytes, d = tmem + (uint32_t)(buf * D * a.n);
+    #pragma unroll
+                    for (int b = 0; b < D; ++b) {
+                        const unsigned long long dw = ex_desc(kExDescCodes, at + b * block_bytes);
+                        const unsigned long long dx = ex_desc(kExDescCodes, at + b * block_bytes + wbytes);
+    #pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            f8_mma<PAIR>(lead, d + (uint32_t)(b * a.n), dx + 2 * j, dw + 2 * j, idesc, j > 0);
+                    }
+                    f8_commit<PAIR>(lead, empty0 + 8u * st);
+                    f8_commit<PAIR>(lead, tfull0 + 8u * buf);
+                    if (++st == a.nst) st = 0, ph ^= 1u;
+                    if (++buf == a.nbuf) buf = 0, bph ^= 1u;
                 }
-                f8_commit<PAIR>(lead, empty0 + 8u * st);
-                f8_commit<PAIR>(lead, tfull0 + 8u * buf);
-                if (++st == a.nst) st = 0, ph ^= 1u;
-                if (++buf == a.nbuf) buf = 0, bph ^= 1u;
+            }
+        } else {
+            // ---- scales, a stage's at a time into the slots of the accumulator buffer: each warp those of 64 rows, a
+            // lane two of them
+            const int last = (a.R - 1) >> 7, row = (warp - 2) * 64 + lane;
+            bool ok = true;
+            for (int64_t t = first; ok && t < a.tiles; t += step) {
+                const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT), bt = ct * a.n >> 7;
+                const int64_t m = (int64_t)(rt * of + rank) * 128 + row;
+                const int64_t end = (int64_t)a.M - 1;
+                const float* xs[2] = {a.xs + min(m, end) * a.ldxs, a.xs + min(m + 32, end) * a.ldxs};
+                const float* ws[3];
+    #pragma unroll
+                for (int j = 0; j < 3; ++j) ws[j] = a.ws + (int64_t)min(bt + j, last) * a.ldws;
+                float x[2][D], w[3][D];
+                auto fetch = [&](int ki) {
+    #pragma unroll
+                    for (int b = 0; b < D; ++b) {
+                        const bool in = D == 1 || ki + b < a.KI;  // (behind K: no scale either)
+    #pragma unroll
+                        for (int i = 0; i < 2; ++i) x[i][b] = in ? __ldg(xs[i] + ki + b) : 0.0f;
+    #pragma unroll
+                        for (int j = 0; j < 3; ++j) w[j][b] = in ? __ldg(ws[j] + ki + b) : 0.0f;
+                    }
+                };
+                fetch(k0);
+                for (int ki = k0; ki < k1; ki += D) {
+                    if (!ex_wait_cta(tempty0 + 8u * buf, bph ^ 1u, a.wait_ns, &s_abort)) {
+                        ok = false;
+                        break;
+                    }
+    #pragma unroll
+                    for (int b = 0; b < D; ++b)
+    #pragma unroll
+                        for (int j = 0; j < 3; ++j)
+    #pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                s_scale[buf * D + b][j][row + 32 * i] = __fmul_rn(x[i][b], w[j][b]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tfull0 + 8u * buf);
+                    if (++buf == a.nbuf) buf = 0, bph ^= 1u;
+                    if (ki + D < k1) fetch(ki + D);
+                }
             }
         }
     } else {
-        // ---- scales, a stage's at a time into the slots of the accumulator buffer: each warp those of 64 rows, a lane
-        // two of them
-        const int last = (a.R - 1) >> 7, row = (warp - 2) * 64 + lane;
-        bool ok = true;
-        for (int64_t t = first; ok && t < a.tiles; t += step) {
-            const int ct = (int)(t / a.RT), rt = (int)(t - (int64_t)ct * a.RT), bt = ct * a.n >> 7;
-            const int64_t m = (int64_t)(rt * of + rank) * 128 + row;
-            const float* xs[2] = {a.xs + min(m, (int64_t)a.M - 1) * a.ldxs, a.xs + min(m + 32, (int64_t)a.M - 1) * a.ldxs};
-            const float* ws[3];
-#pragma unroll
-            for (int j = 0; j < 3; ++j) ws[j] = a.ws + (int64_t)min(bt + j, last) * a.ldws;
-            float x[2][D], w[3][D];
-            auto fetch = [&](int ki) {
-#pragma unroll
-                for (int b = 0; b < D; ++b) {
-                    const bool in = D == 1 || ki + b < a.KI;  // (behind K: no scale either)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) x[i][b] = in ? __ldg(xs[i] + ki + b) : 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 3; ++j) w[j][b] = in ? __ldg(ws[j] + ki + b) : 0.0f;
-                }
-            };
-            fetch(k0);
-            for (int ki = k0; ki < k1; ki += D) {
-                if (!ex_wait_cta(tempty0 + 8u * buf, bph ^ 1u, a.wait_ns, &s_abort)) {
-                    ok = false;
-                    break;
-                }
-#pragma unroll
-                for (int b = 0; b < D; ++b)
-#pragma unroll
-                    for (int j = 0; j < 3; ++j)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) s_scale[buf * D + b][j][row + 32 * i] = __fmul_rn(x[i][b], w[j][b]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tfull0 + 8u * buf);
-                if (++buf == a.nbuf) buf = 0, bph ^= 1u;
-                if (ki + D < k1) fetch(ki + D);
-            }
-        }
-    }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-        // ---- scaled sums: three groups of four warps, each a third of the columns
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ---- scaled sums: two groups of four warps, each half of the columns
         // (each takes MC chunks of 16 columns; where they are more than there are, the last ones twice, and stores
         // its own: a read in a branch takes 130 cycles more)
         const int wq = warp & 3, grp = (warp >> 2) - 1, nch = a.n >> 4;
@@ -384,7 +401,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 for (int c = 0; c < MC; ++c) {
                     const int i = c0 + c, owner = i % a.slices;
                     if (c < own || owner == slice) continue;
-                    const uint32_t to = map_rank(base, (unsigned)owner) + (uint32_t)((slice * most + i / a.slices) * 2048 + at) * 4u;
+                    const uint32_t to =
+                        map_rank(base, (unsigned)owner) + (uint32_t)((slice * most + i / a.slices) * 2048 + at) * 4u;
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 512u * q), "f"(acc[c][q]) : "memory");
@@ -403,7 +421,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
                             float x = acc[c][q];
-                            if (z != slice) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(from + 512u * q) : "memory");
+                            if (z != slice)
+                                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(from + 512u * q) : "memory");
                             sum[q] = __fadd_rn(sum[q], x);
                         }
                     }
@@ -482,14 +501,18 @@ cudaError_t launch_single(const Fp8Plan& p, const Fp8Args& a, cudaStream_t st) {
         case 21: return launch_one<false, 2, 1, SPLIT>(a, p.grid, st);
         case 22: return launch_one<false, 2, 2, SPLIT>(a, p.grid, st);
         case 23: return launch_one<false, 2, 3, SPLIT>(a, p.grid, st);
-        case 13: return launch_one<false, 1, 3, SPLIT>(a, p.grid, st);
-        default: return launch_one<false, 1, 4, SPLIT>(a, p.grid, st);
+        case 24: return launch_one<false, 2, 4, SPLIT>(a, p.grid, st);
+        case 14: return launch_one<false, 1, 4, SPLIT>(a, p.grid, st);
+        case 16: return launch_one<false, 1, 6, SPLIT>(a, p.grid, st);
+        default: return launch_one<false, 1, 7, SPLIT>(a, p.grid, st);
     }
 }
 cudaError_t launch_plan(const Fp8Plan& p, const Fp8Args& a, cudaStream_t st) {
     if (p.slices > 1) return launch_single<true>(p, a, st);
     if (!p.pair) return launch_single<false>(p, a, st);
-    return p.mc == 3 ? launch_one<true, 1, 3, false>(a, p.grid, st) : launch_one<true, 1, 4, false>(a, p.grid, st);
+    return p.mc == 4   ? launch_one<true, 1, 4, false>(a, p.grid, st)
+           : p.mc == 6 ? launch_one<true, 1, 6, false>(a, p.grid, st)
+                       : launch_one<true, 1, 7, false>(a, p.grid, st);
 }
 
 }  // namespace

@@ -13,8 +13,12 @@
 // which of the block's products a step adds is the same permutation of k for
 // both operands, and the sum does not depend on it.  (mma.sync on E4M3 itself
 // converts both operands again for every step here: 64 rows of x took 33 us with
-// 6144 x 6144, 12 without the products.  The conversions, three cycles each, are
-// why few means 16.)
+// 6144 x 6144, 12 without the products.)
+//
+// The weight's bytes bound it, and for small ones the start: 1 x 6144 x 6144 7.9
+// us (4.8 TB/s, with the start's 2; the tensor core kernel took 13.1), 1 x 1536 x
+// 6144 5.0, 8 x 6144 x 768 2.8.  The conversions, three cycles each, are why few
+// means 16: 16 x 6144 x 6144 9.3 us, 24 by the other kernel 10.9.
 #include "../../include/moe_route.h"
 #include "fp8_plan.h"
 #include "internal.h"
@@ -102,7 +106,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) fp8_few_kernel(const __grid
     };
     if (mine > 0) fetch(0);
     // bytes of a row's two 16-byte words in a stage: word w of row r is at r * 128 + ((w ^ (r & 7)) << 4)
-    const uint32_t o0 = (uint32_t)g * 128u + (uint32_t)(((2 * t) ^ g) << 4), o1 = (uint32_t)g * 128u + (uint32_t)(((2 * t + 1) ^ g) << 4);
+    const uint32_t o0 = (uint32_t)(g * 128 + (((2 * t) ^ g) << 4)), o1 = (uint32_t)(g * 128 + (((2 * t + 1) ^ g) << 4));
     int st = 0;
     unsigned ph = 0;
     bool ok = true;

@@ -150,13 +150,14 @@ def test_plans_keep_what_the_kernel_relies_on(tmp_path):
     for line in out:
         M, R, K, sms, pair, n, xrows, RT, CT, D, mc, nst, nbuf, grid, slices, len_ = map(int, line.split())
         of = 2 if pair else 1
-        assert n % (16 * of) == 0 and 16 * of <= n <= 192 and (D, n <= {1: 192, 2: 128, 4: 64}[D]) in {(1, True), (2, True), (4, True)}
+        assert n % (16 * of) == 0 and 16 * of <= n <= 224 and (D, n <= {1: 224, 2: 128, 4: 64}[D]) in {(1, True), (2, True), (4, True)}
         # copies: whole groups of 8 rows, no more than the operand's 128, and every row of x has one
         assert xrows % 8 == 0 and 8 <= xrows <= 128 and (xrows == 128 or (M <= xrows and not pair))
         assert RT == -(-M // (128 * of)) and (CT - 1) * n < R <= CT * n
-        # three groups of mc chunks of 16 columns cover the tile, and none is wider than it
-        assert mc <= n // 16 <= 3 * mc and (pair, D, mc) in {
-            (0, 4, 1), (0, 4, 2), (0, 2, 1), (0, 2, 2), (0, 2, 3), (0, 1, 3), (0, 1, 4), (1, 1, 3), (1, 1, 4)}
+        # two groups of mc chunks of 16 columns cover the tile, and none is wider than it
+        assert mc <= n // 16 <= 2 * mc and (pair, D, mc) in {
+            (0, 4, 1), (0, 4, 2), (0, 2, 1), (0, 2, 2), (0, 2, 3), (0, 2, 4), (0, 1, 4), (0, 1, 6), (0, 1, 7), (1, 1, 4),
+            (1, 1, 6), (1, 1, 7)}
         # accumulators and stages (the product reads 128 rows of x whatever was copied)
         assert 2 <= nbuf and nbuf * D <= 8 and nbuf * D * n <= 512
         assert 3 <= nst <= 24 and nst * D * (xrows + n // of) * 128 + (128 - xrows) * 128 + 1024 <= 208 * 1024
