@@ -62,7 +62,8 @@ inline Fp8Plan fp8_plan(int M, int R, int K, int sms) {
     for (int pair = 0; pair <= (M > 128 && sms >= 2 ? 1 : 0); ++pair) {
         const int of = 1 + pair, slots = sms / of, rt = (M + 128 * of - 1) / (128 * of);
         const int xrows = M >= 128 ? 128 : (M + 7) / 8 * 8;
-        for (int n = 224; n >= (pair ? 128 : 16); n -= 16 * of) {
+        // (narrower pairs: twice as many single CTAs are faster)
+        for (int n = 224; n >= (pair ? 160 : 16); n -= 16 * of) {
             const int ct = (R + n - 1) / n;
             const int64_t tiles = (int64_t)rt * ct;
             for (int s = 1; s <= (pair ? 1 : 8); s *= 2) {

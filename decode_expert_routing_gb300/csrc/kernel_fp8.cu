@@ -510,9 +510,7 @@ cudaError_t launch_single(const Fp8Plan& p, const Fp8Args& a, cudaStream_t st) {
 cudaError_t launch_plan(const Fp8Plan& p, const Fp8Args& a, cudaStream_t st) {
     if (p.slices > 1) return launch_single<true>(p, a, st);
     if (!p.pair) return launch_single<false>(p, a, st);
-    return p.mc == 4   ? launch_one<true, 1, 4, false>(a, p.grid, st)
-           : p.mc == 6 ? launch_one<true, 1, 6, false>(a, p.grid, st)
-                       : launch_one<true, 1, 7, false>(a, p.grid, st);
+    return p.mc == 6 ? launch_one<true, 1, 6, false>(a, p.grid, st) : launch_one<true, 1, 7, false>(a, p.grid, st);
 }
 
 }  // namespace

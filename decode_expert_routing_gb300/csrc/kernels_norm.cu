@@ -64,7 +64,7 @@ __device__ __forceinline__ void fp8_scales(const float (&amax)[C], float (&scale
 }
 
 // One warp per 128 chunks of 8 elements (8 groups) of a row, four loads in
-// flight per lane.
+// flight per lane: bytes bound it.
 constexpr int kFp8Threads = 256, kFp8Unroll = 4;
 __global__ void __launch_bounds__(kFp8Threads) fp8_quant_kernel(const uint16_t* x, int64_t ldx, int M, int K,
                                                                 uint8_t* q, float* scale) {
@@ -111,7 +111,11 @@ cudaError_t launch_fp8_quant(const void* x, int64_t ldx, int M, int K, uint8_t* 
 
 // ------------------------------------------------------------------ residual + RMSNorm
 //
-// One CTA per row, the row in registers: C chunks of 8 elements a thread.
+// One CTA per row, the row in registers: C chunks of 8 elements a thread.  Of
+// many rows memory bounds it: 4096 x 6144 with sres and FP8 codes 33 us, 5.4 TB/s,
+// 80 % of a plain copy's rate (a row's CTA reads nothing while it sums; persistent
+// CTAs that load the next row ahead took 41).  Of few the launch, one load's way
+// and the sum's: 1 row 2.6 us, 48 2.9.
 //   sres = bf16(x + residual)
 //   rstd = 1 / sqrt(mean(sres^2) + eps)
 //   xn   = bf16((sres * rstd) * s)      (norm_pair, as the route and mr_norm_apply have it)

@@ -106,12 +106,15 @@ typedef enum mr_quant_format {
  * touches anything else (x, logits, ids, scratch, outputs).  The caller must
  * then not write w in the kernel launched just before the routing call on
  * the same stream (where that one is a call of this library: nor in the one
- * before it).  The expert products are always launched so, whatever the
- * flags; they touch nothing before that wait.  With MR_LAUNCH_LEGACY_MMA the router GEMV of more than
- * 64 rows runs as the split-K GEMV with last-arriver fixup on warp-level
- * mma.sync instead of the tcgen05 cluster kernel (the two sum the split-K
- * partials in different orders, so their logits agree within fp32 rounding,
- * not bit for bit); up to 64 rows it always runs on mma.sync.
+ * before it).  The expert products and the calls behind them in this file
+ * (mr_add_rms_norm to mr_moe_combine_grad) are always launched so, whatever
+ * the flags; they use nothing before that wait (mr_fp8_gemm asks for the first
+ * bytes of w to be brought into L2, where a later write is seen: its weight
+ * may be written by the kernel just before).  With MR_LAUNCH_LEGACY_MMA the
+ * router GEMV of more than 64 rows runs as the split-K GEMV with last-arriver
+ * fixup on warp-level mma.sync instead of the tcgen05 cluster kernel (the two
+ * sum the split-K partials in different orders, so their logits agree within
+ * fp32 rounding, not bit for bit); up to 64 rows it always runs on mma.sync.
  * MR_LAUNCH_TEST_SLOW_SIGMOID (a test of the sigmoid gate, never for
  * production): every exact sigmoid score takes its double-double path
  * instead of the fp64 fast path with its rounding test; the outputs are the
@@ -136,7 +139,8 @@ int mr_get_launch_flags(void);
  * data between the CTAs of a thread-block cluster (split-K partials to the
  * CTA that owns a token, chosen ids to the CTA that sorts).  Each receiving
  * CTA waits for the bytes it expects at most the wait limit (default 1 s);
- * the expert products wait so for their own copies and products.
+ * the expert products and mr_fp8_gemm wait so for their own copies and
+ * products.
  * When a wait runs out the kernel sets a device-side flag and returns early;
  * the outputs of that call are undefined, and after a call with M > 16 the
  * scratch counters must be zeroed again (mr_scratch_reset).
@@ -688,8 +692,8 @@ int mr_add_rms_norm(const mr_add_rms_norm_params *params, void *stream);
  *   scale[m, b] = max(amax / 448, 2^-126),  amax = the group's largest |x|
  *   q[m, k]     = e4m3(x[m, k] * (1 / scale[m, k / 128]))
  * each fp32 step and the codes rounded to nearest even, the codes saturating
- * at 448.  A NaN or an infinity in a group makes what is read back of it (code
- * times scale) NaN.  x: bf16 [M, ldx]; q: [M, K], 8-byte aligned; scale: fp32
+ * at 448.  A NaN or an infinity in a group makes its scale NaN, and with it
+ * what is read back of the group (code times scale).  x: bf16 [M, ldx]; q: [M, K], 8-byte aligned; scale: fp32
  * [M, ceil(K / 128)].  K % 16 == 0, else MR_ERR_UNSUPPORTED.  One launch.
  */
 int mr_fp8_quant(const void *x, int64_t ldx, int M, int K, uint8_t *q, float *scale, void *stream);
@@ -699,9 +703,13 @@ int mr_fp8_quant(const void *x, int64_t ldx, int M, int K, uint8_t *q, float *sc
  * x and one for 128 x 128 of w:
  *   out[m, r] = sum_b x_scale[m, b] w_scale[r / 128, b] sum_{k in b} q[m, k] w[r, k]
  * over the blocks b of 128 along K (the last of each kind may be shorter).
- * The inner sums are those of the tensor core in fp32; the scaled sums are
- * added in fp32 in ascending b, or, where the K range is shared between
- * CTAs, ascending within each share and over the shares.
+ * The inner sums are those of the tensor core in fp32.  The product of the two
+ * scales is rounded to fp32 first, and one fused multiply-add a block adds the
+ * scaled sums in fp32 in ascending b, or, where K is shared out, ascending
+ * within each share and then over the shares: of up to 16 rows eight shares of
+ * every eighth block, else up to eight ranges.  Sizes alone decide which, so a
+ * call repeated gives the same bits; the same row in a batch of another size
+ * may differ by the order of these sums.
  * q: [M, K] with row stride ldq in bytes; w: [R, K] with row stride ldw in
  * bytes; both 16-byte aligned and their strides multiples of 16.  x_scale:
  * fp32 [M, ceil(K / 128)] with row stride ldxs; w_scale: fp32 [ceil(R / 128),

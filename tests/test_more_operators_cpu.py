@@ -156,8 +156,8 @@ def test_plans_keep_what_the_kernel_relies_on(tmp_path):
         assert RT == -(-M // (128 * of)) and (CT - 1) * n < R <= CT * n
         # two groups of mc chunks of 16 columns cover the tile, and none is wider than it
         assert mc <= n // 16 <= 2 * mc and (pair, D, mc) in {
-            (0, 4, 1), (0, 4, 2), (0, 2, 1), (0, 2, 2), (0, 2, 3), (0, 2, 4), (0, 1, 4), (0, 1, 6), (0, 1, 7), (1, 1, 4),
-            (1, 1, 6), (1, 1, 7)}
+            (0, 4, 1), (0, 4, 2), (0, 2, 1), (0, 2, 2), (0, 2, 3), (0, 2, 4), (0, 1, 4), (0, 1, 6), (0, 1, 7), (1, 1, 6),
+            (1, 1, 7)}
         # accumulators and stages (the product reads 128 rows of x whatever was copied)
         assert 2 <= nbuf and nbuf * D <= 8 and nbuf * D * n <= 512
         assert 3 <= nst <= 24 and nst * D * (xrows + n // of) * 128 + (128 - xrows) * 128 + 1024 <= 208 * 1024
