@@ -689,6 +689,16 @@ def _given_stream(device, stream):
     return stream
 
 
+_CUDA = None  # torch's raw CUDA calls, once a prepared call has been made
+
+
+def _cuda_calls():
+    global _CUDA
+    _torch().cuda.init()
+    _CUDA = _torch()._C
+    return _CUDA
+
+
 class _Prepared:
     """A call over fixed buffers: its parameter block is built and checked
     once, and each call is one ABI call on the given (or torch's current)
@@ -743,10 +753,9 @@ class _Prepared:
         """Launch on the buffers' device; stream: a torch stream of that
         device, a raw cudaStream_t (int) of that device, or None (torch's
         current stream there)."""
-        torch = _torch()
-        index = self.device.index
+        c, index = _CUDA or _cuda_calls(), self.device.index
         if stream is None:
-            sp = torch._C._cuda_getCurrentRawStream(index)  # (current_stream().cuda_stream costs 2 us)
+            sp = c._cuda_getCurrentRawStream(index)  # (current_stream().cuda_stream costs 2 us)
         elif isinstance(stream, int):
             sp = stream
         else:
@@ -755,7 +764,7 @@ class _Prepared:
             sp = stream.cuda_stream
         if self._streams is not None and sp not in self._streams:
             self._first_on(sp)
-        if torch.cuda.current_device() == index:
+        if c._cuda_getDevice() == index:
             status = self._fn(self._ref, sp)
         else:
             with _launch_ctx(self.device):

@@ -36,25 +36,25 @@ inline int fp8_chunks(int n, int D) {  // of 16 columns, of a read-back warp (tw
     return D > 1 ? mc : mc <= 4 ? 4 : mc <= 6 ? 6 : 7;
 }
 // Cycles of a block of K in one CTA, fitted to the times of every tile and
-// number of slices at 12 sizes: the read-back, by its chunks and by how many
-// blocks share its waits (four blocks of 48 columns 305, two of 96 460, one of
-// 128 570, of 192 810; pairs of 176 750, of 224 820), or the bytes' way from L2,
-// 51 a cycle (128 rows and 48 columns: 440).
+// number of slices at 21 sizes (off by 8 %, the chosen tile by 1 %, at most 4): the
+// read-back, by its chunks and by how many blocks share its waits (four blocks of
+// 48 columns 305, two of 96 460, one of 128 576, of 192 804; pairs of 192 655, of
+// 224 716), or the bytes' way from L2, 57 a cycle (128 rows and 48 columns: 396).
 inline int fp8_block_cycles(bool pair, int xrows, int n) {
-    if (pair) return 400 + 2 * n;
-    const int D = fp8_depth(false, xrows, n), mc = fp8_chunks(n, D), l2 = (xrows + n) * 5 / 2;
-    const int read = D == 4 ? 125 + 90 * mc : D == 2 ? 220 + 80 * mc : 90 + 120 * mc;
+    if (pair) return 290 + n * 19 / 10;
+    const int D = fp8_depth(false, xrows, n), mc = fp8_chunks(n, D), l2 = (xrows + n) * 9 / 4;
+    const int read = D == 4 ? 155 + 75 * mc : D == 2 ? 295 + 55 * mc : 120 + 114 * mc;
     return read > l2 ? read : l2;
 }
-// What a call costs besides: a pair's start, and handing the slices' sums over.
+// What a call costs besides: a pair's start and end, and handing the slices' sums over.
 inline int fp8_call_cycles(bool pair, int n, int slices) {
-    return pair ? 1500 : slices > 1 ? 37 * n + 520 * slices : 0;
+    return pair ? 4900 : slices > 1 ? 38 * n + 570 * slices : 0;
 }
-// The tile and slices whose rounds cost least.  40 x 1536 x 6144: 32 columns in
-// two slices 6.7 us, 48 in four 7.0, 16 in one 8.3; 40 x 6144 x 6144: 48 in one
-// 10.9, 96 in two 12.0; 64 x 6144 x 6144: 96 in two 11.9, 64 in one 12.6; 200 x
-// 6144 x 6144: 176 in two 16.1, 112 in one 18.1; 4096 x 6144 x 6144 by pairs: 224
-// columns 125 us, 192 135.
+// The tile and slices whose rounds cost least.  40 x 1536 x 6144: 48 columns in
+// four slices 6.8 us, 32 in two 6.9, 16 in one 7.9; 40 x 6144 x 6144: 48 in one
+// 10.0, 96 in two 11.5; 128 x 6144 x 6144: 96 in two 12.5, 64 in one 12.8; 700 x
+// 1536 x 6144: 128 in two 12.6, 96 in one 16.4; 2048 x 1536 x 6144: 192 by pairs
+// 20.6, by single CTAs 22.1; 4096 x 6144 x 6144 by pairs: 224 112, 192 120.
 inline Fp8Plan fp8_plan(int M, int R, int K, int sms) {
     Fp8Plan p{};
     const int KI = (K + 127) / 128;

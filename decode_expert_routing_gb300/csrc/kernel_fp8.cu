@@ -13,20 +13,19 @@
 // 128 (256) rows of x times n rows of w, row tiles fastest.  Warp 0 copies
 // (tensor maps, 128-byte swizzle, a block of 128 bytes a row per stage), warp 1
 // issues the products, warps 2-3 prepare the scales, warps 4-11 read back, each
-// group of four half of the columns.  (Three groups of a third: 134.7 -> 136.5
-// us at 4096 x 6144 x 6144 with 192 columns, and 224 have no registers, four:
-// 142.  One group that reads what another adds later: 153.)  Few rows leave
+// group of four half of the columns.  (At 4096 x 6144 x 6144 with 192 columns two groups
+// took 134.7 us, three of a third 136.5, four 142.)  Few rows leave
 // most of this idle, so tiles become narrow, stages and buffers take up to four
 // blocks (one wait for all of them), products up to 64 rows are of 64, and
 // where tiles are still fewer than SMs a cluster shares their K range.
 //
-// What bounds it: of 4096 x 6144 x 6144 (125 us, 2480 TFLOP/s, 1.25 of the
-// bf16 rate measured here) a pair's block of K of 224 columns takes 820 cycles:
-// 448 for the products, 600 for its bytes' way from L2, 224 each to read tensor
-// memory and to add; the read-back's waits at both ends of a buffer join them.
-// Below 128 rows it is the weight: 64 x 6144 x 6144 11.8 us (3.3 TB/s), 40 x
-// 1536 x 6144 6.7 us, most of it start, first bytes and the sums' way through
-// the cluster.
+// What bounds it: of 4096 x 6144 x 6144 (112 us, 2770 TFLOP/s, 1.4 of the bf16
+// rate measured here) a pair's block of K of 224 columns takes 780 cycles: 448
+// for the products, 600 for its bytes' way from L2, 224 to read tensor memory,
+// as many to add; the read-back's waits at both ends of a buffer join them.  The
+// results' way out is 3 us of it.  Below 128 rows it is the weight: 40 x 6144 x
+// 6144 10.0 us (3.8 TB/s), 40 x 1536 x 6144 6.8 us, most of it start, first bytes
+// and the sums' way through the cluster.
 #include "../../include/moe_route.h"
 #include "fp8_plan.h"
 #include "internal.h"

@@ -169,3 +169,35 @@ def test_plans_keep_what_the_kernel_relies_on(tmp_path):
             assert not pair and slices in (2, 4, 8) and grid == RT * CT * slices <= sms
             assert len_ % D == 0 and len_ * (slices - 1) < KI <= len_ * slices
             assert slices * -(-(n // 16) // slices) * 16 * 128 * 4 + 1024 <= 208 * 1024
+
+
+SIZES = r'''
+#include <cstdio>
+#include <cstdlib>
+#include "fp8_plan.h"
+int main(int n, char** v) {
+    for (int i = 1; i + 2 < n; i += 3) {
+        const int M = atoi(v[i]), R = atoi(v[i + 1]), K = atoi(v[i + 2]);
+        if (mr::fp8_few(M)) {
+            const mr::Fp8FewPlan p = mr::fp8_few_plan(M, R, K, 152);
+            printf("few %d %d\n", p.A, p.B);
+        } else {
+            const mr::Fp8Plan p = mr::fp8_plan(M, R, K, 152);
+            printf("%d %d %d %d\n", p.pair, p.D, p.mc, p.slices > 1);
+        }
+    }
+}
+'''
+
+
+def test_the_sizes_run_on_the_gpu_take_every_variant(tmp_path):
+    from tests.test_gpu_operators_together import VARIANTS
+    src, exe = tmp_path / "probe.cpp", tmp_path / "probe"
+    src.write_text(SIZES)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "decode_expert_routing_gb300", "csrc"),
+                    "-I", "/usr/local/cuda/include", "-o", str(exe), str(src)], check=True)
+    args = [str(x) for v in VARIANTS for x in v]
+    taken = set(subprocess.run([str(exe), *args], check=True, capture_output=True, text=True).stdout.split("\n")) - {""}
+    single = [(4, 1), (4, 2), (2, 1), (2, 2), (2, 3), (2, 4), (1, 4), (1, 6), (1, 7)]
+    assert taken == {f"few {a} {b}" for a in (1, 2) for b in (1, 2)} | {"1 1 6 0", "1 1 7 0"} | {
+        f"0 {d} {mc} {s}" for d, mc in single for s in (0, 1)}
