@@ -78,6 +78,93 @@ struct Elems {
     }
 };
 
+// Rows whose words do not start on 16 bytes (odd lengths, odd strides), shifted: a thread
+// still takes an aligned 16-byte word of the row that is written, and reads the
+// two aligned words that hold those bytes of each other row, which it shifts
+// into place.  (Element by element 4096 x 4 rows of 1001 took 27 us each way, so
+// 18 and 15.)
+// Words that leave the operand's memory [lo, hi) are read by element, so nothing
+// beside it is.
+struct Words {
+    uint4 a, b;
+    unsigned shift;  // bytes
+};
+template <int UNIT>
+struct Unit;
+template <>
+struct Unit<1> { using T = uint8_t; };
+template <>
+struct Unit<2> { using T = uint16_t; };
+// A row that is read beside one whose first byte is byte off of its first word: word c of that one are the 16 bytes
+// from byte 16 c - off of this one on, those of words [first, last) by aligned words, the others by element.
+struct Source {
+    const uint8_t* from;  // byte -off
+    unsigned shift;
+    int first, last;
+};
+__device__ __forceinline__ Source source(const uint8_t* row, int off, const uint8_t* lo, const uint8_t* hi) {
+    Source s;
+    s.from = row - off;
+    s.shift = (unsigned)(reinterpret_cast<uintptr_t>(s.from) & 15u);
+    const uint8_t* g = s.from - s.shift;  // (at most 30 bytes before the row)
+    s.first = g >= lo ? 0 : g + 16 >= lo ? 1 : 2;
+    const int64_t n = ((hi - g) >> 4) - (s.shift ? 1 : 0);
+    s.last = (int)(n < (1 << 30) ? n : (1 << 30));
+    return s;
+}
+// Word c; of one that is read by element the row's bytes [0, end) alone.  UNIT: bytes that every address is a multiple
+// of (1 or 2; 4-byte elements by halves).
+template <int UNIT>
+__device__ __forceinline__ Words load_words(const Source& s, int c, int off, int end) {
+    using T = typename Unit<UNIT>::T;
+    const uint8_t* from = s.from + (int64_t)c * 16;
+    Words r;
+    r.shift = s.shift;
+    r.b = make_uint4(0u, 0u, 0u, 0u);
+    if (c >= s.first && c < s.last) {
+        r.a = *reinterpret_cast<const uint4*>(from - s.shift);
+        if (s.shift) r.b = *reinterpret_cast<const uint4*>(from - s.shift + 16);
+    } else {
+        r.shift = 0;
+        unsigned long long h0 = 0ull, h1 = 0ull;
+#pragma unroll 1
+        for (int i = 0; i < 16; i += UNIT) {
+            const int at = c * 16 - off + i;
+            if (at < 0 || at >= end) continue;
+            const unsigned long long e = *reinterpret_cast<const T*>(from + i);
+            if (i < 8) h0 |= e << (8 * i);
+            else h1 |= e << (8 * i - 64);
+        }
+        r.a = make_uint4((uint32_t)h0, (uint32_t)(h0 >> 32), (uint32_t)h1, (uint32_t)(h1 >> 32));
+    }
+    return r;
+}
+__device__ __forceinline__ uint4 shifted(const Words& v) {
+    uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+    const bool two = v.shift & 8u, one = v.shift & 4u;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = two ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = one ? w[i + 1] : w[i];
+    const unsigned bits = (v.shift & 3u) * 8u;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+// The row's bytes among the 16 from byte at on (where they start on 16 bytes of memory).
+template <int UNIT>
+__device__ __forceinline__ void store_words(uint8_t* row, int at, int end, const uint4& v) {
+    using T = typename Unit<UNIT>::T;
+    if (at >= 0 && at + 16 <= end) {
+        __stcs(reinterpret_cast<uint4*>(row + at), v);
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 16 / UNIT; ++i)
+        if (at + i * UNIT >= 0 && at + i * UNIT < end)
+            *reinterpret_cast<T*>(row + at + i * UNIT) = (T)(w[i * UNIT / 4] >> (i * UNIT % 4 * 8));
+}
+
 // ------------------------------------------------------------------ to the experts
 
 // lanes threads to a row, kRowThreads / lanes rows to a CTA.  MODE 0: rows as
@@ -171,97 +258,134 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExperts
     }
 }
 
-// ------------------------------------------------------------------ back to the tokens
-
-// lanes threads to a token's row and kTokenVecs words to a thread, whose rows of
-// up to eight slots are under way together.  The sum goes over the slots in
-// ascending order in fp32, from add (or zero), and is rounded once.
-constexpr int kTokenThreads = 128;
-template <int TYPE, int BYTES, int VECS>
-__global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokensArgs a, int lanes, int shift, int vecs,
-                                                                  int blocks, int64_t total) {
-    using E = Elems<TYPE, BYTES>;
-    using V = typename Vec<BYTES>::T;
+// Rows of 1- and 2-byte units that start anywhere, as they are: to_experts_kernel's MODE 0 with shifted words.  (Rows
+// of whole 4- or 8-byte words go faster as such: 2048 x 4 rows of 6142 33 us, shifted 42; of 6143 element by element
+// 44, 1000 x 4 30 and 28.  With the weights' sums, MODE 1, shifting both rows gains nothing: 63 us and 67.)
+template <int UNIT>
+__global__ void __launch_bounds__(kRowThreads) to_experts_shift_kernel(const ToExpertsArgs a, int lanes, int shift,
+                                                                       int slab) {
+    constexpr int U = 4;
     pdl_trigger();
     pdl_wait();
-    const int tid = threadIdx.x, lane = tid & (lanes - 1), per = kTokenThreads >> shift;
-    for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
-        const int64_t mb = blocks == 1 ? b : b / blocks, m = mb * per + (tid >> shift);
-        const int c0 = (int)(b - mb * blocks) * lanes * VECS + lane;
-        if (m >= a.M || c0 >= vecs) continue;
-        float s[VECS][E::N];
+    const int tid = threadIdx.x, lane = tid & (lanes - 1), mk = a.M * a.topk;
+    const int64_t p = ((int64_t)blockIdx.x << (__ffs(kRowThreads) - 1 - shift)) + (tid >> shift);
+    const int64_t i0 = (int64_t)blockIdx.x * kRowThreads + tid;
+    if (blockIdx.y == 0 && i0 < mk && (unsigned)a.ids[i0] >= (unsigned)a.E) a.positions[i0] = -1;
+    if (p >= a.cap || p >= __ldg(a.npost)) return;
+    const int f = __ldg(a.sorted + p);
+    // the row that is written, its words counted from the 16 bytes that hold its first byte on
+    uint8_t* out = static_cast<uint8_t*>(a.out) + p * a.row_bytes;
+    const int off = (int)(reinterpret_cast<uintptr_t>(out) & 15u);
+    const int c0 = (int)blockIdx.y * slab, c1 = min(c0 + slab, (off + a.row_bytes + 15) / 16);
+    if ((unsigned)f >= (unsigned)mk) {
+        for (int c = c0 + lane; c < c1; c += lanes)
+            store_words<UNIT>(out, c * 16 - off, a.row_bytes, make_uint4(0u, 0u, 0u, 0u));
+        return;
+    }
+    if (lane == 0 && blockIdx.y == 0) a.positions[f] = (int32_t)p;
+    const uint8_t* x = static_cast<const uint8_t*>(a.x);
+    const Source from = source(x + (int64_t)((unsigned)f / (unsigned)a.topk) * a.ldx, off, x, x + a.x_bytes);
+    for (int c = c0 + lane; c < c1; c += lanes * U) {
+        Words v[U];
 #pragma unroll
-        for (int k = 0; k < VECS; ++k)
+        for (int u = 0; u < U; ++u)
+            if (c + u * lanes < c1) v[u] = load_words<UNIT>(from, c + u * lanes, off, a.row_bytes);
 #pragma unroll
-            for (int q = 0; q < E::N; ++q) s[k][q] = 0.0f;
-        if (a.add != nullptr) {
-            // (plain loads: out may be add itself)
-            const V* add = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.add) + m * a.ldadd) + c0;
-#pragma unroll
-            for (int k = 0; k < VECS; ++k)
-                if (c0 + k * lanes < vecs) E::get(add[k * lanes], s[k]);
-        }
-        const int32_t* pos = a.positions + m * a.topk;
-        const float* wts = a.weights + (a.weights != nullptr ? m * a.topk : 0);
-        for (int j0 = 0; j0 < a.topk; j0 += 8) {
-            V v[8][VECS];
-            float w[8];
-            int p[8];
-            unsigned in = 0u;
-            // (one word a thread: all positions, then all rows; more of them, small ones, go slot by slot: rows of 6143
-            // 75 us instead of 91)
-            if (VECS == 1) {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    p[u] = j0 + u < a.topk ? __ldg(pos + j0 + u) : -1;
-                    w[u] = a.weights != nullptr && j0 + u < a.topk ? __ldg(wts + j0 + u) : 1.0f;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (VECS > 1) {
-                    w[u] = 1.0f;
-                    if (j0 + u >= a.topk) continue;
-                    p[u] = __ldg(pos + j0 + u);
-                    if (a.weights != nullptr) w[u] = __ldg(wts + j0 + u);
-                }
-                if ((uint64_t)(int64_t)p[u] >= (uint64_t)a.cap) continue;
-                in |= 1u << u;
-                const V* y = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + (int64_t)p[u] * a.ldy) + c0;
-#pragma unroll
-                for (int k = 0; k < VECS; ++k)
-                    if (c0 + k * lanes < vecs) v[u][k] = __ldcs(y + k * lanes);
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (!(in >> u & 1u)) continue;
-#pragma unroll
-                for (int k = 0; k < VECS; ++k) {
-                    if (c0 + k * lanes >= vecs) continue;
-                    float f[E::N];
-                    E::get(v[u][k], f);
-#pragma unroll
-                    for (int q = 0; q < E::N; ++q) s[k][q] = __fmaf_rn(w[u], f[q], s[k][q]);
-                }
-            }
-        }
-        V* out = static_cast<V*>(a.out) + m * vecs + c0;
-#pragma unroll
-        for (int k = 0; k < VECS; ++k)
-            if (c0 + k * lanes < vecs) out[k * lanes] = E::put(s[k]);
+        for (int u = 0; u < U; ++u)
+            if (c + u * lanes < c1) store_words<UNIT>(out, (c + u * lanes) * 16 - off, a.row_bytes, shifted(v[u]));
     }
 }
 
-// The same of many tokens with rows of whole 8- or 16-byte words: a CTA takes
-// every nth piece of lanes * VECS words; a warp has one token at a time, its
-// lanes the slots' positions and weights, which are read one piece ahead.  4096
-// x 8 rows of 6144: 73 us, 79 by the kernel above; 64 tokens 3.5 and 3.2, rows
-// of 6143 138 and 75.
-template <int TYPE, int BYTES, int VECS>
-__global__ void __launch_bounds__(kTokenThreads)
-    to_tokens_many_kernel(const ToTokensArgs a, int lanes, int shift, int vecs, int blocks, int64_t total) {
-    using E = Elems<TYPE, BYTES>;
-    using V = typename Vec<BYTES>::T;
+// ------------------------------------------------------------------ back to the tokens
+
+// lanes threads to a token's row and a word to a thread, whose rows of up to
+// eight slots (SHIFT: rows that start anywhere; four) are under way together.
+// The sum goes over the slots in ascending order in fp32, from add (or zero), and
+// is rounded once.  2048 x 4 rows of 6143: 43 us, element by element 81, of 6140
+// 41 and by 8-byte words 46.
+constexpr int kTokenThreads = 128;
+template <int TYPE, bool SHIFT>
+__global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokensArgs a, int lanes, int shift,
+                                                                  int blocks, int64_t total) {
+    using E = Elems<TYPE, 16>;
+    constexpr int U = SHIFT ? 4 : 8;
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & (lanes - 1), per = kTokenThreads >> shift;
+    const uint8_t *y0 = static_cast<const uint8_t*>(a.y), *y1 = y0 + a.y_bytes;
+    for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+        const int64_t mb = blocks == 1 ? b : b / blocks, m = mb * per + (tid >> shift);
+        if (m >= a.M) continue;
+        // the row that is written, its words counted from the 16 bytes that hold its first byte on
+        uint8_t* out = static_cast<uint8_t*>(a.out) + m * a.row_bytes;
+        const int off = SHIFT ? (int)(reinterpret_cast<uintptr_t>(out) & 15u) : 0;
+        const int c = (int)(b - mb * blocks) * lanes + lane, at = c * 16 - off;
+        if (at >= a.row_bytes) continue;
+        float s[E::N];
+#pragma unroll
+        for (int q = 0; q < E::N; ++q) s[q] = 0.0f;
+        if (a.add != nullptr) {
+            // (plain loads: out may be add itself)
+            const uint8_t *add0 = static_cast<const uint8_t*>(a.add), *add = add0 + m * a.ldadd;
+            if (SHIFT) {
+                const Source from = source(add, off, add0, add0 + a.add_bytes);
+                E::get(shifted(load_words<2>(from, c, off, a.row_bytes)), s);
+            } else {
+                E::get(*reinterpret_cast<const uint4*>(add + at), s);
+            }
+        }
+        const int32_t* pos = a.positions + m * a.topk;
+        const float* wts = a.weights + (a.weights != nullptr ? m * a.topk : 0);
+        for (int j0 = 0; j0 < a.topk; j0 += U) {
+            int p[U];
+            float w[U];
+            bool in[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                p[u] = j0 + u < a.topk ? __ldg(pos + j0 + u) : -1;
+                w[u] = a.weights != nullptr && j0 + u < a.topk ? __ldg(wts + j0 + u) : 1.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) in[u] = (uint64_t)(int64_t)p[u] < (uint64_t)a.cap;
+            auto add = [&](int u, const uint4& v) {
+                float f[E::N];
+                E::get(v, f);
+#pragma unroll
+                for (int q = 0; q < E::N; ++q) s[q] = __fmaf_rn(w[u], f[q], s[q]);
+            };
+            if constexpr (SHIFT) {
+                Words v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (in[u])
+                        v[u] = load_words<2>(source(y0 + (int64_t)p[u] * a.ldy, off, y0, y1), c, off, a.row_bytes);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (in[u]) add(u, shifted(v[u]));
+            } else {
+                uint4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (in[u]) v[u] = __ldcs(reinterpret_cast<const uint4*>(y0 + (int64_t)p[u] * a.ldy + at));
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (in[u]) add(u, v[u]);
+            }
+        }
+        if (SHIFT) store_words<2>(out, at, a.row_bytes, E::put(s));
+        else *reinterpret_cast<uint4*>(out + at) = E::put(s);
+    }
+}
+
+// The same of many tokens with aligned rows: a CTA takes every nth piece of
+// lanes * VECS words; a warp has one token at a time, its lanes the slots'
+// positions and weights, which are read one piece ahead.  4096 x 8 rows of 6144:
+// 73 us, 79 by the kernel above; 64 tokens 3.5 and 3.2.
+template <int TYPE, int VECS>
+__global__ void __launch_bounds__(kTokenThreads) to_tokens_many_kernel(const ToTokensArgs a, int lanes, int shift,
+                                                                       int vecs, int blocks, int64_t total) {
+    using E = Elems<TYPE, 16>;
+    using V = uint4;
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & (lanes - 1), slot = tid & 31, per = kTokenThreads >> shift;
@@ -356,18 +480,12 @@ int log2_of(int v) {
     return s;
 }
 
-cudaError_t device_sms(int* sms) {
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-}
-
 template <int MODE, int TYPE, int BYTES>
 cudaError_t launch_experts_v(const ToExpertsArgs& a, cudaStream_t st) {
-    const int vecs = (int)((int64_t)a.K * row_elem_bytes(a.type) / BYTES);
+    const int vecs = a.row_bytes / BYTES;
     // 8- and 16-byte words: 64 threads a row, four words each (4 KB) in a slab; MODE 1 so of many rows (2048 x 8
     // positions of 6144: 75 us, with 128 threads 80, with 256 94), of few 256 (64 x 8: 6.9 us, with 64 7.4).
-    // Smaller words, whose instructions count: whole rows (2048 x 4 rows of 6143: 37 us, in slabs 75).
+    // Smaller words, whose instructions count: whole rows (2048 x 4 rows of 6142: 33 us, in slabs twice that).
     const bool wide = BYTES >= 8;
     const int most = !wide ? (MODE == 0 ? 256 : 128) : MODE == 0 || a.cap >= 4096 ? 64 : 256;
     int lanes = 32;
@@ -381,36 +499,54 @@ cudaError_t launch_experts_v(const ToExpertsArgs& a, cudaStream_t st) {
                              log2_of(lanes), vecs, slab);
 }
 
-template <int TYPE, int BYTES, int VECS>
-cudaError_t launch_tokens_n(const ToTokensArgs& a, int vecs, cudaStream_t st) {
-    int lanes = 32;
-    while (lanes < kTokenThreads && lanes * VECS < vecs) lanes *= 2;
-    const int per = kTokenThreads / lanes, blocks = (vecs + lanes * VECS - 1) / (lanes * VECS);
+template <int UNIT>
+cudaError_t launch_experts_shift(const ToExpertsArgs& a, cudaStream_t st) {
+    const int vecs = (a.row_bytes + 30) / 16;  // (at most)
+    int lanes = 8;
+    while (lanes < 64 && lanes < vecs) lanes *= 2;
+    const int64_t per = kRowThreads / lanes, mk = (int64_t)a.M * a.topk;
+    int64_t ctas = (a.cap + per - 1) / per;
+    if (ctas * kRowThreads < mk) ctas = (mk + kRowThreads - 1) / kRowThreads;  // (a thread for each assignment)
+    const int slab = lanes * 4;
+    const dim3 grid((unsigned)ctas, (unsigned)((vecs + slab - 1) / slab));
+    return launch_overlapped(to_experts_shift_kernel<UNIT>, grid, dim3(kRowThreads), 0, st, a, lanes, log2_of(lanes),
+                             slab);
+}
+
+template <int TYPE, bool SHIFT>
+cudaError_t launch_tokens_v(const ToTokensArgs& a, cudaStream_t st) {
+    const int vecs = (a.row_bytes + (SHIFT ? 15 : 0) + 15) / 16;  // (at most)
+    constexpr int VECS = 2;
+    if constexpr (!SHIFT) {
+        // two words a thread where that leaves enough CTAs
+        if ((int64_t)a.M * vecs >= (1 << 18)) {
+            int dev = 0, sms = 0;
+            cudaError_t e = cudaGetDevice(&dev);
+            if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+            if (e != cudaSuccess) return e;
+            int lanes = 32;
+            while (lanes < kTokenThreads && lanes * VECS < vecs) lanes *= 2;
+            const int per = kTokenThreads / lanes, blocks = (vecs + lanes * VECS - 1) / (lanes * VECS);
+            const int64_t total = ((int64_t)a.M + per - 1) / per * blocks, most = (int64_t)sms * 4;
+            const dim3 grid((unsigned)(total < most ? total : most));
+            return launch_overlapped(to_tokens_many_kernel<TYPE, VECS>, grid, dim3(kTokenThreads), 0, st, a, lanes,
+                                     log2_of(lanes), vecs, blocks, total);
+        }
+    }
+    int lanes = 8;
+    while (lanes < kTokenThreads && lanes < vecs) lanes *= 2;
+    const int per = kTokenThreads / lanes, blocks = (vecs + lanes - 1) / lanes;
     const int64_t total = ((int64_t)a.M + per - 1) / per * blocks;
     const int64_t ctas = total < ((int64_t)1 << 30) ? total : ((int64_t)1 << 30);
-    return launch_overlapped(to_tokens_kernel<TYPE, BYTES, VECS>, dim3((unsigned)ctas), dim3(kTokenThreads), 0, st, a,
-                             lanes, log2_of(lanes), vecs, blocks, total);
+    return launch_overlapped(to_tokens_kernel<TYPE, SHIFT>, dim3((unsigned)ctas), dim3(kTokenThreads), 0, st, a, lanes,
+                             log2_of(lanes), blocks, total);
 }
-template <int TYPE, int BYTES>
-cudaError_t launch_tokens_v(const ToTokensArgs& a, cudaStream_t st) {
-    constexpr int VECS = 2;
-    const int vecs = (int)((int64_t)a.K * row_elem_bytes(a.type) / BYTES);
-    // two words a thread where that leaves enough CTAs
-    if ((int64_t)a.M * vecs < (1 << 18)) return launch_tokens_n<TYPE, BYTES, 1>(a, vecs, st);
-    if constexpr (BYTES >= 8) {
-        int sms = 0;
-        const cudaError_t e = device_sms(&sms);
-        if (e != cudaSuccess) return e;
-        int lanes = 32;
-        while (lanes < kTokenThreads && lanes * VECS < vecs) lanes *= 2;
-        const int per = kTokenThreads / lanes, blocks = (vecs + lanes * VECS - 1) / (lanes * VECS);
-        const int64_t total = ((int64_t)a.M + per - 1) / per * blocks, most = (int64_t)sms * 4;
-        const dim3 grid((unsigned)(total < most ? total : most));
-        return launch_overlapped(to_tokens_many_kernel<TYPE, BYTES, VECS>, grid, dim3(kTokenThreads), 0, st, a, lanes,
-                                 log2_of(lanes), vecs, blocks, total);
-    }
-    return launch_tokens_n<TYPE, BYTES, VECS>(a, vecs, st);
+template <int TYPE>
+cudaError_t launch_tokens_t(const ToTokensArgs& a, bool aligned, cudaStream_t st) {
+    return aligned ? launch_tokens_v<TYPE, false>(a, st) : launch_tokens_v<TYPE, true>(a, st);
 }
+
+uintptr_t bits_of(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 }  // namespace
 
@@ -419,17 +555,18 @@ cudaError_t launch_to_experts(const ToExpertsArgs& a0, cudaStream_t st) {
     const int eb = row_elem_bytes(a.type);
     a.ldx *= eb;  // bytes from here on
     a.ldy *= eb;
-    uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.ldx |
-                     (uintptr_t)((int64_t)a.K * eb);
-    if (a.y != nullptr) bits |= reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)a.ldy;
+    a.row_bytes = a.K * eb;
+    a.x_bytes = (a.M - 1) * a.ldx + a.row_bytes;
+    uintptr_t bits = bits_of(a.x) | bits_of(a.out) | (uintptr_t)a.ldx | (uintptr_t)a.row_bytes;
+    if (a.y != nullptr) bits |= bits_of(a.y) | (uintptr_t)a.ldy;
     const int v = vec_bytes(bits, eb);
     if (a.grad_w == nullptr) {
         switch (v) {
             case 16: return launch_experts_v<0, kRowU8, 16>(a, st);
             case 8: return launch_experts_v<0, kRowU8, 8>(a, st);
             case 4: return launch_experts_v<0, kRowU8, 4>(a, st);
-            case 2: return launch_experts_v<0, kRowU8, 2>(a, st);
-            default: return launch_experts_v<0, kRowU8, 1>(a, st);
+            case 2: return launch_experts_shift<2>(a, st);
+            default: return launch_experts_shift<1>(a, st);
         }
     }
 #define MR_EXPERTS(T)                                              \
@@ -450,21 +587,15 @@ cudaError_t launch_to_tokens(const ToTokensArgs& a0, cudaStream_t st) {
     const int eb = row_elem_bytes(a.type);
     a.ldy *= eb;
     a.ldadd *= eb;
-    uintptr_t bits = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.ldy |
-                     (uintptr_t)((int64_t)a.K * eb);
-    if (a.add != nullptr) bits |= reinterpret_cast<uintptr_t>(a.add) | (uintptr_t)a.ldadd;
-    const int v = vec_bytes(bits, eb);
-#define MR_TOKENS(T)                                               \
-    switch (v) {                                                   \
-        case 16: return launch_tokens_v<T, 16>(a, st);             \
-        case 8: return launch_tokens_v<T, 8>(a, st);               \
-        case 4: return launch_tokens_v<T, 4>(a, st);               \
-        default: return launch_tokens_v<T, T == kRowFp32 ? 4 : 2>(a, st); \
-    }
-    if (a.type == kRowBf16) MR_TOKENS(kRowBf16)
-    if (a.type == kRowFp16) MR_TOKENS(kRowFp16)
-    MR_TOKENS(kRowFp32)
-#undef MR_TOKENS
+    a.row_bytes = a.K * eb;
+    a.y_bytes = (a.cap - 1) * a.ldy + a.row_bytes;
+    a.add_bytes = (a.M - 1) * a.ldadd + a.row_bytes;
+    uintptr_t bits = bits_of(a.y) | bits_of(a.out) | (uintptr_t)a.ldy | (uintptr_t)a.row_bytes;
+    if (a.add != nullptr) bits |= bits_of(a.add) | (uintptr_t)a.ldadd;
+    const bool aligned = bits % 16 == 0;
+    if (a.type == kRowBf16) return launch_tokens_t<kRowBf16>(a, aligned, st);
+    if (a.type == kRowFp16) return launch_tokens_t<kRowFp16>(a, aligned, st);
+    return launch_tokens_t<kRowFp32>(a, aligned, st);
 }
 
 }  // namespace mr

@@ -24,6 +24,8 @@ struct ToExpertsArgs {
     void* out;             // [cap, K]
     int64_t cap;
     int M, K, topk, E, type;
+    int row_bytes;         // of a row; this and x_bytes, from the first row's start to the last one's end, are
+    int64_t x_bytes;       // set by the launcher
 };
 // Back to the tokens: out[m] = add[m] + sum_j weights[m, j] y[positions[m, j]].
 struct ToTokensArgs {
@@ -33,6 +35,8 @@ struct ToTokensArgs {
     const float* weights;  // or null: ones
     void* out;             // [M, K]
     int M, K, topk, type;
+    int row_bytes;         // of a row; this, y_bytes and add_bytes, from the first row's start to the last one's
+    int64_t y_bytes, add_bytes;  // end, are set by the launcher
 };
 cudaError_t launch_to_experts(const ToExpertsArgs& a, cudaStream_t st);
 cudaError_t launch_to_tokens(const ToTokensArgs& a, cudaStream_t st);

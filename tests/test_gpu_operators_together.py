@@ -231,3 +231,48 @@ def test_many_tokens_of_many_slots(mr, topk, K):
     # topk fused multiply-adds in fp32, then bf16
     tol = (topk * 2.0 ** -24) * x.double().abs() * (1 + size)
     ref.assert_within(out, val, tol + 2.0 ** -8 * (val.abs() + tol))
+
+
+@pytest.mark.parametrize("K", [1, 3, 8, 9, 33, 100, 1001])
+@pytest.mark.parametrize("dtype", [BF16, F32, torch.uint8])
+def test_rows_that_start_anywhere(mr, K, dtype):
+    """Operands and results that start at any element of their memory, in place too: the values of aligned ones, and
+    nothing beside them changed.  (Memory beside the operands holds NaN.)"""
+    M, E, topk = 37, 8, 3
+    ids, wts = ref.routed(M, E, topk, 2, 0.2)
+    st, _, nt = mr.moe_sort(ids, E, 8)
+    n, cap = int(nt), st.numel()
+    codes = dtype == torch.uint8
+
+    def within(t, off):
+        fill = 77 if codes else float("nan")
+        flat = torch.full((t.numel() + 48,), fill, dtype=t.dtype, device="cuda")
+        view = flat[off:off + t.numel()].view(t.shape)
+        view.copy_(t)
+        return flat, view
+
+    def beside(flat, off, count):
+        left = torch.cat([flat[:off], flat[off + count:]])
+        return (left == 77).all() if codes else torch.isnan(left).all()
+
+    x = ref.codes(1, M, K) if codes else ref.rows(1, M, K, dtype)
+    rows, pos = mr.moe_permute(x, ids, E, st, nt, out=torch.zeros(cap, K, dtype=dtype, device="cuda"))
+    for off in (1, 2, 5, 8, 15):
+        flat, out = within(torch.zeros_like(rows), 16 - off)
+        got, p = mr.moe_permute(within(x, off)[1], ids, E, st, nt, out=out)
+        assert torch.equal(got, rows) and torch.equal(p, pos) and beside(flat, 16 - off, cap * K)
+        if codes:
+            continue
+        y, add = ref.rows(3, cap, K, dtype), ref.rows(4, M, K, dtype)
+        want = mr.moe_combine(y, pos, wts, add=add)
+        flat, out = within(add, off)
+        assert torch.equal(mr.moe_combine(within(y, 17 - off)[1], pos, wts, add=out, out=out), want)
+        assert beside(flat, off, M * K)
+        assert torch.equal(mr.moe_permute_grad(within(y, off)[1], pos), mr.moe_permute_grad(y, pos))
+        gy, gw = mr.moe_combine_grad(x, y, pos, wts, st, nt, out=torch.zeros_like(y))
+        flat, out = within(y, off)
+        gy2, gw2 = mr.moe_combine_grad(within(x, 16 - off)[1], out, pos, wts, st, nt, out=out)
+        assert torch.equal(gy2[:n], gy[:n]) and torch.equal(gy2[n:], y[n:]) and beside(flat, off, cap * K)
+        # (fp32 sums over K in another order)
+        tol = K * 2.0 ** -23 * (x.double().abs().max() * y[:n].double().abs().max()) * K
+        assert ((gw2 - gw).double().abs() <= tol).all()
