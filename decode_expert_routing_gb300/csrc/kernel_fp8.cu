@@ -140,6 +140,39 @@ __device__ __forceinline__ void f8_store_words(uint8_t* at, int64_t pitch, int64
     for (int i = 0; i < W; ++i)
         if (i < left) *reinterpret_cast<uint4*>(at + i * pitch) = w[i];
 }
+// The same where rows do not start on 16 bytes or columns end: words of 4 bytes
+// (one number, or two of bf16), W * 4 contiguous bytes of each of 32 / W rows an
+// instruction (two of bf16 on odd addresses).  cols: how many numbers there are
+// from the lane's word on.  (4096 x 6143 x 6144: 130 us, each lane for itself 315;
+// 1000 x 6143 x 2048: 23 and 75; with 6144 columns 112 and 17.)
+template <int W>
+__device__ __forceinline__ void f8_store_odd(uint8_t* at, int64_t pitch, int64_t left, uint32_t (&w)[W], int cols,
+                                             bool fp32) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < W; o *= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            if (k & o) continue;
+            const uint32_t got = __shfl_xor_sync(kFull, up ? w[k] : w[k + o], o);
+            if (up) w[k] = got;
+            else w[k + o] = got;
+        }
+    }
+    const int need = fp32 ? 1 : 2;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        if (i >= left) continue;
+        uint8_t* p = at + i * pitch;
+        if (cols >= need && (reinterpret_cast<uintptr_t>(p) & 3u) == 0) {
+            *reinterpret_cast<uint32_t*>(p) = w[i];
+        } else if (!fp32) {
+            if (cols >= 1) *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[i];
+            if (cols >= 2) *reinterpret_cast<uint16_t*>(p + 2) = (uint16_t)(w[i] >> 16);
+        }
+    }
+}
 // N of the chunks f of 16 columns, from c0 on, to the columns from col on of the lanes' rows, the first lane's row
 // row0; rows: how many of the warp's rows there are.  Whole warps call it.
 template <int N, int MC>
@@ -178,19 +211,29 @@ __device__ __forceinline__ void f8_store(const Fp8Args& a, int64_t row0, int row
         }
         return;
     }
-    if (lane >= rows) return;
+    if (a.out_fp32) {
 #pragma unroll
-    for (int c = 0; c < N; ++c)
+        for (int c = 0; c < N; ++c) {
+            const int g = lane & 16, first = col + 16 * c + (lane & 15);
+            uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = col + 16 * c + i;
-            if (r >= a.R) continue;
-            float x[2];
-            f8_split(f[c0 + c][i / 2], x[0], x[1]);
-            const int64_t at = (row0 + lane) * a.ldo + r;
-            if (a.out_fp32) static_cast<float*>(a.out)[at] = x[i % 2];
-            else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(x[i % 2]);
+            for (int i = 0; i < 8; ++i) {
+                float x, y;
+                f8_split(f[c0 + c][i], x, y);
+                w[2 * i] = __float_as_uint(x), w[2 * i + 1] = __float_as_uint(y);
+            }
+            f8_store_odd<16>(static_cast<uint8_t*>(a.out) + (row0 + g) * pitch + (int64_t)first * 4, pitch, rows - g, w,
+                             a.R - first, true);
         }
+    } else {
+        constexpr int W = 8 * N;
+        const int g = lane & ~(W - 1), first = col + 2 * (lane & (W - 1));
+        uint32_t w[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = f8_bf16(f[c0 + i / 8][i % 8]);
+        f8_store_odd<W>(static_cast<uint8_t*>(a.out) + (row0 + g) * pitch + (int64_t)first * 2, pitch, rows - g, w,
+                        a.R - first, false);
+    }
 }
 
 // D: blocks of a stage and of a buffer (those behind K are zeros); MC: chunks
@@ -479,37 +522,38 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 const int most = (nch + a.slices - 1) / a.slices, at = wq * 32 + lane;
 #pragma unroll
                 for (int c = 0; c < MC; ++c) {
-                    const int i = c0 + c, owner = i % a.slices;
-                    if (c < own || owner == slice) continue;
-                    const uint32_t to =
-                        map_rank(base, (unsigned)owner) + (uint32_t)((slice * most + i / a.slices) * 2048 + at) * 4u;
+                    const int i = c0 + c;
+                    if (c < own) continue;
+                    const uint32_t to = map_rank(base, (unsigned)(i % a.slices)) +
+                                        (uint32_t)((slice * most + i / a.slices) * 2048 + at) * 4u;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         float x, y;
                         f8_split(acc[c][q], x, y);
                         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 1024u * q), "f"(x) : "memory");
-                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 1024u * q + 512u), "f"(y) : "memory");
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 1024u * q + 512u), "f"(y)
+                                     : "memory");
                     }
                 }
                 ex_cluster_meet();
                 met = true;
-#pragma unroll
-                for (int c = 0; c < MC; ++c) {
-                    const int i = c0 + c;
-                    if (c < own || i % a.slices != slice || !ok) continue;
+                // (its own sums from there too, in a loop: code that runs once costs its way to the SM)
+#pragma unroll 1
+                for (int i = c0 + own; i < c0 + MC && ok; ++i) {
+                    if (i % a.slices != slice) continue;
                     F8Pair sum[1][8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) sum[0][q] = 0ull;
+#pragma unroll 1
                     for (int z = 0; z < a.slices; ++z) {
                         const uint32_t from = base + (uint32_t)((z * most + i / a.slices) * 2048 + at) * 4u;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            F8Pair x = acc[c][q];
-                            if (z != slice) x = f8_pair(f8_lds(from + 1024u * q), f8_lds(from + 1024u * q + 512u));
-                            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[0][q]) : "l"(x));
-                        }
+                        for (int q = 0; q < 8; ++q)
+                            asm("add.rn.f32x2 %0, %0, %1;"
+                                : "+l"(sum[0][q])
+                                : "l"(f8_pair(f8_lds(from + 1024u * q), f8_lds(from + 1024u * q + 512u))));
                     }
-                    f8_store<1>(a, row0, rows, col0 + 16 * c, sum, 0);
+                    f8_store<1>(a, row0, rows, ct * a.n + 16 * i, sum, 0);
                 }
             } else if (ok) {
                 // two chunks at a time (in fp32 one): 64 bytes of a row
