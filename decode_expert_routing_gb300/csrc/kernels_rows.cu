@@ -32,10 +32,6 @@ template <>
 struct Vec<8> { using T = uint2; };
 template <>
 struct Vec<4> { using T = uint32_t; };
-template <>
-struct Vec<2> { using T = uint16_t; };
-template <>
-struct Vec<1> { using T = uint8_t; };
 
 // N elements of one vector load as fp32, and back with one rounding.
 template <int TYPE, int BYTES>
@@ -60,11 +56,6 @@ struct Elems {
             uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
             for (int i = 0; i < N; ++i) w[i] = __float_as_uint(f[i]);
-        } else if constexpr (N == 1) {
-            uint16_t u;
-            if (TYPE == kRowBf16) asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(u) : "f"(f[0]));
-            else u = __half_as_ushort(__float2half_rn(f[0]));
-            v = u;
         } else {
             uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
@@ -78,13 +69,12 @@ struct Elems {
     }
 };
 
-// Rows whose words do not start on 16 bytes (odd lengths, odd strides), shifted: a thread
-// still takes an aligned 16-byte word of the row that is written, and reads the
-// two aligned words that hold those bytes of each other row, which it shifts
-// into place.  (Element by element 4096 x 4 rows of 1001 took 27 us each way, so
-// 18 and 15.)
-// Words that leave the operand's memory [lo, hi) are read by element, so nothing
-// beside it is.
+// Rows whose words do not start on 16 bytes (odd lengths, odd strides), shifted:
+// a thread still takes an aligned 16-byte word of the row that is written, and
+// reads the two aligned words that hold those bytes of each other row, which it
+// shifts into place.  (Element by element 4096 x 4 rows of 1001 took 27 us each
+// way, so 18 and 15.)  Words that leave the operand's memory [lo, hi) are read by
+// element, so nothing beside it is.
 struct Words {
     uint4 a, b;
     unsigned shift;  // bytes
@@ -260,7 +250,7 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExperts
 
 // Rows of 1- and 2-byte units that start anywhere, as they are: to_experts_kernel's MODE 0 with shifted words.  (Rows
 // of whole 4- or 8-byte words go faster as such: 2048 x 4 rows of 6142 33 us, shifted 42; of 6143 element by element
-// 44, 1000 x 4 30 and 28.  With the weights' sums, MODE 1, shifting both rows gains nothing: 63 us and 67.)
+// 44, 1000 x 4 30 and 28.)
 template <int UNIT>
 __global__ void __launch_bounds__(kRowThreads) to_experts_shift_kernel(const ToExpertsArgs a, int lanes, int shift,
                                                                        int slab) {
@@ -293,6 +283,74 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_shift_kernel(const ToE
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (c + u * lanes < c1) store_words<UNIT>(out, (c + u * lanes) * 16 - off, a.row_bytes, shifted(v[u]));
+    }
+}
+
+// MODE 1 of rows of 2-byte units that start anywhere, both rows shifted.  (2048 x 4 rows of 6143 63 us, element by
+// element 67, 16 x 4 4.8 and 8.5; of whole 4- or 8-byte words 63, as such 52 and 49.)
+template <int TYPE>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_shift_kernel(const ToExpertsArgs a, int lanes, int shift) {
+    using E = Elems<TYPE, 16>;
+    constexpr int U = 2;
+    __shared__ float s_dot[kRowThreads / 32];
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & (lanes - 1), mk = a.M * a.topk;
+    const int64_t p = ((int64_t)blockIdx.x << (__ffs(kRowThreads) - 1 - shift)) + (tid >> shift);
+    const int64_t i0 = (int64_t)blockIdx.x * kRowThreads + tid;
+    if (i0 < mk && (uint64_t)(int64_t)a.known[i0] >= (uint64_t)a.cap) a.grad_w[i0] = 0.0f;
+    int f = -1;
+    bool row = false;
+    if (p < a.cap) {
+        f = __ldg(a.sorted + p);
+        row = p < __ldg(a.npost);
+    }
+    const bool real = row && (unsigned)f < (unsigned)mk;
+    // the row that is written, its words counted from the 16 bytes that hold its first byte on
+    uint8_t* out = static_cast<uint8_t*>(a.out) + p * a.row_bytes;
+    const int off = (int)(reinterpret_cast<uintptr_t>(out) & 15u), words = (off + a.row_bytes + 15) / 16;
+    float dot = 0.0f;
+    if (real) {
+        const uint8_t *x = static_cast<const uint8_t*>(a.x), *y = static_cast<const uint8_t*>(a.y);
+        const Source xs = source(x + (int64_t)((unsigned)f / (unsigned)a.topk) * a.ldx, off, x, x + a.x_bytes);
+        const Source ys = source(y + p * a.ldy, off, y, y + a.y_bytes);
+        const float w = a.weights == nullptr ? 1.0f : __ldg(a.weights + f);
+        for (int c = lane; c < words; c += lanes * U) {
+            Words gv[U], yv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c + u * lanes >= words) continue;
+                gv[u] = load_words<2>(xs, c + u * lanes, off, a.row_bytes);
+                yv[u] = load_words<2>(ys, c + u * lanes, off, a.row_bytes);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c + u * lanes >= words) continue;
+                const int at = (c + u * lanes) * 16 - off;
+                float g[E::N], z[E::N];
+                E::get(shifted(gv[u]), g);
+                E::get(shifted(yv[u]), z);
+#pragma unroll
+                for (int i = 0; i < E::N; ++i) {
+                    if (at + 2 * i >= 0 && at + 2 * i < a.row_bytes) dot = __fmaf_rn(g[i], z[i], dot);
+                    g[i] = __fmul_rn(w, g[i]);
+                }
+                // (out may be y itself: a thread reads its words before it writes them, and no other does)
+                store_words<2>(out, at, a.row_bytes, E::put(g));
+            }
+        }
+    } else if (row) {
+        for (int c = lane; c < words; c += lanes)
+            store_words<2>(out, c * 16 - off, a.row_bytes, make_uint4(0u, 0u, 0u, 0u));
+    }
+    dot = warp_sum_fixed(dot);
+    const int warps = lanes / 32, warp = tid >> 5;
+    if ((tid & 31) == 0) s_dot[warp] = dot;
+    __syncthreads();
+    if (real && lane == 0) {
+        float s = 0.0f;
+        for (int i = 0; i < warps; ++i) s = __fadd_rn(s, s_dot[warp + i]);
+        a.grad_w[f] = s;
     }
 }
 
@@ -513,6 +571,18 @@ cudaError_t launch_experts_shift(const ToExpertsArgs& a, cudaStream_t st) {
                              slab);
 }
 
+template <int TYPE>
+cudaError_t launch_combine_grad_shift(const ToExpertsArgs& a, cudaStream_t st) {
+    const int vecs = (a.row_bytes + 30) / 16, most = a.cap >= 4096 ? 64 : 256;  // (words: at most; lanes as above)
+    int lanes = 32;
+    while (lanes < most && lanes < vecs) lanes *= 2;
+    const int64_t per = kRowThreads / lanes, mk = (int64_t)a.M * a.topk;
+    int64_t ctas = (a.cap + per - 1) / per;
+    if (ctas * kRowThreads < mk) ctas = (mk + kRowThreads - 1) / kRowThreads;  // (a thread for each assignment)
+    return launch_overlapped(combine_grad_shift_kernel<TYPE>, dim3((unsigned)ctas), dim3(kRowThreads), 0, st, a, lanes,
+                             log2_of(lanes));
+}
+
 template <int TYPE, bool SHIFT>
 cudaError_t launch_tokens_v(const ToTokensArgs& a, cudaStream_t st) {
     const int vecs = (a.row_bytes + (SHIFT ? 15 : 0) + 15) / 16;  // (at most)
@@ -557,6 +627,7 @@ cudaError_t launch_to_experts(const ToExpertsArgs& a0, cudaStream_t st) {
     a.ldy *= eb;
     a.row_bytes = a.K * eb;
     a.x_bytes = (a.M - 1) * a.ldx + a.row_bytes;
+    a.y_bytes = (a.cap - 1) * a.ldy + a.row_bytes;
     uintptr_t bits = bits_of(a.x) | bits_of(a.out) | (uintptr_t)a.ldx | (uintptr_t)a.row_bytes;
     if (a.y != nullptr) bits |= bits_of(a.y) | (uintptr_t)a.ldy;
     const int v = vec_bytes(bits, eb);
@@ -569,12 +640,14 @@ cudaError_t launch_to_experts(const ToExpertsArgs& a0, cudaStream_t st) {
             default: return launch_experts_shift<1>(a, st);
         }
     }
-#define MR_EXPERTS(T)                                              \
-    switch (v) {                                                   \
-        case 16: return launch_experts_v<1, T, 16>(a, st);         \
-        case 8: return launch_experts_v<1, T, 8>(a, st);           \
-        case 4: return launch_experts_v<1, T, 4>(a, st);           \
-        default: return launch_experts_v<1, T, T == kRowFp32 ? 4 : 2>(a, st); \
+    if (v == 2)
+        return a.type == kRowBf16 ? launch_combine_grad_shift<kRowBf16>(a, st)
+                                  : launch_combine_grad_shift<kRowFp16>(a, st);
+#define MR_EXPERTS(T)                                         \
+    switch (v) {                                              \
+        case 16: return launch_experts_v<1, T, 16>(a, st);    \
+        case 8: return launch_experts_v<1, T, 8>(a, st);      \
+        default: return launch_experts_v<1, T, 4>(a, st);     \
     }
     if (a.type == kRowBf16) MR_EXPERTS(kRowBf16)
     if (a.type == kRowFp16) MR_EXPERTS(kRowFp16)

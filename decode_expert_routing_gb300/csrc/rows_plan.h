@@ -24,8 +24,8 @@ struct ToExpertsArgs {
     void* out;             // [cap, K]
     int64_t cap;
     int M, K, topk, E, type;
-    int row_bytes;         // of a row; this and x_bytes, from the first row's start to the last one's end, are
-    int64_t x_bytes;       // set by the launcher
+    int row_bytes;         // of a row; this, x_bytes and y_bytes, from the first row's start to the last one's
+    int64_t x_bytes, y_bytes;  // end, are set by the launcher
 };
 // Back to the tokens: out[m] = add[m] + sum_j weights[m, j] y[positions[m, j]].
 struct ToTokensArgs {

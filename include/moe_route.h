@@ -751,8 +751,9 @@ typedef enum mr_row_type {
  * positions: [M, topk].  sorted_token_ids: capacity entries, as mr_moe_sort or
  * the route wrote them (each assignment at one position at most).  rows and
  * positions overlap nothing that is read.  Any K >= 1 and alignment of the
- * type (16-byte aligned rows are moved in 16-byte words).  topk <= 32, M *
- * topk < 2^30, capacity < 2^31.  One launch.
+ * type (16-byte aligned rows are moved in 16-byte words; of others what lies
+ * between an operand's rows may be read too, and changes nothing).  topk <= 32,
+ * M * topk < 2^30, capacity < 2^31.  One launch.
  */
 typedef struct mr_moe_permute_params {
     const void *x;
