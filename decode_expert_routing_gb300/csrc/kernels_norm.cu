@@ -112,10 +112,10 @@ cudaError_t launch_fp8_quant(const void* x, int64_t ldx, int M, int K, uint8_t* 
 // ------------------------------------------------------------------ residual + RMSNorm
 //
 // One CTA per row, the row in registers: C chunks of 8 elements a thread.  Of
-// many rows memory bounds it: 4096 x 6144 with sres and FP8 codes 33 us, 5.4 TB/s,
-// 80 % of a plain copy's rate (a row's CTA reads nothing while it sums; persistent
+// many rows memory bounds it: 4096 x 6144 with sres and FP8 codes 32 us, 5.5 TB/s,
+// 83 % of a plain copy's rate (a row's CTA reads nothing while it sums; persistent
 // CTAs that load the next row ahead took 41).  Of few the launch, one load's way
-// and the sum's: 1 row 2.6 us, 48 2.9.
+// and the sum's: 1 row 2.5 us, 48 2.8.
 //   sres = bf16(x + residual)
 //   rstd = 1 / sqrt(mean(sres^2) + eps)
 //   xn   = bf16((sres * rstd) * s)      (norm_pair, as the route and mr_norm_apply have it)
