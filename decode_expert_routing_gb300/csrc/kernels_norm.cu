@@ -122,12 +122,14 @@ cudaError_t launch_fp8_quant(const void* x, int64_t ldx, int M, int K, uint8_t* 
 // and xn's codes, exactly as the quantisers of this library write them.
 //
 // rstd is the value of the formula rounded once, but for about one row in
-// 10^5: the squares of bf16 numbers are exact in fp32, their sum is kept with
-// its rounding errors (Knuth's two-sum, hi + lo), and the division and the
-// root are put right by one Newton step in the same arithmetic.  What follows
-// rounds to bf16, and a rstd one step off would move some values in 10^4 to
-// their other neighbour, and the scale of a group with them; it makes the
-// codes those of the formula, whatever the order of the sum.
+// 10^5: the squares of bf16 numbers are exact in fp32 (those below 2^-126 but
+// for 2^-150), their sum is kept with its rounding errors (Knuth's two-sum, hi
+// + lo), and the division and the root are put right by one Newton step in the
+// same arithmetic.  What follows rounds to bf16, and a rstd one step off would
+// move some values in 10^4 to their other neighbour, and the scale of a group
+// with them; it makes the codes those of the formula, whatever the order of the
+// sum.  A sum beyond fp32, or one so small that the squares' last bits count
+// beside eps, is taken again with scaled squares (norm_rstd_scaled).
 
 struct Two {
     float hi, lo;
@@ -174,6 +176,12 @@ __device__ __forceinline__ uint32_t pair_to_bf16(Pair p) {
     return d;
 }
 
+// Whether a row's sum of squares, taken as they are, is right to 2^-70 of itself
+// or of K eps: up to 65536 squares that are each off by at most 2^-150, and
+// none of whose sums is beyond fp32 (then it is infinite or NaN).
+__device__ __forceinline__ bool norm_fits(Two sum, float eps) {
+    return sum.hi < __int_as_float(0x7f800000) && (sum.hi >= 0x1p-60f || eps >= 0x1p-60f);
+}
 // 1 / sqrt((hi + lo) / K + eps)
 __device__ __forceinline__ float norm_rstd(Two sum, int K, float eps) {
     const float k = (float)K;  // exact: K <= 65536
@@ -184,16 +192,135 @@ __device__ __forceinline__ float norm_rstd(Two sum, int K, float eps) {
     const float h = v.hi, l = __fadd_rn(v.lo, ql);
     const float r = rsqrtf(h);
     if (!(h > 0.0f && h < __int_as_float(0x7f800000))) return r;  // 0, infinite or NaN
-    // one step: r + r (1 - (h + l) r^2) / 2, the bracket from the exact square of r
-    const float p = __fmul_rn(r, r), pl = __fmaf_rn(r, r, -p);
-    float e = __fmaf_rn(-h, p, 1.0f);
-    e = __fmaf_rn(-h, pl, e);
-    e = __fmaf_rn(-l, p, e);
+    // one step: r + r (1 - (h + l) r r) / 2, the bracket from the exact product h r (the square of r leaves fp32 where
+    // h is below 2^-128 or its last bits where h is above 2^100)
+    const float t = __fmul_rn(h, r), tl = __fmaf_rn(h, r, -t);
+    float e = __fmaf_rn(-t, r, 1.0f);
+    e = __fmaf_rn(-tl, r, e);
+    e = __fmaf_rn(-__fmul_rn(l, r), r, e);
     return __fmaf_rn(__fmul_rn(r, 0.5f), e, r);
 }
 
+// xn and its codes of the chunks c0, c0 + step, ... below vpr of a row m, one
+// thread's (a warp's threads call it together); v: the row's values.
+template <int C, int FMT>
+__device__ __forceinline__ void norm_write(const NormArgs& a, int64_t m, int c0, int step, int vpr, const uint4 (&v)[C],
+                                           const uint4 (&g)[C], float rstd) {
+    const int lane = threadIdx.x & 31;
+    const Pair rr = pair_of(__float_as_uint(rstd), __float_as_uint(rstd)), ones = pair_of(0x3F800000u, 0x3F800000u);
+    uint4 n[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        // norm_pair's steps (a row's end: zeros, whatever rstd is)
+        const int c = c0 + i * step;
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, w[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+        uint32_t* o = &n[i].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Pair k = a.gemma ? pair_add(ones, pair_bf16(w[j])) : pair_bf16(w[j]);
+            o[j] = pair_to_bf16(pair_mul(pair_mul(pair_bf16(x[j]), rr), k));
+        }
+        if (c >= vpr) n[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.xn != nullptr && c < vpr) *reinterpret_cast<uint4*>(a.xn + m * a.K + c * 8) = n[i];
+    }
+    if constexpr (FMT == 3) {
+        float amax[C], s[C], inv[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) amax[i] = fp8_amax_16th(n[i]);
+        fp8_scales(amax, s, inv);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = c0 + i * step;
+            const uint2 q = fp8_codes(n[i], inv[i]);
+            if (c >= vpr) continue;
+            *reinterpret_cast<uint2*>(a.q + m * a.K + c * 8) = q;
+            if ((lane & 15) == 0) static_cast<float*>(a.scale)[m * ((a.K + kFp8Group - 1) / kFp8Group) + c / 16] = s[i];
+        }
+    }
+    if constexpr (FMT == 1 || FMT == 2) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = c0 + i * step;
+            unsigned sb;
+            if (FMT == 1) {
+                const uint2 q = mx_quant_quad(n[i], &sb);
+                if (c < vpr) *reinterpret_cast<uint2*>(a.q + m * a.K + c * 8) = q;
+            } else {
+                const uint32_t q = mx4_quant_quad(n[i], &sb);
+                if (c < vpr) *reinterpret_cast<uint32_t*>(a.q + m * (a.K / 2) + c * 4) = q;
+            }
+            if (c < vpr && (lane & 3) == 0) static_cast<uint8_t*>(a.scale)[m * (a.K / 32) + c / 4] = (uint8_t)sb;
+        }
+    }
+}
+
+// A row whose sum does not fit, taken again by its whole CTA; small: its sum is
+// below 2^-60.  The values of a small one are taken times 2^90, so that every
+// square is above 2^-86 and the sum below 2^120; the squares of a large one times
+// 2^-32.  Both are exact, but for squares that are below 2^-117 of a large sum.  A
+// square beyond fp32, of values from 2^64 on, stays infinite and makes rstd 0; a
+// NaN stays one.
+// The rows that fit pay for none of it (4096 x 6144, FP8: 32.0 us as without it):
+// it is a call behind all else, it reads the row again, and its arguments are a
+// second copy of the kernel's, whose address may be taken.  (The address of the
+// first copy, which the kernel itself works with: 33.2 us and at 500 rows 7.0
+// for 5.5, MXFP8; a copy on the stack: 0.1 us a launch; in the kernel's body, from
+// the row's registers: 34.3.)
+template <int FMT>
+__device__ __noinline__ void norm_again(const NormArgs& a, bool small, float* s_hi, float* s_lo) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
+    const int vpr = a.K / 8;
+    const int64_t m = blockIdx.x;
+    const float by = small ? 0x1p90f : 1.0f, by2 = small ? 1.0f : 0x1p-32f;
+    // (a thread reads the sum that it wrote itself: sres may be x or residual)
+    auto chunk = [&](int c) {
+        if (a.sres != nullptr) return *reinterpret_cast<const uint4*>(a.sres + m * a.lds + c * 8);
+        uint4 v = *reinterpret_cast<const uint4*>(a.x + m * a.ldx + c * 8);
+        if (a.residual != nullptr) {
+            const uint4 r = *reinterpret_cast<const uint4*>(a.residual + m * a.ldr + c * 8);
+            uint32_t* p = &v.x;
+            const uint32_t* q = &r.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = pair_to_bf16(pair_add(pair_bf16(p[j]), pair_bf16(q[j])));
+        }
+        return v;
+    };
+    Two sum{0.0f, 0.0f};
+#pragma unroll 1
+    for (int c = tid; c < vpr; c += nthr) {
+        const uint4 v = chunk(c);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = __fmul_rn(__uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16), by);
+            sum = two_add(sum, Two{__fmul_rn(__fmul_rn(x, x), by2), 0.0f});
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum = two_add(sum, Two{__shfl_xor_sync(kFull, sum.hi, o), __shfl_xor_sync(kFull, sum.lo, o)});
+    __syncthreads();  // (the first sums have been read)
+    if (lane == 0) s_hi[warp] = sum.hi, s_lo[warp] = sum.lo;
+    __syncthreads();
+    sum = lane < nw ? Two{s_hi[lane], s_lo[lane]} : Two{0.0f, 0.0f};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum = two_add(sum, Two{__shfl_xor_sync(kFull, sum.hi, o), __shfl_xor_sync(kFull, sum.lo, o)});
+    const float eps = __fmul_rn(__fmul_rn(__fmul_rn(a.eps, by), by), by2);
+    const float rstd = __fmul_rn(norm_rstd(sum, a.K, eps), small ? by : 0x1p-16f);
+    if (tid == 0 && a.rstd != nullptr) a.rstd[m] = rstd;
+    if (FMT == 0 && a.xn == nullptr) return;
+#pragma unroll 1
+    for (int c = tid; c - lane < vpr; c += nthr) {
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u), v[1] = {c < vpr ? chunk(c) : zero};
+        const uint4 g[1] = {c < vpr ? ld_ro_v4(a.g + c * 8) : zero};
+        norm_write<1, FMT>(a, m, c, 0, vpr, v, g, rstd);
+    }
+}
+
 template <int C, int FMT, int T>
-__global__ void __launch_bounds__(T, T == 256 && C == 3 && FMT == 3 ? 5 : 1) add_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(T, T == 256 && C == 3 && FMT == 3 ? 5 : 1)
+    add_norm_kernel(const NormArgs a, const __grid_constant__ NormArgs same) {
     __shared__ float s_hi[32], s_lo[32], s_rstd;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
     const int vpr = a.K / 8;
@@ -247,7 +374,9 @@ __global__ void __launch_bounds__(T, T == 256 && C == 3 && FMT == 3 ? 5 : 1) add
 #pragma unroll
         for (int o = T > 256 ? 16 : 4; o > 0; o >>= 1)
             sum = two_add(sum, Two{__shfl_xor_sync(kFull, sum.hi, o), __shfl_xor_sync(kFull, sum.lo, o)});
+        // (-1, -2: of a sum that does not fit, small or large)
         rstd = norm_rstd(sum, a.K, a.eps);
+        rstd = norm_fits(sum, a.eps) ? rstd : sum.hi < 0x1p-60f ? -1.0f : -2.0f;
         if (tid == 0) {
             s_rstd = rstd;
             if (a.rstd != nullptr) a.rstd[m] = rstd;
@@ -257,62 +386,20 @@ __global__ void __launch_bounds__(T, T == 256 && C == 3 && FMT == 3 ? 5 : 1) add
         __syncthreads();
         rstd = s_rstd;
     }
-    if (FMT == 0 && a.xn == nullptr) return;
-    const Pair rr = pair_of(__float_as_uint(rstd), __float_as_uint(rstd)), ones = pair_of(0x3F800000u, 0x3F800000u);
-    uint4 n[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        // norm_pair's steps (a row's end: zeros, whatever rstd is)
-        const int c = tid + i * nthr;
-        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, w[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
-        uint32_t* o = &n[i].x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const Pair k = a.gemma ? pair_add(ones, pair_bf16(w[j])) : pair_bf16(w[j]);
-            o[j] = pair_to_bf16(pair_mul(pair_mul(pair_bf16(x[j]), rr), k));
-        }
-        if (c >= vpr) n[i] = zero;
-        if (a.xn != nullptr && c < vpr) *reinterpret_cast<uint4*>(a.xn + m * a.K + c * 8) = n[i];
-    }
-    if constexpr (FMT == 3) {
-        float amax[C], s[C], inv[C];
-#pragma unroll
-        for (int i = 0; i < C; ++i) amax[i] = fp8_amax_16th(n[i]);
-        fp8_scales(amax, s, inv);
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int c = tid + i * nthr;
-            const uint2 q = fp8_codes(n[i], inv[i]);
-            if (c >= vpr) continue;
-            *reinterpret_cast<uint2*>(a.q + m * a.K + c * 8) = q;
-            if ((lane & 15) == 0) static_cast<float*>(a.scale)[m * ((a.K + kFp8Group - 1) / kFp8Group) + c / 16] = s[i];
-        }
-    }
-    if constexpr (FMT == 1 || FMT == 2) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int c = tid + i * nthr;
-            unsigned sb;
-            if (FMT == 1) {
-                const uint2 q = mx_quant_quad(n[i], &sb);
-                if (c < vpr) *reinterpret_cast<uint2*>(a.q + m * a.K + c * 8) = q;
-            } else {
-                const uint32_t q = mx4_quant_quad(n[i], &sb);
-                if (c < vpr) *reinterpret_cast<uint32_t*>(a.q + m * (a.K / 2) + c * 4) = q;
-            }
-            if (c < vpr && (lane & 3) == 0) static_cast<uint8_t*>(a.scale)[m * (a.K / 32) + c / 4] = (uint8_t)sb;
-        }
-    }
+    // (a row whose sum does not fit is written by norm_again alone)
+    const bool fits = rstd >= 0.0f;
+    if (FMT != 0 || a.xn != nullptr) norm_write<C, FMT>(a, m, tid, nthr, fits ? vpr : 0, v, g, rstd);
+    if (!fits) norm_again<FMT>(same, rstd == -1.0f, s_hi, s_lo);
 }
 
 template <int C, int T>
 cudaError_t launch_norm_c(const NormArgs& a, cudaStream_t st) {
-    void (*kernel)(const NormArgs) = a.fmt == 0   ? add_norm_kernel<C, 0, T>
-                                     : a.fmt == 1 ? add_norm_kernel<C, 1, T>
-                                     : a.fmt == 2 ? add_norm_kernel<C, 2, T>
-                                                  : add_norm_kernel<C, 3, T>;
+    void (*kernel)(const NormArgs, const NormArgs) = a.fmt == 0   ? add_norm_kernel<C, 0, T>
+                                                     : a.fmt == 1 ? add_norm_kernel<C, 1, T>
+                                                     : a.fmt == 2 ? add_norm_kernel<C, 2, T>
+                                                                  : add_norm_kernel<C, 3, T>;
     const int threads = ((a.K / 8 + C - 1) / C + 31) / 32 * 32;
-    return launch_overlapped(kernel, dim3((unsigned)a.M), dim3((unsigned)threads), 0, st, a);
+    return launch_overlapped(kernel, dim3((unsigned)a.M), dim3((unsigned)threads), 0, st, a, a);
 }
 
 cudaError_t launch_add_norm(const NormArgs& a, cudaStream_t st) {

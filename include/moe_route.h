@@ -655,9 +655,13 @@ int mr_moe_down(const mr_moe_down_params *params, void *stream);
  *                of the bf16 rows, bit for bit.
  * The sum of squares is kept with its rounding errors and rstd is the
  * formula's value rounded to nearest but for about one row in 10^5, so it
- * depends on no order of summation.  Squares beyond fp32 (|sres| above 1.8e19)
- * make rstd 0, a NaN or an infinity in a row makes the row NaN (an infinity:
- * rstd 0, itself NaN and the others 0).
+ * depends on no order of summation.  That holds for rows of any size below
+ * 2^64, subnormals too: a sum of squares beyond fp32, or so small that squares
+ * have lost bits, is taken again with scaled squares (such rows take about twice
+ * as long).  A rstd beyond fp32 is infinite.  A value whose own square is
+ * beyond fp32 (|sres| from 2^64 = 1.8e19 on) makes its row's rstd 0; a NaN or an
+ * infinity in a row makes the row NaN (an infinity: rstd 0, itself NaN and the
+ * others 0).
  * x, residual: bf16 with row strides ldx, ldr in elements; norm_weight: bf16
  * [K]; eps >= 0, finite.  Outputs, each optional (NULL) but one at least: sres
  * bf16 with row stride lds (it may be x or residual itself, with that one's
