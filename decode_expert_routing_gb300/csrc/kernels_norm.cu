@@ -318,8 +318,22 @@ __device__ __noinline__ void norm_again(const NormArgs& a, bool small, float* s_
     }
 }
 
+// CTAs of 256 threads that an SM's registers are shared among, by the chunks of
+// a thread: as many as hold a row's operands with at most 80 bytes spilled, so
+// that one row's loads run beside another's sum.  Left to the compiler (85 to 134
+// registers, one CTA less) 4096 x 7168 takes 69.5 us with FP8 codes (39.0), 43.6
+// with MXFP8 (38.8), 36.9 without (36.4); x 12288 90.4 (68.2), 75.0 (65.5), 67.7
+// (61.9); x 16384 163 (128), 93.1 (92.9), 84.9 (84.3).  With three chunks FP8
+// codes, whose loads the compiler puts one behind another anyway, take five (4096
+// x 6144 32.0 us, four 33.9; x 5120 29.3 and 31.1; 500 rows 7.3 and 6.9), the
+// others four (1000 x 6144 9.7 us, five 10.5; 500 rows 5.5 and 8.0; 4096 33.1 and
+// 31.7).
+constexpr int norm_ctas(int T, int C, int FMT) {
+    return T > 256 ? 1 : C == 1 ? 6 : C == 2 ? 5 : C == 3 ? (FMT == 3 ? 5 : 4) : C == 4 ? 4 : C == 6 ? 3 : 2;
+}
+
 template <int C, int FMT, int T>
-__global__ void __launch_bounds__(T, T == 256 && C == 3 && FMT == 3 ? 5 : 1)
+__global__ void __launch_bounds__(T, norm_ctas(T, C, FMT))
     add_norm_kernel(const NormArgs a, const __grid_constant__ NormArgs same) {
     __shared__ float s_hi[32], s_lo[32], s_rstd;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
