@@ -9,12 +9,12 @@ namespace mr {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// 16-byte streaming load of data read once per launch (the gate weight):
-// read-only path, no L1 allocation.  volatile: the load is issued where it
-// is written, so loads of parameters placed before the programmatic-
+// 16-byte streaming load of a weight that the kernel launched before does not
+// write (the gate weight): read-only path, no L1 allocation.  volatile: the load
+// is issued where it is written, so loads placed before the programmatic-
 // dependent-launch wait are in flight while the kernel waits (a plain asm
 // without memory operands may be sunk to its first use, after the wait).
-__device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
+__device__ __forceinline__ uint4 ld_weight_v4(const void* p) {
     uint4 r;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
@@ -22,11 +22,23 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
     return r;
 }
 
-// 16-byte read-only load that may be served from L1 (activations reused by
-// the warps of one CTA).
-__device__ __forceinline__ uint4 ld_ro_v4(const void* p) {
-    return __ldg(reinterpret_cast<const uint4*>(p));
+// Everything else is read after pdl_wait() and not by the read-only path (no .nc,
+// no __ldg): such a load states that the memory does not change while the kernel
+// is resident, and the compiler may put it before the wait, where the kernel
+// launched before is still writing.  (It did so with the rows of add_norm_kernel.)
+
+// 16-byte streaming load of data read once per launch: no L1 allocation.
+__device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
 }
+
+// 16-byte load that may be served from L1 (activations reused by the warps of
+// one CTA).
+__device__ __forceinline__ uint4 ld_v4(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // D += A * B for one m16n8k16 bf16 tile with fp32 accumulation (no side
 // effects beyond its outputs, so the compiler may interleave independent ones).

@@ -205,7 +205,7 @@ __device__ __forceinline__ uint4 ex_scales16(const uint8_t* at, int left, uint4 
         for (int i = 0; i < 4; ++i) {
             w[i] = 0u;
             for (int u = 0; u < 4; ++u)
-                if (4 * i + u < left) w[i] |= (uint32_t)__ldg(at + 4 * i + u) << (8 * u);
+                if (4 * i + u < left) w[i] |= (uint32_t)at[4 * i + u] << (8 * u);
         }
     }
 #pragma unroll
@@ -564,11 +564,11 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                     v[g] = make_uint4(0u, 0u, 0u, 0u);
                     if (g >= G) continue;
                     if (a.sf_vec == 16) {
-                        if (b < a.kb) v[g] = __ldg(reinterpret_cast<const uint4*>(row[g] + b));
+                        if (b < a.kb) v[g] = ld_v4(row[g] + b);
                     } else {
                         uint2 lo = make_uint2(0u, 0u), hi = make_uint2(0u, 0u);
-                        if (b < a.kb) lo = __ldg(reinterpret_cast<const uint2*>(row[g] + b));
-                        if (b + 8 < a.kb) hi = __ldg(reinterpret_cast<const uint2*>(row[g] + b + 8));
+                        if (b < a.kb) lo = *reinterpret_cast<const uint2*>(row[g] + b);
+                        if (b + 8 < a.kb) hi = *reinterpret_cast<const uint2*>(row[g] + b + 8);
                         v[g] = make_uint4(lo.x, lo.y, hi.x, hi.y);
                     }
                 }
@@ -582,8 +582,8 @@ __global__ void __launch_bounds__(ex_threads(OP), 1) expert_kernel(const __grid_
                 for (int g = 0; g < 4; ++g) {
                     const uint8_t* p = near(g, b);
                     const bool get = whole(p) && g < G && b < a.kb;
-                    lo[g] = get ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
-                    hi[g] = get ? __ldg(reinterpret_cast<const uint4*>(p) + 1) : make_uint4(0u, 0u, 0u, 0u);
+                    lo[g] = get ? ld_v4(p) : make_uint4(0u, 0u, 0u, 0u);
+                    hi[g] = get ? ld_v4(p + 16) : make_uint4(0u, 0u, 0u, 0u);
                 }
             };
             auto shift = [&](uint4 (&v)[4], const uint4 (&lo)[4], const uint4 (&hi)[4], int b) {

@@ -80,7 +80,7 @@ __device__ __forceinline__ void gemv_tile(const GemvArgs& a, int nblk, int split
     uint4 wv[C::KS];
     const uint16_t* wrow = a.w + (int64_t)n * a.K + kbeg;
 #pragma unroll
-    for (int s = 0; s < C::KS; ++s) wv[s] = ld_stream_v4(wrow + s * 32);
+    for (int s = 0; s < C::KS; ++s) wv[s] = ld_weight_v4(wrow + s * 32);
     // The gate weight is never written by the preceding kernel; everything
     // else (x, scratch, outputs) is touched only after it has completed.
     pdl_wait();
@@ -94,8 +94,8 @@ __device__ __forceinline__ void gemv_tile(const GemvArgs& a, int nblk, int split
         const uint16_t* x1 = a.x + (int64_t)r1 * a.ldx + kbeg;
 #pragma unroll
         for (int s = 0; s < C::KS; ++s) {
-            xa[mt][s] = (r0 < a.M) ? ld_ro_v4(x0 + s * 32) : zero;
-            xb[mt][s] = (!C::HALF && r1 < a.M) ? ld_ro_v4(x1 + s * 32) : zero;
+            xa[mt][s] = (r0 < a.M) ? ld_v4(x0 + s * 32) : zero;
+            xb[mt][s] = (!C::HALF && r1 < a.M) ? ld_v4(x1 + s * 32) : zero;
         }
     }
 

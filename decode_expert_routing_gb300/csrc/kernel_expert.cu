@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(kCombineThreads) expert_combine_kernel(const u
                 id[u] = -1;
                 if (j0 + u >= topk) continue;
                 const int64_t f = m * topk + j0 + u, at = f * R + r;
-                id[u] = __ldg(ids + f);
-                w[u] = __ldg(weights + f);
+                id[u] = ids[f];
+                w[u] = weights[f];
                 if (VEC) v[u] = __ldcg(reinterpret_cast<const uint4*>(y + at));
                 else v[u].x = (uint32_t)y[at] << 16;
                 if (VEC && LOW) l[u] = __ldcg(reinterpret_cast<const uint4*>(low + at));

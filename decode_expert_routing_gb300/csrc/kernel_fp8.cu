@@ -408,9 +408,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                     for (int b = 0; b < D; ++b) {
                         const bool in = D == 1 || ki + b < a.KI;  // (behind K: no scale either)
     #pragma unroll
-                        for (int i = 0; i < 2; ++i) x[i][b] = in ? __ldg(xs[i] + ki + b) : 0.0f;
+                        for (int i = 0; i < 2; ++i) x[i][b] = in ? xs[i][ki + b] : 0.0f;
     #pragma unroll
-                        for (int j = 0; j < 3; ++j) w[j][b] = in ? __ldg(ws[j] + ki + b) : 0.0f;
+                        for (int j = 0; j < 3; ++j) w[j][b] = in ? ws[j][ki + b] : 0.0f;
                     }
                 };
                 fetch(k0);

@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) fp8_few_kernel(const __grid
     float nx = 0.0f, nw = 0.0f;  // of one row of x a lane
     auto fetch = [&](int i) {
         const int kb = warp + i * kFewWarps;
-        if (lane < 8 * B && m0 + lane < a.M) nx = __ldg(a.xs + (int64_t)(m0 + lane) * a.ldxs + kb);
-        nw = __ldg(ws + kb);
+        if (lane < 8 * B && m0 + lane < a.M) nx = a.xs[(int64_t)(m0 + lane) * a.ldxs + kb];
+        nw = ws[kb];
     };
     if (mine > 0) fetch(0);
     // bytes of a row's two 16-byte words in a stage: word w of row r is at r * 128 + ((w ^ (r & 7)) << 4)

@@ -319,7 +319,7 @@ __device__ __forceinline__ void quant_rows_to_positions(const uint16_t* x, int64
 #pragma unroll
         for (int u = 0; u < kQuantUnroll; ++u) {
             const int c = c0 + u * 32;
-            v[u] = c < vpr ? ld_ro_v4(xr + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+            v[u] = c < vpr ? ld_v4(xr + c * 8) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < kQuantUnroll; ++u) {
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kSortQuantThreads) psort_kernel(PSortArgs a) {
         ids = all;
         for (int i = tid; i < n_own; i += nthr) own_ids[i] = all[f0 + i];
     } else {
-        for (int i = tid; i < n_own; i += nthr) own_ids[i] = __ldg(a.s.ids + f0 + i);
+        for (int i = tid; i < n_own; i += nthr) own_ids[i] = a.s.ids[f0 + i];
     }
     __syncthreads();
     psort_hist(ids, 0, f0, N, rs.wcnt, pre);
@@ -523,13 +523,13 @@ __global__ void __launch_bounds__(256) norm_apply_kernel(const uint16_t* x, int6
     const int nwarps = (int)((gridDim.x * blockDim.x) >> 5);
     for (int tile = warp_id; tile < tiles; tile += nwarps) {
         const int r = tile / tpr, c0 = (tile - r * tpr) * kQuantTileVec + lane;
-        const float rs = __ldg(rstd + r);
+        const float rs = rstd[r];
         uint4 v[kQuantUnroll], gv[kQuantUnroll];
 #pragma unroll
         for (int u = 0; u < kQuantUnroll; ++u) {
             const int c = c0 + u * 32;
             v[u] = c < vpr ? ld_stream_v4(x + (int64_t)r * ldx + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-            gv[u] = c < vpr ? ld_ro_v4(g + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+            gv[u] = c < vpr ? ld_v4(g + c * 8) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < kQuantUnroll; ++u) {

@@ -112,10 +112,10 @@ cudaError_t launch_fp8_quant(const void* x, int64_t ldx, int M, int K, uint8_t* 
 // ------------------------------------------------------------------ residual + RMSNorm
 //
 // One CTA per row, the row in registers: C chunks of 8 elements a thread.  Of
-// many rows memory bounds it: 4096 x 6144 with sres and FP8 codes 32 us, 5.5 TB/s,
-// 83 % of a plain copy's rate (a row's CTA reads nothing while it sums; persistent
+// many rows memory bounds it: 4096 x 6144 with sres and FP8 codes 34.8 us, 5.1 TB/s,
+// 76 % of a plain copy's rate (a row's CTA reads nothing while it sums; persistent
 // CTAs that load the next row ahead took 41).  Of few the launch, one load's way
-// and the sum's: 1 row 2.5 us, 48 2.8.
+// and the sum's: 1 row 2.5 us, 48 3.1 with MXFP8.
 //   sres = bf16(x + residual)
 //   rstd = 1 / sqrt(mean(sres^2) + eps)
 //   xn   = bf16((sres * rstd) * s)      (norm_pair, as the route and mr_norm_apply have it)
@@ -129,7 +129,7 @@ cudaError_t launch_fp8_quant(const void* x, int64_t ldx, int M, int K, uint8_t* 
 // move some values in 10^4 to their other neighbour, and the scale of a group
 // with them; it makes the codes those of the formula, whatever the order of the
 // sum.  A sum beyond fp32, or one so small that the squares' last bits count
-// beside eps, is taken again with scaled squares (norm_rstd_scaled).
+// beside eps, is taken again with scaled squares (norm_again).
 
 struct Two {
     float hi, lo;
@@ -260,12 +260,8 @@ __device__ __forceinline__ void norm_write(const NormArgs& a, int64_t m, int c0,
 // 2^-32.  Both are exact, but for squares that are below 2^-117 of a large sum.  A
 // square beyond fp32, of values from 2^64 on, stays infinite and makes rstd 0; a
 // NaN stays one.
-// The rows that fit pay for none of it (4096 x 6144, FP8: 32.0 us as without it):
-// it is a call behind all else, it reads the row again, and its arguments are a
-// second copy of the kernel's, whose address may be taken.  (The address of the
-// first copy, which the kernel itself works with: 33.2 us and at 500 rows 7.0
-// for 5.5, MXFP8; a copy on the stack: 0.1 us a launch; in the kernel's body, from
-// the row's registers: 34.3.)
+// It is a call behind all else and reads the row again: in the kernel's body, from
+// the row's registers, it cost every row ten registers a thread.
 template <int FMT>
 __device__ __noinline__ void norm_again(const NormArgs& a, bool small, float* s_hi, float* s_lo) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
@@ -313,28 +309,40 @@ __device__ __noinline__ void norm_again(const NormArgs& a, bool small, float* s_
 #pragma unroll 1
     for (int c = tid; c - lane < vpr; c += nthr) {
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u), v[1] = {c < vpr ? chunk(c) : zero};
-        const uint4 g[1] = {c < vpr ? ld_ro_v4(a.g + c * 8) : zero};
+        const uint4 g[1] = {c < vpr ? ld_v4(a.g + c * 8) : zero};
         norm_write<1, FMT>(a, m, c, 0, vpr, v, g, rstd);
     }
 }
 
+// 16 bytes of a row, streamed; zeros without p.  By predicate, so that a row's loads
+// are issued one behind another (in branches 4096 x 6144 with FP8 codes took 35.7
+// us, so 34.8; x 8192 45.9 and 42.0).
+__device__ __forceinline__ uint4 ld_row_v4(const void* at, bool p) {
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)
+        : "l"(at), "r"((uint32_t)p));
+    return r;
+}
+
 // CTAs of 256 threads that an SM's registers are shared among, by the chunks of
 // a thread: as many as hold a row's operands with at most 80 bytes spilled, so
-// that one row's loads run beside another's sum.  Left to the compiler (85 to 134
-// registers, one CTA less) 4096 x 7168 takes 69.5 us with FP8 codes (39.0), 43.6
-// with MXFP8 (38.8), 36.9 without (36.4); x 12288 90.4 (68.2), 75.0 (65.5), 67.7
-// (61.9); x 16384 163 (128), 93.1 (92.9), 84.9 (84.3).  With three chunks FP8
-// codes, whose loads the compiler puts one behind another anyway, take five (4096
-// x 6144 32.0 us, four 33.9; x 5120 29.3 and 31.1; 500 rows 7.3 and 6.9), the
-// others four (1000 x 6144 9.7 us, five 10.5; 500 rows 5.5 and 8.0; 4096 33.1 and
-// 31.7).
+// that one row's loads run beside another's sum.  Left to the compiler 4096 x
+// 4096 takes 27.0 us with FP8 codes (so 24.3), 26.5 with MXFP8 (23.7), 24.7 without
+// (22.6); x 6144 58.2 (34.8), 36.9 (33.0), 35.2 (31.9); x 8192 66.4 (42.0), 53.7
+// (40.6), 42.2 (41.5); x 12288 167 (64.7), 71.2 (63.5), 64.7 (61.0); x 16384 132
+// (85.4), 125 (90.3), 116 (82.8).  With three chunks FP8 codes, which take more
+// registers, are better off with five (4096 x 6144 34.8 us, four 39.9; 500 rows 7.6
+// and 7.2), the others with four (500 x 6144 with MXFP8 6.9 us, five 7.8; 4096 33.0
+// and 32.3).
 constexpr int norm_ctas(int T, int C, int FMT) {
     return T > 256 ? 1 : C == 1 ? 6 : C == 2 ? 5 : C == 3 ? (FMT == 3 ? 5 : 4) : C == 4 ? 4 : C == 6 ? 3 : 2;
 }
 
 template <int C, int FMT, int T>
-__global__ void __launch_bounds__(T, norm_ctas(T, C, FMT))
-    add_norm_kernel(const NormArgs a, const __grid_constant__ NormArgs same) {
+__global__ void __launch_bounds__(T, norm_ctas(T, C, FMT)) add_norm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float s_hi[32], s_lo[32], s_rstd;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nw = nthr >> 5;
     const int vpr = a.K / 8;
@@ -346,13 +354,13 @@ __global__ void __launch_bounds__(T, norm_ctas(T, C, FMT))
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int c = tid + i * nthr;
-        v[i] = c < vpr ? ld_stream_v4(a.x + m * a.ldx + c * 8) : zero;
-        r[i] = c < vpr && a.residual != nullptr ? ld_stream_v4(a.residual + m * a.ldr + c * 8) : zero;
+        v[i] = ld_row_v4(a.x + m * a.ldx + c * 8, c < vpr);
+        r[i] = ld_row_v4(a.residual + m * a.ldr + c * 8, c < vpr && a.residual != nullptr);
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int c = tid + i * nthr;
-        g[i] = c < vpr ? ld_ro_v4(a.g + c * 8) : zero;
+        g[i] = c < vpr ? ld_v4(a.g + c * 8) : zero;
     }
     Pair hi = 0ull, lo = 0ull;  // sums of the even and of the odd elements' squares, and their rounding errors
 #pragma unroll
@@ -403,17 +411,17 @@ __global__ void __launch_bounds__(T, norm_ctas(T, C, FMT))
     // (a row whose sum does not fit is written by norm_again alone)
     const bool fits = rstd >= 0.0f;
     if (FMT != 0 || a.xn != nullptr) norm_write<C, FMT>(a, m, tid, nthr, fits ? vpr : 0, v, g, rstd);
-    if (!fits) norm_again<FMT>(same, rstd == -1.0f, s_hi, s_lo);
+    if (!fits) norm_again<FMT>(a, rstd == -1.0f, s_hi, s_lo);
 }
 
 template <int C, int T>
 cudaError_t launch_norm_c(const NormArgs& a, cudaStream_t st) {
-    void (*kernel)(const NormArgs, const NormArgs) = a.fmt == 0   ? add_norm_kernel<C, 0, T>
+    void (*kernel)(const NormArgs) = a.fmt == 0   ? add_norm_kernel<C, 0, T>
                                                      : a.fmt == 1 ? add_norm_kernel<C, 1, T>
                                                      : a.fmt == 2 ? add_norm_kernel<C, 2, T>
                                                                   : add_norm_kernel<C, 3, T>;
     const int threads = ((a.K / 8 + C - 1) / C + 31) / 32 * 32;
-    return launch_overlapped(kernel, dim3((unsigned)a.M), dim3((unsigned)threads), 0, st, a, a);
+    return launch_overlapped(kernel, dim3((unsigned)a.M), dim3((unsigned)threads), 0, st, a);
 }
 
 cudaError_t launch_add_norm(const NormArgs& a, cudaStream_t st) {

@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExperts
     int f = -1;
     bool row = false;
     if (p < a.cap) {
-        f = __ldg(a.sorted + p);
-        row = p < __ldg(a.npost);
+        f = a.sorted[p];
+        row = p < *a.npost;
     }
     {
         // assignments that the sort left out
@@ -202,20 +202,20 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_kernel(const ToExperts
                 V v[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (c + u * lanes < c1) v[u] = __ldg(x + c + u * lanes);
+                    if (c + u * lanes < c1) v[u] = x[c + u * lanes];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (c + u * lanes < c1) __stcs(out + c + u * lanes, v[u]);
             }
         } else {
             using E = Elems<TYPE, BYTES>;
-            const float w = a.weights == nullptr ? 1.0f : __ldg(a.weights + f);
+            const float w = a.weights == nullptr ? 1.0f : a.weights[f];
             const V* y = reinterpret_cast<const V*>(static_cast<const uint8_t*>(a.y) + p * a.ldy);
             for (int c = lane; c < vecs; c += lanes * U) {
                 V gv[U], yv[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (c + u * lanes < vecs) gv[u] = __ldg(x + c + u * lanes), yv[u] = __ldcs(y + c + u * lanes);
+                    if (c + u * lanes < vecs) gv[u] = x[c + u * lanes], yv[u] = __ldcs(y + c + u * lanes);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (c + u * lanes >= vecs) continue;
@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(kRowThreads) to_experts_shift_kernel(const ToE
     const int64_t p = ((int64_t)blockIdx.x << (__ffs(kRowThreads) - 1 - shift)) + (tid >> shift);
     const int64_t i0 = (int64_t)blockIdx.x * kRowThreads + tid;
     if (blockIdx.y == 0 && i0 < mk && (unsigned)a.ids[i0] >= (unsigned)a.E) a.positions[i0] = -1;
-    if (p >= a.cap || p >= __ldg(a.npost)) return;
-    const int f = __ldg(a.sorted + p);
+    if (p >= a.cap || p >= *a.npost) return;
+    const int f = a.sorted[p];
     // the row that is written, its words counted from the 16 bytes that hold its first byte on
     uint8_t* out = static_cast<uint8_t*>(a.out) + p * a.row_bytes;
     const int off = (int)(reinterpret_cast<uintptr_t>(out) & 15u);
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_shift_kernel(const T
     int f = -1;
     bool row = false;
     if (p < a.cap) {
-        f = __ldg(a.sorted + p);
-        row = p < __ldg(a.npost);
+        f = a.sorted[p];
+        row = p < *a.npost;
     }
     const bool real = row && (unsigned)f < (unsigned)mk;
     // the row that is written, its words counted from the 16 bytes that hold its first byte on
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_shift_kernel(const T
         const uint8_t *x = static_cast<const uint8_t*>(a.x), *y = static_cast<const uint8_t*>(a.y);
         const Source xs = source(x + (int64_t)((unsigned)f / (unsigned)a.topk) * a.ldx, off, x, x + a.x_bytes);
         const Source ys = source(y + p * a.ldy, off, y, y + a.y_bytes);
-        const float w = a.weights == nullptr ? 1.0f : __ldg(a.weights + f);
+        const float w = a.weights == nullptr ? 1.0f : a.weights[f];
         for (int c = lane; c < words; c += lanes * U) {
             Words gv[U], yv[U];
 #pragma unroll
@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokens
             bool in[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                p[u] = j0 + u < a.topk ? __ldg(pos + j0 + u) : -1;
-                w[u] = a.weights != nullptr && j0 + u < a.topk ? __ldg(wts + j0 + u) : 1.0f;
+                p[u] = j0 + u < a.topk ? pos[j0 + u] : -1;
+                w[u] = a.weights != nullptr && j0 + u < a.topk ? wts[j0 + u] : 1.0f;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) in[u] = (uint64_t)(int64_t)p[u] < (uint64_t)a.cap;
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kTokenThreads) to_tokens_many_kernel(const ToT
         q.m = mb * per + (tid >> shift);
         q.c0 = (int)(b - mb * blocks) * lanes * VECS + lane;
         if (q.m < a.M && slot < a.topk) {
-            q.p = __ldg(a.positions + q.m * a.topk + slot);
-            if (a.weights != nullptr) q.w = __ldg(a.weights + q.m * a.topk + slot);
+            q.p = a.positions[q.m * a.topk + slot];
+            if (a.weights != nullptr) q.w = a.weights[q.m * a.topk + slot];
         }
         return q;
     };

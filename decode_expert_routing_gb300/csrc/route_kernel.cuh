@@ -101,7 +101,7 @@ __device__ __forceinline__ void load_w_batch(const RouteArgs& a, const uint16_t*
         const uint16_t* wp = wg + (int64_t)(j * 8 + g) * a.K + kslice + (int64_t)p * a.spw * 32 + 8 * t;
 #pragma unroll
         for (int s = 0; s < kRouteSpwMax; ++s)
-            wv[uu][s] = (ok && s < a.spw) ? ld_stream_v4(wp + s * 32) : make_uint4(0u, 0u, 0u, 0u);
+            wv[uu][s] = (ok && s < a.spw) ? ld_weight_v4(wp + s * 32) : make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -357,8 +357,8 @@ static __device__ __noinline__ void shared_gate_up_cta(const RouteArgs& a, int s
     bool exact = true;
     for (int v = tid; v < Mq * vpr; v += kRouteThreads) {
         const int r = v / vpr, cv = v - r * vpr;
-        uint4 d = ld_ro_v4(xg + (int64_t)r * ldx + kslice + cv * 8);
-        if (rstd != nullptr) d = norm_chunk(d, ld_ro_v4(norm_w + kslice + cv * 8), __ldg(rstd + r), gemma);
+        uint4 d = ld_v4(xg + (int64_t)r * ldx + kslice + cv * 8);
+        if (rstd != nullptr) d = norm_chunk(d, ld_v4(norm_w + kslice + cv * 8), rstd[r], gemma);
         d = make_uint4(bf16x2_to_f16x2(d.x, &exact), bf16x2_to_f16x2(d.y, &exact), bf16x2_to_f16x2(d.z, &exact),
                        bf16x2_to_f16x2(d.w, &exact));
         *reinterpret_cast<uint4*>(xs + r * xpitch + cv * 16) = d;
@@ -385,8 +385,8 @@ static __device__ __noinline__ void shared_gate_up_cta(const RouteArgs& a, int s
     if (!use_f16) {
         for (int v = tid; v < Mq * vpr; v += kRouteThreads) {
             const int r = v / vpr, cv = v - r * vpr;
-            uint4 d = ld_ro_v4(xg + (int64_t)r * ldx + kslice + cv * 8);
-            if (rstd != nullptr) d = norm_chunk(d, ld_ro_v4(norm_w + kslice + cv * 8), __ldg(rstd + r), gemma);
+            uint4 d = ld_v4(xg + (int64_t)r * ldx + kslice + cv * 8);
+            if (rstd != nullptr) d = norm_chunk(d, ld_v4(norm_w + kslice + cv * 8), rstd[r], gemma);
             *reinterpret_cast<uint4*>(xs + r * xpitch + cv * 16) = d;
         }
         __syncthreads();
@@ -558,20 +558,19 @@ __global__ void __launch_bounds__(kRouteThreads, 1) route_cluster_kernel(RouteAr
     const uint16_t* wg = a.w + (int64_t)e_off * K;  // this cluster's expert rows
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(sm + a.off_mask);
 
-    // ---- loads of the gate weight (first batch) and of the selection bias:
-    //      parameters, never written by the preceding kernel, so they may
-    //      precede the wait
+    // ---- loads of the gate weight (first batch), which the preceding kernel
+    //      does not write, so they may precede the wait
     uint4 wv[kRouteBatch][kRouteSpwMax];
     const int vpr = a.kc / 8;  // 16-byte chunks per row of the CTA's K slice
     load_w_batch(a, wg, kslice, warp, g, t, 0, wv);
-    float bpre0 = 0.0f, bpre1 = 0.0f;  // selection bias of this thread's experts t and t + 512
-    if (a.bias != nullptr) {
-        if (tid < N) bpre0 = __ldg(a.bias + e_off + tid);
-        if (tid + kRouteThreads < N) bpre1 = __ldg(a.bias + e_off + tid + kRouteThreads);
-    }
     if (sorts)
         for (int e = tid; e < N; e += kRouteThreads) mask[e] = 0ull;  // token bitmasks (2 x 32 bits per expert)
     pdl_wait();
+    float bpre0 = 0.0f, bpre1 = 0.0f;  // selection bias of this thread's experts t and t + 512
+    if (a.bias != nullptr) {
+        if (tid < N) bpre0 = a.bias[e_off + tid];
+        if (tid + kRouteThreads < N) bpre1 = a.bias[e_off + tid + kRouteThreads];
+    }
     MR_TRACE_STAMP(a.trace, 8);
 
     // ---- this CTA's x slice -> shared memory (on the norm's scale: the
@@ -582,8 +581,8 @@ __global__ void __launch_bounds__(kRouteThreads, 1) route_cluster_kernel(RouteAr
     if (norm) {
         for (int v = tid; v < Mq * vpr; v += kRouteThreads) {
             const int r = fdiv(v, a.mag_vpr), cv = v - r * vpr;
-            uint4 d = ld_ro_v4(xq + (int64_t)r * a.ldx + kslice + cv * 8);
-            d = norm_chunk(d, ld_ro_v4(a.norm_w + kslice + cv * 8), __ldg(a.rstd + row0 + r), a.norm_gemma != 0);
+            uint4 d = ld_v4(xq + (int64_t)r * a.ldx + kslice + cv * 8);
+            d = norm_chunk(d, ld_v4(a.norm_w + kslice + cv * 8), a.rstd[row0 + r], a.norm_gemma != 0);
             *reinterpret_cast<uint4*>(xs + r * a.xpitch + cv * 16) = d;
         }
     } else {  // straight to shared memory: every chunk in flight at once, no register round trip
@@ -846,7 +845,7 @@ __global__ void __launch_bounds__(kRouteThreads, 1) route_cluster_kernel(RouteAr
         if constexpr (SIG) {  // the candidates' exact scores and keys (correctly rounded sigmoid + bias)
             for (int i = tid; i < C; i += kRouteThreads) {
                 const int id = 0x7FFFFFFF - (int)(unsigned)(ccand[i] & 0xFFFFFFFFull);
-                const float b = a.bias != nullptr ? __ldg(a.bias + id) : 0.0f;
+                const float b = a.bias != nullptr ? a.bias[id] : 0.0f;
                 const float sc = sigmoid_exact(rowbuf[rl * N + id - e_off], (a.flags & 8) != 0);
                 cscore[i] = sc;
                 ccand[i] = composite(ordered_key(__fadd_rn(sc, b)), id);

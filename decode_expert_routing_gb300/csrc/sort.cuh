@@ -166,7 +166,7 @@ __device__ __forceinline__ const int* stage_ids(const int32_t* ids, int n, int* 
 #pragma unroll
         for (int u = 0; u < kLoadBatch; ++u) {
             const int i = base + u * nthr;
-            v[u] = i < n ? __ldg(ids + i) : 0;
+            v[u] = i < n ? ids[i] : 0;
         }
 #pragma unroll
         for (int u = 0; u < kLoadBatch; ++u) {

@@ -94,7 +94,7 @@ __device__ __forceinline__ void warp_topk_row(const TopkArgs& a, int m, int* ids
         unsigned kv = 0u;  // below every real key: never selected while real keys remain
         if (id < a.N) {
             float sel = val[j];
-            if constexpr (SIG) sel = __fadd_rn(sigmoid_approx(val[j]), a.bias ? __ldg(a.bias + id) : 0.0f);
+            if constexpr (SIG) sel = __fadd_rn(sigmoid_approx(val[j]), a.bias ? a.bias[id] : 0.0f);
             kv = ordered_key(sel);
         }
         key[j] = kv;
@@ -114,7 +114,7 @@ __device__ __forceinline__ void warp_topk_row(const TopkArgs& a, int m, int* ids
             const int id = lane + 32 * j;
             const bool cand = id < a.N && key[j] >= floor_key;
             score[j] = cand ? sigmoid_exact_call(val[j], a.slow_sigmoid != 0) : 0.0f;
-            key[j] = cand ? ordered_key(__fadd_rn(score[j], a.bias ? __ldg(a.bias + id) : 0.0f)) : 0u;
+            key[j] = cand ? ordered_key(__fadd_rn(score[j], a.bias ? a.bias[id] : 0.0f)) : 0u;
         }
         warp_select<NPL>(key, score, a.k, &my_id, &my_val);
     } else {

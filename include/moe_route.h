@@ -102,10 +102,11 @@ typedef enum mr_quant_format {
  * MR_ERR_INVALID_ARG for unknown bits.  With MR_LAUNCH_PDL each kernel is
  * launched with programmatic stream serialization: it may start while the
  * kernel before it on the stream is still running, issues its loads of the
- * gate weight w at once, and waits for that kernel to complete before it
- * touches anything else (x, logits, ids, scratch, outputs).  The caller must
- * then not write w in the kernel launched just before the routing call on
- * the same stream (where that one is a call of this library: nor in the one
+ * gate weight w (and of the shared expert's w13 and w13_scale) at once, and
+ * waits for that kernel to complete before it touches anything else (x,
+ * logits, ids, sel_bias, scratch, outputs).  The caller must then not write
+ * these weights in the kernel launched just before the routing call on the
+ * same stream (where that one is a call of this library: nor in the one
  * before it).  The expert products and the calls behind them in this file
  * (mr_add_rms_norm to mr_moe_combine_grad) are always launched so, whatever
  * the flags; they use nothing before that wait (mr_fp8_gemm asks for the first
