@@ -426,10 +426,11 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     #pragma unroll
                             for (int i = 0; i < 2; ++i)
                                 s_scale[buf * D + b][j][row + 32 * i] = __fmul_rn(x[i][b], w[j][b]);
+                    // (asked for before the arrival: nothing crosses it; after it 4096 x 6144 x 6144 took 1.5 % more)
+                    if (ki + D < k1) fetch(ki + D);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(tfull0 + 8u * buf);
                     if (++buf == a.nbuf) buf = 0, bph ^= 1u;
-                    if (ki + D < k1) fetch(ki + D);
                 }
             }
         }

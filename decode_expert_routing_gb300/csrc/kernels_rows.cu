@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokens
         float s[E::N];
 #pragma unroll
         for (int q = 0; q < E::N; ++q) s[q] = 0.0f;
+        uint4 start = make_uint4(0u, 0u, 0u, 0u);  // of aligned rows what the sum starts from, waited for with the slots' rows
         if (a.add != nullptr) {
             // (plain loads: out may be add itself)
             const uint8_t *add0 = static_cast<const uint8_t*>(a.add), *add = add0 + m * a.ldadd;
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokens
                 const Source from = source(add, off, add0, add0 + a.add_bytes);
                 E::get(shifted(load_words<2>(from, c, off, a.row_bytes)), s);
             } else {
-                E::get(*reinterpret_cast<const uint4*>(add + at), s);
+                start = *reinterpret_cast<const uint4*>(add + at);
             }
         }
         const int32_t* pos = a.positions + m * a.topk;
@@ -425,6 +426,7 @@ __global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokens
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (in[u]) v[u] = __ldcs(reinterpret_cast<const uint4*>(y0 + (int64_t)p[u] * a.ldy + at));
+                if (j0 == 0) E::get(start, s);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (in[u]) add(u, v[u]);
