@@ -19,13 +19,15 @@
 // blocks (one wait for all of them), products up to 64 rows are of 64, and
 // where tiles are still fewer than SMs a cluster shares their K range.
 //
-// What bounds it: of 4096 x 6144 x 6144 (112 us, 2770 TFLOP/s, 1.4 of the bf16
-// rate measured here) a pair's block of K of 224 columns takes 780 cycles: 448
-// for the products, 600 for its bytes' way from L2, 224 to read tensor memory,
-// as many to add; the read-back's waits at both ends of a buffer join them.  The
-// results' way out is 3 us of it.  Below 128 rows it is the weight: 40 x 6144 x
-// 6144 10.0 us (3.8 TB/s), 40 x 1536 x 6144 6.8 us, most of it start, first bytes
-// and the sums' way through the cluster.
+// What bounds it: of 4096 x 6144 x 6144 (117 us captured, 2640 TFLOP/s, 1.4 of the
+// bf16 rate measured here; called over and over the power cap makes it 130) a
+// pair's block of K of 224 columns takes some 800 cycles: 448 for the products,
+// 540 for its bytes' way from L2 (57 a cycle), 224 to read tensor memory, as many
+// to add; the read-back's waits at both ends of a buffer join them.  The results'
+// way out is 3 us of it.  Of few rows it is the blocks' read-back too, 305 cycles
+// for one of 48 columns whatever the rows: 40 x 6144 x 6144 10.0 us (3.8 TB/s), 48
+// blocks one behind another 7.1 of them; 40 x 1536 x 6144 6.7 us, 12 blocks 1.8,
+// the sums' way through the cluster 2.0, start and first bytes 3.
 #include "../../include/moe_route.h"
 #include "fp8_plan.h"
 #include "internal.h"
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                     }
                     const uint32_t full = full0 + 8u * st, at = base + (uint32_t)st * stage_bytes;
                     ex_expect(lead, full, stage_bytes + (((a.flags & 2) && issued == 0) ? 16u : 0u));
-    #pragma unroll
+#pragma unroll
                     for (int b = 0; b < D; ++b) {
                         ex_load_2d(lead, at + b * block_bytes, &a.tm_w, (ki + b) * 128, w0, full);
                         ex_load_2d(lead, at + b * block_bytes + wbytes, &a.tm_x, (ki + b) * 128, m0, full);
@@ -375,11 +377,11 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                     }
                     tc_fence_after();
                     const uint32_t at = base + (uint32_t)st * stage_bytes, d = tmem + (uint32_t)(buf * D * a.n);
-    #pragma unroll
+#pragma unroll
                     for (int b = 0; b < D; ++b) {
                         const unsigned long long dw = ex_desc(kExDescCodes, at + b * block_bytes);
                         const unsigned long long dx = ex_desc(kExDescCodes, at + b * block_bytes + wbytes);
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < 4; ++j)
                             f8_mma<PAIR>(lead, d + (uint32_t)(b * a.n), dx + 2 * j, dw + 2 * j, idesc, j > 0);
                     }
@@ -400,16 +402,16 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 const int64_t end = (int64_t)a.M - 1;
                 const float* xs[2] = {a.xs + min(m, end) * a.ldxs, a.xs + min(m + 32, end) * a.ldxs};
                 const float* ws[3];
-    #pragma unroll
+#pragma unroll
                 for (int j = 0; j < 3; ++j) ws[j] = a.ws + (int64_t)min(bt + j, last) * a.ldws;
                 float x[2][D], w[3][D];
                 auto fetch = [&](int ki) {
-    #pragma unroll
+#pragma unroll
                     for (int b = 0; b < D; ++b) {
                         const bool in = D == 1 || ki + b < a.KI;  // (behind K: no scale either)
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 2; ++i) x[i][b] = in ? xs[i][ki + b] : 0.0f;
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < 3; ++j) w[j][b] = in ? ws[j][ki + b] : 0.0f;
                     }
                 };
@@ -419,11 +421,11 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         ok = false;
                         break;
                     }
-    #pragma unroll
+#pragma unroll
                     for (int b = 0; b < D; ++b)
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < 3; ++j)
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 2; ++i)
                                 s_scale[buf * D + b][j][row + 32 * i] = __fmul_rn(x[i][b], w[j][b]);
                     // (asked for before the arrival: nothing crosses it; after it 4096 x 6144 x 6144 took 1.5 % more)

@@ -64,7 +64,9 @@ __device__ __forceinline__ void fp8_scales(const float (&amax)[C], float (&scale
 }
 
 // One warp per 128 chunks of 8 elements (8 groups) of a row, four loads in
-// flight per lane: bytes bound it.
+// flight per lane.  Of many rows bytes bound it: 4096 x 6144 14.8 us, 5.2 TB/s, 77 %
+// of a plain copy's rate, x 16384 34.4 (5.9 TB/s, 88 %); of few the launch: 1 row
+// 1.6 us, 48 1.8, 1000 5.5.
 constexpr int kFp8Threads = 256, kFp8Unroll = 4;
 __global__ void __launch_bounds__(kFp8Threads) fp8_quant_kernel(const uint16_t* x, int64_t ldx, int M, int K,
                                                                 uint8_t* q, float* scale) {

@@ -1,8 +1,9 @@
 // Rows between the tokens and the sorted positions of their assignments, with
 // the weights applied on the way back, and the gradients of both.  Bytes bound
 // all of them (a plain copy moves 6.7 TB/s): 4096 tokens x 8 x 6144 bf16 to the
-// experts 77 us (6.5 TB/s), back 73 (6.2); the gradients of the way back of 2048
-// tokens 75 (6.4), of the way there of 1001 19.4 (5.7).
+// experts 77 us (6.5 TB/s), back 72 (6.3); the gradients of the way back of 2048
+// tokens 74 (6.4), of the way there of 1001 19.9 (5.6).  (Bytes that a call reads
+// and writes; up to 60 MB of what it writes are still in L2 when it ends.)
 //
 //   mr_moe_permute        rows[p] = x[f / topk]                  f = sorted[p]
 //   mr_moe_permute_grad   gx[m]   = sum_j grows[pos[m, j]]
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_shift_kernel(const T
 // eight slots (SHIFT: rows that start anywhere; four) are under way together.
 // The sum goes over the slots in ascending order in fp32, from add (or zero), and
 // is rounded once.  2048 x 4 rows of 6143: 43 us, element by element 81, of 6140
-// 41 and by 8-byte words 46.
+// 42 and by 8-byte words 46.
 constexpr int kTokenThreads = 128;
 template <int TYPE, bool SHIFT>
 __global__ void __launch_bounds__(kTokenThreads) to_tokens_kernel(const ToTokensArgs a, int lanes, int shift,

@@ -6,7 +6,10 @@
 
 namespace mr {
 
-constexpr int kNormMaxK = 65536;  // 1024 threads x 8 chunks of 8 elements
+// 1024 threads x 8 chunks of 8 elements.  Beyond 32768 a thread's chunks do not fit
+// its 64 registers, and some 450 bytes of them are spilled: 1024 x 32768 with FP8
+// codes 53 us (4.5 TB/s), x 65536 150 (3.1 TB/s).
+constexpr int kNormMaxK = 65536;
 
 struct NormArgs {
     const uint16_t *x, *residual, *g;

@@ -709,12 +709,13 @@ int mr_fp8_quant(const void *x, int64_t ldx, int M, int K, uint8_t *q, float *sc
  *   out[m, r] = sum_b x_scale[m, b] w_scale[r / 128, b] sum_{k in b} q[m, k] w[r, k]
  * over the blocks b of 128 along K (the last of each kind may be shorter).
  * The inner sums are those of the tensor core in fp32.  The product of the two
- * scales is rounded to fp32 first, and one fused multiply-add a block adds the
- * scaled sums in fp32 in ascending b, or, where K is shared out, ascending
- * within each share and then over the shares: of up to 16 rows eight shares of
- * every eighth block, else up to eight ranges.  Sizes alone decide which, so a
- * call repeated gives the same bits; the same row in a batch of another size
- * may differ by the order of these sums.
+ * scales is rounded to fp32 first (below 2^-126 it has fewer bits, from 2^128 on
+ * it is infinite, and NaN where it meets a sum of zero), and one fused
+ * multiply-add a block adds the scaled sums in fp32 in ascending b, or, where K
+ * is shared out, ascending within each share and then over the shares: of up to
+ * 16 rows eight shares of every eighth block, else up to eight ranges.  Sizes
+ * alone decide which, so a call repeated gives the same bits; the same row in a
+ * batch of another size may differ by the order of these sums.
  * q: [M, K] with row stride ldq in bytes; w: [R, K] with row stride ldw in
  * bytes; both 16-byte aligned and their strides multiples of 16.  x_scale:
  * fp32 [M, ceil(K / 128)] with row stride ldxs; w_scale: fp32 [ceil(R / 128),
