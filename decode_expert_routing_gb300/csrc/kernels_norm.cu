@@ -259,7 +259,7 @@ __device__ __forceinline__ void norm_write(const NormArgs& a, int64_t m, int c0,
 // A row whose sum does not fit, taken again by its whole CTA; small: its sum is
 // below 2^-60.  The values of a small one are taken times 2^90, so that every
 // square is above 2^-86 and the sum below 2^120; the squares of a large one times
-// 2^-32.  Both are exact, but for squares that are below 2^-117 of a large sum.  A
+// 2^-32.  Both are exact, but for squares below 2^-94 beside a sum above 2^127.  A
 // square beyond fp32, of values from 2^64 on, stays infinite and makes rstd 0; a
 // NaN stays one.
 // It is a call behind all else and reads the row again: in the kernel's body, from
@@ -419,9 +419,9 @@ __global__ void __launch_bounds__(T, norm_ctas(T, C, FMT)) add_norm_kernel(const
 template <int C, int T>
 cudaError_t launch_norm_c(const NormArgs& a, cudaStream_t st) {
     void (*kernel)(const NormArgs) = a.fmt == 0   ? add_norm_kernel<C, 0, T>
-                                                     : a.fmt == 1 ? add_norm_kernel<C, 1, T>
-                                                     : a.fmt == 2 ? add_norm_kernel<C, 2, T>
-                                                                  : add_norm_kernel<C, 3, T>;
+                                     : a.fmt == 1 ? add_norm_kernel<C, 1, T>
+                                     : a.fmt == 2 ? add_norm_kernel<C, 2, T>
+                                                  : add_norm_kernel<C, 3, T>;
     const int threads = ((a.K / 8 + C - 1) / C + 31) / 32 * 32;
     return launch_overlapped(kernel, dim3((unsigned)a.M), dim3((unsigned)threads), 0, st, a);
 }
